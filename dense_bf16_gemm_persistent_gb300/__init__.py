@@ -8,6 +8,9 @@ fallback of any kind, and every call raises if the library is missing.
     ffn_gated(X, W1, W3)                         ->  bf16(silu(X @ W1.T) * (X @ W3.T))
     linear_dact(dY, W, Z, act="none")            ->  bf16((dY @ W) * act'(Z))
 
+and, from block.py, the operators around them: linear_w4, ffn_gated_w4 (4-bit weights, a few
+tokens), add_rms_norm (and its 8-bit and backward forms), dropout.
+
 Tensors are torch CUDA bf16 tensors, 2-D with a contiguous last dimension
 (bias: contiguous 1-D).  Work is enqueued on ``torch.cuda.current_stream()``
 unless a stream is given.
@@ -80,6 +83,17 @@ def lib() -> ctypes.CDLL:
         L.gb_probe_mma_issue.argtypes = [ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                          ctypes.c_int, ctypes.POINTER(ctypes.c_double),
                                          ctypes.POINTER(ctypes.c_double)]
+        i, u64, f64 = ctypes.c_int, ctypes.c_uint64, ctypes.c_double
+        L.gb_gemm_linear_w4.argtypes = [p, i64, i, p, i64, p, i64, p, i64, p, i64, i, p, p, i64, i, p, i64, i64, i64,
+                                        i64, p]
+        L.gb_gemm_ffn_gated_w4.argtypes = [p, i64, i, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, p, i64, i, p,
+                                           i64, i64, i64, i64, p]
+        L.gb_dropout.argtypes = [p, i64, p, i64, f64, u64, u64, p, p, i64, i64, i64, p]
+        L.gb_add_rms_norm.argtypes = [p, i64, p, i64, p, f64, f64, u64, u64, p, p, i64, p, i64, p, i64, i64, p]
+        L.gb_add_rms_norm_q8.argtypes = [p, i64, p, i64, p, f64, i, p, i64, p, i64, p, i64, i64, i64, p]
+        L.gb_add_rms_norm_backward.argtypes = [p, i64, p, i64, p, p, p, i64, f64, u64, u64, p, p, i64, p, i64, p, p,
+                                               ctypes.c_size_t, i64, i64, p]
+        L.gb_add_rms_norm_backward_workspace_bytes.argtypes = [i64, i64, ctypes.POINTER(ctypes.c_size_t)]
         L.gb_version.argtypes = []
         L.gb_version.restype = ctypes.c_char_p
         for name in ("gb_gemm_linear", "gb_gemm_ffn_gated", "gb_gemm_linear_preact", "gb_gemm_linear_dact",
@@ -89,7 +103,9 @@ def lib() -> ctypes.CDLL:
                      "gb_splitk_workspace_bytes", "gb_gemm_linear_splitk_noalloc", "gb_static_scratch_bytes",
                      "gb_get_device_status", "gb_set_config",
                      "gb_set_wait_timeout_ns", "gb_set_fault_injection", "gb_last_plan", "gb_set_trace_buffer",
-                     "gb_measure_mma_rate", "gb_probe_mma_issue"):
+                     "gb_measure_mma_rate", "gb_probe_mma_issue", "gb_gemm_linear_w4", "gb_gemm_ffn_gated_w4",
+                     "gb_dropout", "gb_add_rms_norm", "gb_add_rms_norm_q8", "gb_add_rms_norm_backward",
+                     "gb_add_rms_norm_backward_workspace_bytes"):
             getattr(L, name).restype = st
         _lib = L
         return L
@@ -309,3 +325,7 @@ def last_plan() -> str:
 
 def version() -> str:
     return lib().gb_version().decode()
+
+
+from .block import (add_rms_norm, add_rms_norm_backward, add_rms_norm_backward_workspace_bytes,  # noqa: E402
+                    add_rms_norm_q8, dropout, ffn_gated_w4, linear_w4)

@@ -9,8 +9,8 @@ CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgbgemm.so")
 LOG_DIR = os.path.join(PKG, "_build")
-SOURCES = ["gbgemm.cu"]
-HEADERS = ["gemm_kernel.cuh", "ptx.cuh", "probe.cuh"]
+SOURCES = ["gbgemm.cu", "rowwise.cu", "w4.cu"]
+HEADERS = ["gemm_kernel.cuh", "host.h", "ptx.cuh", "probe.cuh", "rowwise.cuh", "w4_kernel.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-Xptxas", "-v",
               "--diag-suppress", "177"]
@@ -70,18 +70,33 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False) -> st
     if not force and not _stale(out):
         return out
     os.makedirs(LOG_DIR, exist_ok=True)
+    tag = f"{'trace.' if trace else ''}{os.getpid()}"
+    flags = [*NVCC_FLAGS, *(["-DGB_TRACE"] if trace else [])]
+    objs = [os.path.join(LOG_DIR, f"{s}.{tag}.o") for s in SOURCES]
     tmp = out + f".tmp{os.getpid()}"
-    cmd = [_nvcc(), *NVCC_FLAGS, *(["-DGB_TRACE"] if trace else []), "-shared", "-o", tmp,
-           *[os.path.join(CSRC, s) for s in SOURCES]]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    with open(os.path.join(LOG_DIR, "ptxas_trace.log" if trace else "ptxas.log"), "w") as f:
-        f.write(" ".join(cmd) + "\n" + res.stdout + res.stderr)
-    if res.returncode != 0:
-        raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stderr[-4000:]}")
-    _check_register_budgets(res.stdout + res.stderr)
-    if verbose:
-        print(res.stderr)
-    os.replace(tmp, out)
+    try:
+        # one compiler process per source, all at once; their reports in the sources' order
+        cmds = [[_nvcc(), *flags, "-c", os.path.join(CSRC, s), "-o", o] for s, o in zip(SOURCES, objs)]
+        procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
+        logs = [p.communicate()[0] for p in procs]
+        log = "".join(" ".join(c) + "\n" + text for c, text in zip(cmds, logs))
+        failed = [p.returncode for p in procs if p.returncode]
+        if not failed:
+            link = subprocess.run([_nvcc(), *flags, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
+            log += link.stdout + link.stderr
+            failed = [link.returncode] if link.returncode else []
+        with open(os.path.join(LOG_DIR, "ptxas_trace.log" if trace else "ptxas.log"), "w") as f:
+            f.write(log)
+        if failed:
+            raise RuntimeError(f"nvcc failed ({failed[0]}):\n{log[-4000:]}")
+        _check_register_budgets(log)
+        if verbose:
+            print(log)
+        os.replace(tmp, out)
+    finally:
+        for path in (*objs, tmp):
+            if os.path.exists(path):
+                os.remove(path)
     return out
 
 

@@ -16,13 +16,18 @@
 
 #include "../../include/gbgemm.h"
 #include "gemm_kernel.cuh"
+#include "host.h"
 #include "probe.cuh"
 
 namespace {
 
 using gb::GemmParams;
+using gb::host::cuda_fail;
+using gb::host::device_info;
+using gb::host::DeviceInfo;
+using gb::host::fail;
 
-constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;  // TMA coordinates are signed 32-bit
+constexpr int64_t kMaxDim = gb::host::kMaxDim;       // TMA coordinates are signed 32-bit
 constexpr int64_t kMaxLd = (int64_t(1) << 39) - 1;   // TMA strides are below 2^40 bytes
 constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;
 
@@ -44,6 +49,21 @@ struct PlanRec {
 };
 thread_local PlanRec t_plan_rec;
 
+// The plan of a call that is not a matrix product on the persistent kernel: a format of six
+// numbers, formatted like the above only when asked for.
+struct PlanNote {
+    const char* fmt = nullptr;
+    long long v[6] = {};
+};
+thread_local PlanNote t_note;
+
+}  // namespace
+
+namespace gb {
+namespace host {
+
+void clear_error() { t_error.clear(); }
+
 gb_status_t fail(gb_status_t s, const char* fmt, ...) {
     char buf[512];
     va_list ap;
@@ -57,6 +77,49 @@ gb_status_t fail(gb_status_t s, const char* fmt, ...) {
 gb_status_t cuda_fail(cudaError_t e, const char* what) {
     return fail(GB_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
 }
+
+void note_plan(const char* fmt, long long a, long long b, long long c, long long d, long long e, long long f) {
+    t_plan_rec.valid = false;
+    t_note = PlanNote{fmt, {a, b, c, d, e, f}};
+}
+
+// ---------------------------------------------------------------- device properties
+
+static std::mutex g_dev_mu;
+static DeviceInfo g_dev[64];
+
+gb_status_t device_info(int* dev_out, DeviceInfo* info) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+    if (dev < 0 || dev >= 64) return fail(GB_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
+    std::lock_guard<std::mutex> lk(g_dev_mu);
+    DeviceInfo& d = g_dev[dev];
+    if (!d.ready) {
+        int v = 0;
+        if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
+            return cuda_fail(e, "cudaDeviceGetAttribute(SM count)");
+        if ((e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess)
+            return cuda_fail(e, "cudaDeviceGetAttribute(major)");
+        if ((e = cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess)
+            return cuda_fail(e, "cudaDeviceGetAttribute(minor)");
+        if ((e = cudaDeviceGetAttribute(&v, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess)
+            return cuda_fail(e, "cudaDeviceGetAttribute(smem)");
+        d.smem_optin = static_cast<size_t>(v);
+        d.ready = true;
+    }
+    if (d.major != 10 || d.minor != 3)
+        return fail(GB_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a only", dev, d.major,
+                    d.minor);
+    *dev_out = dev;
+    *info = d;
+    return GB_OK;
+}
+
+}  // namespace host
+}  // namespace gb
+
+namespace {
 
 // ---------------------------------------------------------------- configuration override
 
@@ -96,45 +159,6 @@ Config current_config(uint64_t* timeout, int* inject) {
     *timeout = g_timeout_ns;
     *inject = g_inject;
     return g_cfg;
-}
-
-// ---------------------------------------------------------------- device properties
-
-struct DeviceInfo {
-    bool ready = false;
-    int sms = 0;
-    int major = 0, minor = 0;
-    size_t smem_optin = 0;
-};
-std::mutex g_dev_mu;
-DeviceInfo g_dev[64];
-
-gb_status_t device_info(int* dev_out, DeviceInfo* info) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
-    if (dev < 0 || dev >= 64) return fail(GB_ERR_UNSUPPORTED, "device ordinal %d out of range", dev);
-    std::lock_guard<std::mutex> lk(g_dev_mu);
-    DeviceInfo& d = g_dev[dev];
-    if (!d.ready) {
-        int v = 0;
-        if ((e = cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
-            return cuda_fail(e, "cudaDeviceGetAttribute(SM count)");
-        if ((e = cudaDeviceGetAttribute(&d.major, cudaDevAttrComputeCapabilityMajor, dev)) != cudaSuccess)
-            return cuda_fail(e, "cudaDeviceGetAttribute(major)");
-        if ((e = cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, dev)) != cudaSuccess)
-            return cuda_fail(e, "cudaDeviceGetAttribute(minor)");
-        if ((e = cudaDeviceGetAttribute(&v, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess)
-            return cuda_fail(e, "cudaDeviceGetAttribute(smem)");
-        d.smem_optin = static_cast<size_t>(v);
-        d.ready = true;
-    }
-    if (d.major != 10 || d.minor != 3)
-        return fail(GB_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a only", dev, d.major,
-                    d.minor);
-    *dev_out = dev;
-    *info = d;
-    return GB_OK;
 }
 
 // ---------------------------------------------------------------- TMA descriptors
@@ -724,6 +748,7 @@ gb_status_t run(const Problem& pr, void* stream_ptr, const SplitReq& sr = SplitR
     if (pr.m == 0 || pr.n == 0) {
         t_plan = "empty (no launch)";
         t_plan_rec.valid = false;
+        t_note.fmt = nullptr;
         if (sr.query_only) *sr.ws_needed = 0;
         return GB_OK;
     }
@@ -1078,6 +1103,7 @@ gb_status_t gb_gemm_linear_splitk_noalloc(const void* A, int64_t lda, const void
     if (pr.m == 0 || pr.n == 0) {
         t_plan = "empty (no launch)";
         t_plan_rec.valid = false;
+        t_note.fmt = nullptr;
         return GB_OK;
     }
     int dev = 0;
@@ -1186,7 +1212,11 @@ gb_status_t gb_last_plan(char* buf, size_t len) {
     if (len == 0) return GB_OK;
     const PlanRec& r = t_plan_rec;
     if (!r.valid) {
-        snprintf(buf, len, "%s", t_plan.c_str());
+        const PlanNote& n = t_note;
+        if (n.fmt)
+            snprintf(buf, len, n.fmt, n.v[0], n.v[1], n.v[2], n.v[3], n.v[4], n.v[5]);
+        else
+            snprintf(buf, len, "%s", t_plan.c_str());
         return GB_OK;
     }
     snprintf(buf, len,

@@ -1,0 +1,261 @@
+// C ABI of the products with 4-bit weights: argument checks, the plan and the launch of the
+// kernel in w4_kernel.cuh.
+#include <algorithm>
+#include <atomic>
+#include <cinttypes>
+#include <cstring>
+
+#include "host.h"
+#include "w4_kernel.cuh"
+
+namespace {
+
+using namespace gb::host;
+using gb::w4::kRows;
+using gb::w4::kUnit;
+using gb::w4::Params;
+
+struct Weights {
+    const char* name;
+    const void* q;
+    int64_t ldq;
+    const void* s;
+    int64_t lds;
+    const void* z;
+    int64_t ldz;
+};
+
+struct Problem {
+    const void* x;
+    int64_t ldx;
+    int x_type;
+    const float* x_scale;
+    int64_t ldxs;
+    Weights w[2];
+    int group;
+    const void* bias;
+    const void* r;
+    int64_t ldr;
+    int act;
+    void* d;
+    int64_t ldd;
+    int64_t m, n, k;
+    bool gated;
+};
+
+gb_status_t validate(const Problem& pr) {
+    if (pr.m < 0 || pr.n < 0 || pr.k < 0)
+        return fail(GB_ERR_INVALID_ARG, "negative size M=%" PRId64 " N=%" PRId64 " K=%" PRId64, pr.m, pr.n, pr.k);
+    if (pr.m > kMaxDim || pr.n > kMaxDim || pr.k > kMaxDim)
+        return fail(GB_ERR_UNSUPPORTED, "sizes must be below 2^31 (M=%" PRId64 " N=%" PRId64 " K=%" PRId64 ")", pr.m,
+                    pr.n, pr.k);
+    if (pr.act < GB_ACT_NONE || pr.act > GB_ACT_RELU) return fail(GB_ERR_INVALID_ARG, "unknown activation %d", pr.act);
+    if (pr.group != 32 && pr.group != 64 && pr.group != 128)
+        return fail(GB_ERR_INVALID_ARG, "group=%d: 32, 64 or 128 columns", pr.group);
+    if (pr.x_type < GB_X_BF16 || pr.x_type > GB_X_E4M3_GROUP_SCALE)
+        return fail(GB_ERR_INVALID_ARG, "unknown type of X %d", pr.x_type);
+    if (pr.m == 0 || pr.n == 0) return GB_OK;
+    const int64_t groups = ceil_div(pr.k, pr.group);
+    if (!pr.d) return fail(GB_ERR_INVALID_ARG, "D is null");
+    if (pr.ldd < pr.n) return fail(GB_ERR_INVALID_ARG, "ldd=%" PRId64 " < N=%" PRId64, pr.ldd, pr.n);
+    if (pr.r && pr.ldr < pr.n) return fail(GB_ERR_INVALID_ARG, "ldr=%" PRId64 " < N=%" PRId64, pr.ldr, pr.n);
+    if (!aligned_to(pr.d, 2) || !aligned_to(pr.r, 2) || !aligned_to(pr.bias, 2))
+        return fail(GB_ERR_UNSUPPORTED, "D, R and bias must be 2-byte aligned");
+    if (pr.k == 0) return GB_OK;
+    if (pr.k % 32) return fail(GB_ERR_UNSUPPORTED, "K=%" PRId64 " must be a multiple of 32", pr.k);
+    if (!pr.x) return fail(GB_ERR_INVALID_ARG, "X is null");
+    if (pr.ldx < pr.k) return fail(GB_ERR_INVALID_ARG, "ldx=%" PRId64 " < K=%" PRId64, pr.ldx, pr.k);
+    if (pr.x_type == GB_X_BF16 && !aligned_to(pr.x, 2)) return fail(GB_ERR_UNSUPPORTED, "X must be 2-byte aligned");
+    if (pr.x_type != GB_X_BF16) {
+        const int64_t scales = pr.x_type == GB_X_E4M3_GROUP_SCALE ? ceil_div(pr.k, 128) : 1;
+        if (!pr.x_scale) return fail(GB_ERR_INVALID_ARG, "x_scale is null");
+        if (pr.ldxs < scales) return fail(GB_ERR_INVALID_ARG, "ldxs=%" PRId64 " < %" PRId64 " scales a row", pr.ldxs, scales);
+        if (!aligned_to(pr.x_scale, 4)) return fail(GB_ERR_UNSUPPORTED, "x_scale must be 4-byte aligned");
+    }
+    for (int i = 0; i < (pr.gated ? 2 : 1); ++i) {
+        const Weights& w = pr.w[i];
+        if (!w.q || !w.s) return fail(GB_ERR_INVALID_ARG, "%s%s is null", w.name, w.q ? "'s scales" : "");
+        if (w.ldq < pr.k / 2)
+            return fail(GB_ERR_INVALID_ARG, "leading dimension %" PRId64 " of %s is below its %" PRId64 " bytes a row", w.ldq,
+                        w.name, pr.k / 2);
+        if (w.lds < groups || (w.z && w.ldz < groups))
+            return fail(GB_ERR_INVALID_ARG, "leading dimension of %s's scales or zeros is below its %" PRId64 " groups",
+                        w.name, groups);
+        if (!aligned_to(w.q, 16) || w.ldq % 16)
+            return fail(GB_ERR_UNSUPPORTED, "%s: base address and leading dimension must be multiples of 16 bytes", w.name);
+        if (!aligned_to(w.s, 2)) return fail(GB_ERR_UNSUPPORTED, "%s's scales must be 2-byte aligned", w.name);
+    }
+    return GB_OK;
+}
+
+struct Plan {
+    int tokens;     // of a pass
+    int cluster;    // CTAs that share a row tile's columns
+    int k_warps;    // warps of a CTA that share them
+    int warps;
+    int slice_units;
+    size_t smem;
+};
+
+template <int G, int NT, bool GATED, bool X8>
+gb_status_t launch(const Params& prm, const Plan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
+    static std::atomic<bool> ready[64];  // (two threads may both set the attribute: to the same value)
+    auto kern = gb::w4::w4_kernel<G, NT, GATED, X8>;
+    cudaError_t e;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(info.smem_optin));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        ready[dev].store(true, std::memory_order_release);
+    }
+    const int64_t groups = ceil_div(prm.tiles, pl.warps / pl.k_warps);
+    const int64_t clusters = std::min<int64_t>(groups, std::max(1, 2 * info.sms / pl.cluster));
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * pl.cluster), static_cast<unsigned>(ceil_div(prm.m, pl.tokens)), 1);
+    cfg.blockDim = dim3(32 * pl.warps, 1, 1);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = pl.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, prm);
+    if (e != cudaSuccess) return cuda_fail(e, "w4 kernel launch");
+    note_plan("kernel=w4 group=%lld tokens=%lld cluster=%lld warps=%lld k_warps=%lld clusters=%lld", G, pl.tokens, pl.cluster,
+              pl.warps, pl.k_warps, clusters);
+    return GB_OK;
+}
+
+template <int G, int NT, bool GATED>
+gb_status_t launch_x(const Params& prm, const Plan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
+    return prm.x_type == GB_X_BF16 ? launch<G, NT, GATED, false>(prm, pl, dev, info, stream)
+                                   : launch<G, NT, GATED, true>(prm, pl, dev, info, stream);
+}
+
+template <int G, bool GATED>
+gb_status_t launch_nt(const Params& prm, const Plan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
+    if (pl.tokens <= 8) return launch_x<G, 1, GATED>(prm, pl, dev, info, stream);
+    if (pl.tokens <= 16) return launch_x<G, 2, GATED>(prm, pl, dev, info, stream);
+    return launch_x<G, 4, GATED>(prm, pl, dev, info, stream);
+}
+
+template <bool GATED>
+gb_status_t launch_g(const Params& prm, const Plan& pl, int group, int dev, const DeviceInfo& info, cudaStream_t stream) {
+    if (group == 32) return launch_nt<32, GATED>(prm, pl, dev, info, stream);
+    if (group == 64) return launch_nt<64, GATED>(prm, pl, dev, info, stream);
+    return launch_nt<128, GATED>(prm, pl, dev, info, stream);
+}
+
+size_t smem_of(int slice_units, int tokens, int warps, bool x8) {
+    const size_t nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
+    return static_cast<size_t>(slice_units) * 4 * tokens * (256 + (x8 ? 4 : 0)) + 2 * warps * nt * 8 * kRows * 4;
+}
+
+gb_status_t run(const Problem& pr, void* stream) {
+    gb_status_t st = validate(pr);
+    if (st != GB_OK || pr.m == 0 || pr.n == 0) return st;
+    int dev = 0;
+    DeviceInfo info;
+    if ((st = device_info(&dev, &info)) != GB_OK) return st;
+
+    const int out_rows = pr.gated ? 8 : kRows;
+    const int64_t tiles = ceil_div(pr.n, out_rows);
+    const int units = static_cast<int>(ceil_div(pr.k, kUnit));
+    const bool x8 = pr.x_type != GB_X_BF16;
+    Plan pl{};
+    pl.tokens = static_cast<int>(std::min<int64_t>(pr.m, 32));
+    pl.warps = gb::w4::kMaxWarps;
+    pl.cluster = 1;
+    auto slice = [&](int c) { return std::max(1, static_cast<int>(ceil_div(units, c))); };
+    // Split the columns over a cluster while x's slice does not fit, or while there are too few
+    // row tiles to give every SM a CTA and each warp keeps a unit of its own.
+    while (pl.cluster < 8 && (smem_of(slice(pl.cluster), pl.tokens, pl.warps, x8) > info.smem_optin / 2 - 1024 ||
+                              (tiles * pl.cluster < info.sms && slice(pl.cluster) > pl.warps)))
+        pl.cluster *= 2;
+    while (smem_of(slice(pl.cluster), pl.tokens, pl.warps, x8) > info.smem_optin && pl.tokens > 1)
+        pl.tokens = (pl.tokens + 1) / 2;
+    pl.slice_units = slice(pl.cluster);
+    pl.smem = smem_of(pl.slice_units, pl.tokens, pl.warps, x8);
+    if (ceil_div(pr.m, pl.tokens) > 65535)
+        return fail(GB_ERR_UNSUPPORTED, "M=%" PRId64 " is too large for the few-token product", pr.m);
+    if (pl.smem > info.smem_optin) return fail(GB_ERR_UNSUPPORTED, "K=%" PRId64 " is too large", pr.k);
+    pl.k_warps = 1;
+    while (pl.k_warps < pl.warps && pl.k_warps < pl.slice_units) pl.k_warps *= 2;
+
+    Params prm;
+    memset(&prm, 0, sizeof prm);
+    prm.x = pr.x;
+    prm.x_scale = pr.x_scale;
+    prm.ldx = pr.ldx;
+    prm.ldxs = pr.ldxs;
+    for (int i = 0; i < 2; ++i) {
+        const Weights& w = pr.w[pr.gated ? i : 0];
+        prm.q[i] = static_cast<const uint8_t*>(w.q);
+        prm.s[i] = static_cast<const uint16_t*>(w.s);
+        prm.z[i] = static_cast<const uint8_t*>(w.z);
+        prm.ldq[i] = w.ldq;
+        prm.lds[i] = w.lds;
+        prm.ldz[i] = w.ldz;
+    }
+    prm.bias = static_cast<const uint16_t*>(pr.bias);
+    prm.r = static_cast<const uint16_t*>(pr.r);
+    prm.d = static_cast<uint16_t*>(pr.d);
+    prm.ldr = pr.ldr;
+    prm.ldd = pr.ldd;
+    prm.m = static_cast<int>(pr.m);
+    prm.n = static_cast<int>(pr.n);
+    prm.k = static_cast<int>(pr.k);
+    prm.act = pr.act;
+    prm.x_type = pr.x_type;
+    prm.tiles = static_cast<int>(tiles);
+    prm.slice_units = pl.slice_units;
+    prm.k_warps = pl.k_warps;
+    prm.tokens = pl.tokens;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return pr.gated ? launch_g<true>(prm, pl, pr.group, dev, info, s) : launch_g<false>(prm, pl, pr.group, dev, info, s);
+}
+
+}  // namespace
+
+extern "C" {
+
+gb_status_t gb_gemm_linear_w4(const void* X, int64_t ldx, int x_type, const float* x_scale, int64_t ldxs,
+                              const void* Wq, int64_t ldq, const void* scales, int64_t lds, const void* zeros,
+                              int64_t ldz, int group, const void* bias, const void* R, int64_t ldr, int act, void* D,
+                              int64_t ldd, int64_t M, int64_t N, int64_t K, void* stream) {
+    clear_error();
+    const Problem pr{X,     ldx,  x_type, x_scale, ldxs, {{"W", Wq, ldq, scales, lds, zeros, ldz}, {}},
+                     group, bias, R,      ldr,     act,  D,
+                     ldd,   M,    N,      K,       false};
+    return run(pr, stream);
+}
+
+gb_status_t gb_gemm_ffn_gated_w4(const void* X, int64_t ldx, int x_type, const float* x_scale, int64_t ldxs,
+                                 const void* W1q, int64_t ldq1, const void* scales1, int64_t lds1, const void* zeros1,
+                                 int64_t ldz1, const void* W3q, int64_t ldq3, const void* scales3, int64_t lds3,
+                                 const void* zeros3, int64_t ldz3, int group, void* D, int64_t ldd, int64_t M,
+                                 int64_t N, int64_t K, void* stream) {
+    clear_error();
+    const Problem pr{X,
+                     ldx,
+                     x_type,
+                     x_scale,
+                     ldxs,
+                     {{"W1", W1q, ldq1, scales1, lds1, zeros1, ldz1}, {"W3", W3q, ldq3, scales3, lds3, zeros3, ldz3}},
+                     group,
+                     nullptr,
+                     nullptr,
+                     0,
+                     GB_ACT_NONE,
+                     D,
+                     ldd,
+                     M,
+                     N,
+                     K,
+                     true};
+    return run(pr, stream);
+}
+
+}  // extern "C"

@@ -213,6 +213,136 @@ GB_API gb_status_t gb_gemm_linear_dact(const void* dY, int64_t lddy, const void*
                                        const void* Z, int64_t ldz, int act, void* D, int64_t ldd,
                                        int64_t M, int64_t N, int64_t K, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Around the products: the layer for a few tokens with 4-bit weights, the norm between layers,
+ * and dropout.  Matrices are row-major with a leading dimension in elements (bytes for the packed
+ * weights), pointers, streams, errors and ownership as above; nothing is allocated.
+ */
+
+/*
+ * Linear layer with 4-bit weights for a few tokens (the form of gb_gemm_linear that a decoding
+ * step calls: bound by the weights' bytes, which are a quarter of bf16's):
+ *
+ *   W[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group]
+ *   D[m,n] = bf16( act( sum_k X[m,k] W[n,k] + bias[n] ) + R[m,n] )
+ *
+ * No weight is rounded: the products with the integers q - z are summed in fp32 within a group,
+ * and the sums are scaled in fp32.
+ *   X       [M,K], leading dimension ldx (elements); x_type is a gb_x_type_t:
+ *           GB_X_BF16              bf16; x_scale is not read
+ *           GB_X_E4M3_ROW_SCALE    e4m3, row m times x_scale[m*ldxs]
+ *           GB_X_E4M3_GROUP_SCALE  e4m3, X[m,k] times x_scale[m*ldxs + k/128]
+ *           (the two outputs of gb_add_rms_norm_q8)
+ *   Wq      [N,K/2] bytes, row n at Wq + n*ldq (ldq in BYTES): the low nibble of byte j is
+ *           q[n,2j], the high one q[n,2j+1]
+ *   scales  [N,ceil(K/group)] bf16 (lds elements)
+ *   zeros   [N,ceil(K/group)] bytes of 0..15 (ldz bytes), or NULL: z = 8 everywhere
+ *   group   32, 64 or 128 columns; the last group of a row may be shorter
+ *   bias, R, act, D  as gb_gemm_linear (any 2-byte alignment and leading dimension)
+ * K a multiple of 32; Wq's base and ldq multiples of 16 bytes (16-byte loads).  M may be any
+ * size below 2^20; the weights are read again for every 32 tokens, so many tokens belong to
+ * gb_gemm_linear.  M == 0 or N == 0 is a no-op; K == 0 gives D = act(bias) + R.  D must not
+ * overlap X or the weights; D == R is allowed.  Results are the same on every run.
+ */
+typedef enum {
+    GB_X_BF16 = 0,
+    GB_X_E4M3_ROW_SCALE = 1,
+    GB_X_E4M3_GROUP_SCALE = 2
+} gb_x_type_t;
+
+GB_API gb_status_t gb_gemm_linear_w4(const void* X, int64_t ldx, int x_type, const float* x_scale, int64_t ldxs,
+                                     const void* Wq, int64_t ldq, const void* scales, int64_t lds, const void* zeros,
+                                     int64_t ldz, int group, const void* bias, const void* R, int64_t ldr, int act,
+                                     void* D, int64_t ldd, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * The gated pair with 4-bit weights: D = bf16( silu(X . W1^T) * (X . W3^T) ), both products in
+ * fp32 until the end.  W1 and W3 as W above, with the same group; either may have zeros.
+ */
+GB_API gb_status_t gb_gemm_ffn_gated_w4(const void* X, int64_t ldx, int x_type, const float* x_scale, int64_t ldxs,
+                                        const void* W1q, int64_t ldq1, const void* scales1, int64_t lds1,
+                                        const void* zeros1, int64_t ldz1, const void* W3q, int64_t ldq3,
+                                        const void* scales3, int64_t lds3, const void* zeros3, int64_t ldz3, int group,
+                                        void* D, int64_t ldd, int64_t M, int64_t N, int64_t K, void* stream);
+
+/*
+ * Dropout of a matrix's elements, added to a residual:
+ *
+ *   D[m,n] = bf16( keep[m,n] X[m,n] / (1 - p) + R[m,n] )
+ *
+ * keep[m,n] = (word >= round(p 2^32)), where word is number n % 4 of the four 32-bit words of
+ * Philox4x32 with ten rounds (Salmon et al., SC 2011) under the key `seed` (low word first) at
+ * the counter (n / 4, m, offset low, offset high).  The mask depends on nothing else, so it is
+ * never stored: the gradient of X is the same call on the gradient of D, without R.  Give each
+ * use of one seed its own offset.  A dropped element counts as zero whatever it is.
+ *   R  [M,N] (ldr) or NULL;  p in [0, 1]: 0 keeps everything, 1 nothing
+ *   rng_state  NULL, or device memory of two 64-bit words {seed, offset} (8-byte aligned) read
+ *              when the kernel runs, in the place of the two arguments: a captured graph draws
+ *              new masks when the program moves the offset between replays
+ * M == 0 or N == 0 is a no-op.  D == X or D == R (same pointer and leading dimension) is
+ * allowed, other overlaps are not.  Rows move in 16-byte words when every matrix has its rows at
+ * the same addresses modulo 16 bytes (any width), else element by element.
+ */
+GB_API gb_status_t gb_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, double p, uint64_t seed,
+                              uint64_t offset, const void* rng_state, void* D, int64_t ldd, int64_t M, int64_t N,
+                              void* stream);
+
+/*
+ * Root-mean-square norm of a row with the residual's addition before it:
+ *
+ *   h = dropout(X) + R        rstd = 1 / sqrt(mean(h^2) + eps)        Y = bf16(h rstd weight)
+ *
+ * in fp32 from h before its rounding.  dropout(X) is gb_dropout's with p, seed, offset and
+ * rng_state (p = 0: X itself).
+ *   X, Y  [M,D];  weight [D] bf16;  D at most 16384
+ *   R     [M,D] or NULL
+ *   H     [M,D] or NULL: receives bf16(h), the residual stream
+ *   rstd  [M] fp32 or NULL: what the backward pass wants
+ * H == R, H == X, Y == X or Y == R (same pointer and leading dimension) are allowed, other
+ * overlaps are not.  M == 0 or D == 0 is a no-op.
+ */
+GB_API gb_status_t gb_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                                   double eps, double p, uint64_t seed, uint64_t offset, const void* rng_state, void* H,
+                                   int64_t ldh, void* Y, int64_t ldy, float* rstd, int64_t M, int64_t D, void* stream);
+
+/*
+ * The norm with an 8-bit output for serving (no dropout): with y = h rstd weight in fp32,
+ *
+ *   scale = max( max |y| / 448, 2^-126 )       Q = e4m3( y / scale )
+ *
+ * over the row (scale_group = 0: scale[m*lds]) or over each 128 columns (scale_group = 128:
+ * scale[m*lds + d/128]).  Q [M,D] bytes (ldq).  A row or group with a NaN has a NaN scale.
+ */
+GB_API gb_status_t gb_add_rms_norm_q8(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                                      double eps, int scale_group, void* H, int64_t ldh, void* Q, int64_t ldq,
+                                      float* scale, int64_t lds, int64_t M, int64_t D, void* stream);
+
+/*
+ * Backward pass of gb_add_rms_norm.  With xhat = h rstd and g = dY weight:
+ *
+ *   dR = bf16( rstd (g - xhat mean(g xhat)) + dH )      the residual's gradient, and X's if p = 0
+ *   dX = bf16( keep dR / (1 - p) )                      X's gradient (dR before its rounding)
+ *   dweight[d] = sum_m dY[m,d] xhat[m,d]                fp32
+ *
+ *   dY, H   [M,D] bf16; H and rstd as gb_add_rms_norm gave them
+ *   dH      [M,D] or NULL: the gradient that reaches h past the norm
+ *   dX      [M,D]; written and required only if p > 0
+ *   dweight [D], written whole (zeros if M == 0)
+ *   workspace  device memory, 4-byte aligned, of at least
+ *              gb_add_rms_norm_backward_workspace_bytes(); need not be cleared; calls that
+ *              overlap on the GPU need one each
+ * Sums run in a fixed order: results are the same on every run.  dR == dY or dR == dH (same
+ * pointer and leading dimension) is allowed, other overlaps are not.  D at most 16384.
+ */
+GB_API gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh,
+                                            const void* weight, const float* rstd, const void* dH, int64_t lddh,
+                                            double p, uint64_t seed, uint64_t offset, const void* rng_state, void* dR,
+                                            int64_t lddr, void* dX, int64_t lddx, float* dweight, void* workspace,
+                                            size_t workspace_bytes, int64_t M, int64_t D, void* stream);
+
+/* Workspace bytes of gb_add_rms_norm_backward on the current device (0 if M or D is 0). */
+GB_API gb_status_t gb_add_rms_norm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes);
+
 /*
  * Workspace bytes the split-K call needs for this problem on the current
  * device under the current configuration (ffn: 0 = linear, 1 = FFN fusion;
