@@ -143,6 +143,8 @@ struct Config {
     int prod = 0;        // producer threads: 0 auto, 1 or 2 (A and B loads issued by different warps)
     int r_async = -1;    // unaligned R rows (no split): -1 auto, 0 synchronous loads at use, 1 cp.async queue
     int r_boxes = 0;     // R queue depth per epilogue warp: 0 = heuristic, 2..8
+    int w4_cluster = 0;  // 4-bit products: CTAs that share a row tile's columns, 0 = heuristic
+    int w4_k_warps = 0;  // and warps of a CTA that do
     int wide = -1;       // 32x64 boxes on the paired epilogue path: -1 auto, 0 off, 1 R and D, 2 D only
 };
 
@@ -982,6 +984,11 @@ gb_status_t probe_measure(int cta_group, int n, int mode, int alternate, int alu
 
 }  // namespace
 
+gb::host::W4Override gb::host::w4_override() {
+    std::lock_guard<std::mutex> lk(g_cfg_mu);
+    return W4Override{g_cfg.w4_cluster, g_cfg.w4_k_warps};
+}
+
 extern "C" {
 
 gb_status_t gb_measure_mma_rate(int cta_group, int n, int alternate, int num_mma, int units,
@@ -1190,6 +1197,8 @@ gb_status_t gb_set_config(const char* spec) {
             else if (key == "prod" && v >= 0 && v <= 3) c.prod = static_cast<int>(v);
             else if (key == "r_async" && v >= -1 && v <= 1) c.r_async = static_cast<int>(v);
             else if (key == "r_boxes" && (v == 0 || (v >= 2 && v <= gb::kMaxBoxes))) c.r_boxes = static_cast<int>(v);
+            else if (key == "w4_cluster" && (v == 0 || v == 1 || v == 2 || v == 4 || v == 8)) c.w4_cluster = static_cast<int>(v);
+            else if (key == "w4_k_warps" && v >= 0 && v <= 16) c.w4_k_warps = static_cast<int>(v);
             else if (key == "wide" && v >= -1 && v <= 2) c.wide = static_cast<int>(v);
             else return fail(GB_ERR_INVALID_ARG, "unknown config key or value: %s=%ld", key.c_str(), v);
             s += len;

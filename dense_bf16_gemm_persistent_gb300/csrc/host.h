@@ -31,6 +31,12 @@ struct DeviceInfo {
 // The current device's ordinal and properties (read once); refuses a device that is not sm_103.
 gb_status_t device_info(int* dev_out, DeviceInfo* info);
 
+// The plan of the 4-bit products as gb_set_config() fixes it; 0: not.
+struct W4Override {
+    int cluster, k_warps;
+};
+W4Override w4_override();
+
 // What gb_last_plan() reports: a static format that takes six %lld.
 void note_plan(const char* fmt, long long a, long long b, long long c, long long d, long long e, long long f);
 

@@ -91,16 +91,17 @@ gb_status_t validate(const Problem& pr) {
 struct Plan {
     int tokens;     // of a pass
     int cluster;    // CTAs that share a row tile's columns
+    int clusters;   // at once
     int k_warps;    // warps of a CTA that share them
     int warps;
     int slice_units;
     size_t smem;
 };
 
-template <int G, int NT, bool GATED, bool X8>
+template <int G, int NT, bool GATED, int X>
 gb_status_t launch(const Params& prm, const Plan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
     static std::atomic<bool> ready[64];  // (two threads may both set the attribute: to the same value)
-    auto kern = gb::w4::w4_kernel<G, NT, GATED, X8>;
+    auto kern = gb::w4::w4_kernel<G, NT, GATED, X>;
     cudaError_t e;
     if (!ready[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(info.smem_optin));
@@ -108,7 +109,7 @@ gb_status_t launch(const Params& prm, const Plan& pl, int dev, const DeviceInfo&
         ready[dev].store(true, std::memory_order_release);
     }
     const int64_t groups = ceil_div(prm.tiles, pl.warps / pl.k_warps);
-    const int64_t clusters = std::min<int64_t>(groups, std::max(1, 2 * info.sms / pl.cluster));
+    const int64_t clusters = std::min<int64_t>(groups, pl.clusters);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * pl.cluster), static_cast<unsigned>(ceil_div(prm.m, pl.tokens)), 1);
@@ -130,8 +131,9 @@ gb_status_t launch(const Params& prm, const Plan& pl, int dev, const DeviceInfo&
 
 template <int G, int NT, bool GATED>
 gb_status_t launch_x(const Params& prm, const Plan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
-    return prm.x_type == GB_X_BF16 ? launch<G, NT, GATED, false>(prm, pl, dev, info, stream)
-                                   : launch<G, NT, GATED, true>(prm, pl, dev, info, stream);
+    if (prm.x_type == GB_X_BF16) return launch<G, NT, GATED, gb::w4::kXBf16>(prm, pl, dev, info, stream);
+    if (prm.x_type == GB_X_E4M3_ROW_SCALE) return launch<G, NT, GATED, gb::w4::kXRowScale>(prm, pl, dev, info, stream);
+    return launch<G, NT, GATED, gb::w4::kXGroupScale>(prm, pl, dev, info, stream);
 }
 
 template <int G, bool GATED>
@@ -148,9 +150,93 @@ gb_status_t launch_g(const Params& prm, const Plan& pl, int group, int dev, cons
     return launch_nt<128, GATED>(prm, pl, dev, info, stream);
 }
 
-size_t smem_of(int slice_units, int tokens, int warps, bool x8) {
-    const size_t nt = tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4;
-    return static_cast<size_t>(slice_units) * 4 * tokens * (256 + (x8 ? 4 : 0)) + 2 * warps * nt * 8 * kRows * 4;
+// mma tiles of eight tokens that a pass holds
+int tiles_of(int tokens) { return tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4; }
+
+// tokens for which a CTA keeps the sums, times the CTAs that the tokens are shared out to (as the
+// kernel does: the rows first, two or four octets of them, then the tokens)
+int share_tokens(int tokens, int cluster) {
+    const int by_token = std::max(1, cluster / 2);  // (at most)
+    return static_cast<int>(ceil_div(tokens, by_token)) * by_token;
+}
+
+size_t smem_of(int slice_units, int tokens, int warps, int group, int cluster, bool group_x) {
+    const size_t nt = tiles_of(tokens), units = slice_units;
+    return static_cast<size_t>(warps) * gb::w4::slots_of(group, static_cast<int>(nt)) * gb::w4::kUnitBytes +  // rings
+           units * (kUnit / 8) * tokens * 16 +                                    // x
+           ((group_x ? units * (kUnit / gb::w4::kStep) : 1) + units * (kUnit / group)) * 8 * nt * 4 +  // its scales and sums
+           static_cast<size_t>(2) * warps * share_tokens(tokens, cluster) * kRows * 4 +  // the warps' sums
+           static_cast<size_t>(warps) * (kUnit / group) * 128;                      // their units' scales
+}
+
+// Clusters of `cluster` CTAs that run at once, one CTA an SM (the GPU's partitions need not hold a
+// whole number of them).
+gb_status_t clusters_at_once(int cluster, int dev, const DeviceInfo& info, int* out) {
+    static std::atomic<int> known[64][4];
+    std::atomic<int>& slot = known[dev][cluster == 1 ? 0 : cluster == 2 ? 1 : cluster == 4 ? 2 : 3];
+    int n = cluster == 1 ? info.sms : slot.load(std::memory_order_relaxed);
+    if (n == 0) {
+        auto kern = gb::w4::w4_kernel<128, 1, false, gb::w4::kXBf16>;
+        cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(info.smem_optin));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(info.sms / cluster * cluster, 1, 1);
+        cfg.blockDim = dim3(32 * gb::w4::warps_of(1), 1, 1);
+        cfg.dynamicSmemBytes = info.smem_optin;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&n, kern, &cfg)) != cudaSuccess)
+            return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+        n = std::max(1, n);
+        slot.store(n, std::memory_order_relaxed);
+    }
+    *out = n;
+    return GB_OK;
+}
+
+// The plan of least time by a model of three measured parts: a unit of each of an SM's warps takes
+// 1.4 us (64 KB of weights at its share of the memory's rate), the join of a tile 0.3 us in a CTA
+// and 1.2 us over a cluster, and x's slice 20 ns for each 16 bytes a thread to lay out.
+gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInfo& info, Plan* out) {
+    const int units = std::max(1, static_cast<int>(ceil_div(pr.k, kUnit)));
+    const W4Override want = w4_override();
+    double best = 0.0;
+    // (with every token in one pass if any plan has room for its x, else fewer at a time)
+    for (int tokens = static_cast<int>(std::min<int64_t>(pr.m, 32)); tokens >= 1 && best == 0.0;
+         tokens = tokens > 1 ? (tokens + 1) / 2 : 0) {
+        const int warps = gb::w4::warps_of(tiles_of(tokens));
+        for (int cluster = 1; cluster <= 8 && (cluster <= units || want.cluster); cluster *= 2) {
+            if (want.cluster && cluster != want.cluster) continue;
+            const int slice = static_cast<int>(ceil_div(units, cluster));
+            const size_t smem = smem_of(slice, tokens, warps, pr.group, cluster, pr.x_type == GB_X_E4M3_GROUP_SCALE);
+            if (smem > info.smem_optin) continue;
+            int clusters = 0;
+            const gb_status_t st = clusters_at_once(cluster, dev, info, &clusters);
+            if (st != GB_OK) return st;
+            for (int k_warps = 1; k_warps <= warps; ++k_warps) {
+                if (warps % k_warps || (want.k_warps && k_warps != want.k_warps)) continue;
+                const int64_t rounds = ceil_div(ceil_div(tiles, warps / k_warps), clusters);
+                const double join = cluster > 1 ? 1.2 : k_warps > 1 ? 0.3 : 0.1;
+                const double time = rounds * (ceil_div(slice, k_warps) * 1.4 * warps / 16 + join) +
+                                    0.02 * slice * (kUnit / 8) * tokens / (32 * warps);
+                if (best == 0.0 || time < best) {
+                    best = time;
+                    *out = Plan{tokens, cluster, clusters, k_warps, warps, slice, smem};
+                }
+                if (k_warps >= slice && !want.k_warps) break;
+            }
+        }
+    }
+    if (best == 0.0) return fail(GB_ERR_UNSUPPORTED, "K=%" PRId64 " is too large", pr.k);
+    if (ceil_div(pr.m, out->tokens) > 65535)
+        return fail(GB_ERR_UNSUPPORTED, "M=%" PRId64 " is too large for the few-token product", pr.m);
+    return GB_OK;
 }
 
 gb_status_t run(const Problem& pr, void* stream) {
@@ -160,29 +246,10 @@ gb_status_t run(const Problem& pr, void* stream) {
     DeviceInfo info;
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
 
-    const int out_rows = pr.gated ? 8 : kRows;
+    const int out_rows = pr.gated ? kRows / 2 : kRows;
     const int64_t tiles = ceil_div(pr.n, out_rows);
-    const int units = static_cast<int>(ceil_div(pr.k, kUnit));
-    const bool x8 = pr.x_type != GB_X_BF16;
     Plan pl{};
-    pl.tokens = static_cast<int>(std::min<int64_t>(pr.m, 32));
-    pl.warps = gb::w4::kMaxWarps;
-    pl.cluster = 1;
-    auto slice = [&](int c) { return std::max(1, static_cast<int>(ceil_div(units, c))); };
-    // Split the columns over a cluster while x's slice does not fit, or while there are too few
-    // row tiles to give every SM a CTA and each warp keeps a unit of its own.
-    while (pl.cluster < 8 && (smem_of(slice(pl.cluster), pl.tokens, pl.warps, x8) > info.smem_optin / 2 - 1024 ||
-                              (tiles * pl.cluster < info.sms && slice(pl.cluster) > pl.warps)))
-        pl.cluster *= 2;
-    while (smem_of(slice(pl.cluster), pl.tokens, pl.warps, x8) > info.smem_optin && pl.tokens > 1)
-        pl.tokens = (pl.tokens + 1) / 2;
-    pl.slice_units = slice(pl.cluster);
-    pl.smem = smem_of(pl.slice_units, pl.tokens, pl.warps, x8);
-    if (ceil_div(pr.m, pl.tokens) > 65535)
-        return fail(GB_ERR_UNSUPPORTED, "M=%" PRId64 " is too large for the few-token product", pr.m);
-    if (pl.smem > info.smem_optin) return fail(GB_ERR_UNSUPPORTED, "K=%" PRId64 " is too large", pr.k);
-    pl.k_warps = 1;
-    while (pl.k_warps < pl.warps && pl.k_warps < pl.slice_units) pl.k_warps *= 2;
+    if ((st = make_plan(pr, tiles, dev, info, &pl)) != GB_OK) return st;
 
     Params prm;
     memset(&prm, 0, sizeof prm);
@@ -198,6 +265,14 @@ gb_status_t run(const Problem& pr, void* stream) {
         prm.ldq[i] = w.ldq;
         prm.lds[i] = w.lds;
         prm.ldz[i] = w.ldz;
+    }
+    const int64_t unit_groups = kUnit / pr.group;
+    prm.wide_scales = 1;
+    for (int i = 0; i < (pr.gated ? 2 : 1); ++i) {
+        const Weights& w = pr.w[i];
+        if (!aligned_to(w.s, 2 * unit_groups) || w.lds % unit_groups ||
+            (w.z && (!aligned_to(w.z, unit_groups) || w.ldz % unit_groups)))
+            prm.wide_scales = 0;
     }
     prm.bias = static_cast<const uint16_t*>(pr.bias);
     prm.r = static_cast<const uint16_t*>(pr.r);

@@ -428,6 +428,10 @@ GB_API const char* gb_last_error(void);
  * hint_a, hint_b, hint_r, hint_d (L2 eviction policy of the TMA loads of A,
  * of B / W1 / W3, of R, and of the TMA stores of D and Z: 0 = none, 1 = evict
  * first, 2 = evict last, -1 = the built-in choice).
+ * The products with 4-bit weights take w4_cluster (CTAs that share a row tile's
+ * columns: 1, 2, 4 or 8; 0 = auto) and w4_k_warps (warps of a CTA that share
+ * them: a divisor of its warps, 1..16; 0 = auto); a pair of values that no plan
+ * has makes their calls return GB_ERR_UNSUPPORTED.
  * Process-wide; returns GB_ERR_INVALID_ARG on an unknown key or value.
  */
 GB_API gb_status_t gb_set_config(const char* spec);
