@@ -138,9 +138,8 @@ gb_status_t launch_x(const Params& prm, const Plan& pl, int dev, const DeviceInf
 
 template <int G, bool GATED>
 gb_status_t launch_nt(const Params& prm, const Plan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
-    if (pl.tokens <= 8) return launch_x<G, 1, GATED>(prm, pl, dev, info, stream);
-    if (pl.tokens <= 16) return launch_x<G, 2, GATED>(prm, pl, dev, info, stream);
-    return launch_x<G, 4, GATED>(prm, pl, dev, info, stream);
+    return pl.tokens <= 8 ? launch_x<G, 1, GATED>(prm, pl, dev, info, stream)
+                          : launch_x<G, 2, GATED>(prm, pl, dev, info, stream);
 }
 
 template <bool GATED>
@@ -151,7 +150,7 @@ gb_status_t launch_g(const Params& prm, const Plan& pl, int group, int dev, cons
 }
 
 // mma tiles of eight tokens that a pass holds
-int tiles_of(int tokens) { return tokens <= 8 ? 1 : tokens <= 16 ? 2 : 4; }
+int tiles_of(int tokens) { return tokens <= 8 ? 1 : 2; }
 
 // tokens for which a CTA keeps the sums, times the CTAs that the tokens are shared out to (as the
 // kernel does: the rows first, two or four octets of them, then the tokens)
@@ -162,7 +161,7 @@ int share_tokens(int tokens, int cluster) {
 
 size_t smem_of(int slice_units, int tokens, int warps, int group, int cluster, bool group_x) {
     const size_t nt = tiles_of(tokens), units = slice_units;
-    return static_cast<size_t>(warps) * gb::w4::slots_of(group, static_cast<int>(nt)) * gb::w4::kUnitBytes +  // rings
+    return static_cast<size_t>(warps) * gb::w4::kUnitBytes +                        // slots
            units * (kUnit / 8) * tokens * 16 +                                    // x
            ((group_x ? units * (kUnit / gb::w4::kStep) : 1) + units * (kUnit / group)) * 8 * nt * 4 +  // its scales and sums
            static_cast<size_t>(2) * warps * share_tokens(tokens, cluster) * kRows * 4 +  // the warps' sums
@@ -187,7 +186,7 @@ gb_status_t clusters_at_once(int cluster, int dev, const DeviceInfo& info, int* 
         attr[0].val.clusterDim.y = 1;
         attr[0].val.clusterDim.z = 1;
         cfg.gridDim = dim3(info.sms / cluster * cluster, 1, 1);
-        cfg.blockDim = dim3(32 * gb::w4::warps_of(1), 1, 1);
+        cfg.blockDim = dim3(32 * gb::w4::warps_of(128, 1), 1, 1);
         cfg.dynamicSmemBytes = info.smem_optin;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
@@ -208,9 +207,9 @@ gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInf
     const W4Override want = w4_override();
     double best = 0.0;
     // (with every token in one pass if any plan has room for its x, else fewer at a time)
-    for (int tokens = static_cast<int>(std::min<int64_t>(pr.m, 32)); tokens >= 1 && best == 0.0;
+    for (int tokens = static_cast<int>(std::min<int64_t>(pr.m, gb::w4::kMaxTokens)); tokens >= 1 && best == 0.0;
          tokens = tokens > 1 ? (tokens + 1) / 2 : 0) {
-        const int warps = gb::w4::warps_of(tiles_of(tokens));
+        const int warps = gb::w4::warps_of(pr.group, tiles_of(tokens));
         for (int cluster = 1; cluster <= 8 && (cluster <= units || want.cluster); cluster *= 2) {
             if (want.cluster && cluster != want.cluster) continue;
             const int slice = static_cast<int>(ceil_div(units, cluster));

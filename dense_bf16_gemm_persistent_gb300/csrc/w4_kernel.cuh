@@ -39,14 +39,11 @@ constexpr int kStep = 128;           // columns of one step: four lanes x 16 byt
 constexpr int kUnit = 2 * kStep;     // columns that a warp loads at a time
 constexpr int kRows = 32;            // weight rows of a tile: two of mma's, which share x's fragments
 constexpr int kUnitBytes = kRows * kUnit / 2;  // weights of a unit: 32 rows of 128 bytes
-// Warps of a CTA (one CTA an SM): the more tokens, the more registers hold their sums.
-__host__ __device__ constexpr int warps_of(int nt) { return nt == 1 ? 16 : nt == 2 ? 12 : 8; }
-
-// A warp multiplies a unit from registers while the next is on its way to its slot in shared memory
-// (64 KB for an SM's sixteen warps: at the memory's rate it takes 1.4 us to consume that, longer
-// than a load takes).  With more tokens, and more groups, there are two slots and the registers hold
-// a group of it at a time.
-__host__ __device__ constexpr int slots_of(int group, int nt) { return nt == 1 || (nt == 2 && group == 128) ? 1 : 2; }
+// Warps of a CTA (one CTA an SM): more tokens and groups, more registers for them.  A warp multiplies a
+// unit from registers while the next is on its way to its slot in shared memory (64 KB for an SM's
+// sixteen warps: at the memory's rate it takes 1.4 us to consume that, longer than a load takes).
+__host__ __device__ constexpr int warps_of(int group, int nt) { return nt == 1 ? 16 : group == 128 ? 12 : 8; }
+constexpr int kMaxTokens = 16;       // of a pass: two mma tiles of eight
 
 enum { kXBf16 = 0, kXRowScale = 1, kXGroupScale = 2 };
 
@@ -216,68 +213,87 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
     const int at = threadIdx.x & 15, first = threadIdx.x >> 4, stride = blockDim.x >> 4;
     const int group = at / (4 * kPer), lt = at / kPer & 3, c = group * kPer + at % kPer;
     const int total = steps * tokens;  // a step of a token is sixteen threads
+    constexpr int kBatch = NT == 1 ? 2 : 4;  // loads that a thread has on their way
     bool finite = true;
     uint32_t kept[4];  // the thread's first chunk, which is often its only one
     if (!X8) {
         // the largest finite exponent of each token's columns
         if (threadIdx.x < tokens) top[threadIdx.x] = 0;
         __syncthreads();
-        for (int i = first; (i & ~1) < total; i += stride) {
-            const int token = i / steps, col = col_base + (i - token * steps) * kStep + at * 8;
-            const bool any = i < total;
-            uint32_t w[4], most = 0;
-            load_x<X8>(p, wide, token0 + token, col, any && col < p.k, w);
+        for (int i = first; (i & ~1) < total; i += kBatch * stride) {
+            uint32_t w[kBatch][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (i == first) kept[j] = w[j];
-                const uint32_t lo = w[j] >> 7 & 0xff, hi = w[j] >> 23 & 0xff;
-                finite = finite && lo != 0xff && hi != 0xff;
-                most = max(most, max(lo == 0xff ? 0u : lo, hi == 0xff ? 0u : hi));
+            for (int u = 0; u < kBatch; ++u) {
+                const int at_u = i + u * stride, token = at_u / steps, col = col_base + (at_u - token * steps) * kStep + at * 8;
+                load_x<X8>(p, wide, token0 + token, col, at_u < total && col < p.k, w[u]);
             }
 #pragma unroll
-            for (int d = 8; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-            if (any && at == 0) atomicMax(&top[token], most);
+            for (int u = 0; u < kBatch; ++u) {
+                const int at_u = i + u * stride;
+                if ((at_u & ~1) >= total) break;
+                uint32_t most = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (at_u == first) kept[j] = w[u][j];
+                    const uint32_t lo = w[u][j] >> 7 & 0xff, hi = w[u][j] >> 23 & 0xff;
+                    finite = finite && lo != 0xff && hi != 0xff;
+                    most = max(most, max(lo == 0xff ? 0u : lo, hi == 0xff ? 0u : hi));
+                }
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+                if (at_u < total && at == 0) atomicMax(&top[at_u / steps], most);
+            }
         }
         __syncthreads();
     }
-    for (int i = first; i < total; i += stride) {
-        const int token = i / steps, step = i - token * steps, col = col_base + step * kStep + at * 8;
-        uint32_t w[4];
-        if (!X8 && i == first) {
+    for (int i = first; i < total; i += kBatch * stride) {
+        uint32_t w[kBatch][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = kept[j];
-        } else {
-            load_x<X8>(p, wide, token0 + token, col, col < p.k, w);
-        }
-        float v[8], scale = kHalfShift;
-        if (X8) {
+        for (int u = 0; u < kBatch; ++u) {
+            const int at_u = i + u * stride, token = at_u / steps, col = col_base + (at_u - token * steps) * kStep + at * 8;
+            if (!X8 && at_u == first) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                __nv_fp8x2_e4m3 pair;
-                pair.__x = static_cast<__nv_fp8x2_storage_t>(w[j / 2] >> (16 * (j & 1)));
-                const float2 f = static_cast<float2>(pair);
-                v[2 * j] = f.x;
-                v[2 * j + 1] = f.y;
+                for (int j = 0; j < 4; ++j) w[u][j] = kept[j];
+            } else {
+                load_x<X8>(p, wide, token0 + token, col, at_u < total && col < p.k, w[u]);
             }
-            if (at == 0 && (X == kXGroupScale || step == 0))
-                scale *= p.x_scale[(token0 + token) * p.ldxs + (X == kXGroupScale ? min(col, p.k - 1) / kStep : 0)];
-        } else {
-            // 2^(14 - (top - 127)), below 2^127; its reciprocal goes to the sum
-            const uint32_t up = min(268u - top[token], 253u);
-            const float f = __uint_as_float(up << 23);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[2 * j] = (w[j] >> 7 & 0xff) == 0xff ? 0.f : __uint_as_float(w[j] << 16) * f;
-                v[2 * j + 1] = (w[j] >> 23 & 0xff) == 0xff ? 0.f : __uint_as_float(w[j] & 0xffff0000u) * f;
-            }
-            scale *= __uint_as_float((254u - up) << 23);
         }
-        constexpr float kSixteenth = 0.0625f;
-        xs[((step * 4 + c) * tokens + token) * 4 + lt] =
-            make_uint4(half_pair(v[0], v[4]), half_pair(v[1] * kSixteenth, v[5] * kSixteenth), half_pair(v[2], v[6]),
-                       half_pair(v[3] * kSixteenth, v[7] * kSixteenth));
-        if (at == 0 && X == kXGroupScale) xscale[step * 8 * NT + token] = scale;
-        if (at == 0 && X != kXGroupScale && step == 0) xscale[token] = scale;
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int at_u = i + u * stride, token = at_u / steps, step = at_u - token * steps;
+            if (at_u >= total) break;
+            float v[8], scale = kHalfShift;
+            if (X8) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    __nv_fp8x2_e4m3 pair;
+                    pair.__x = static_cast<__nv_fp8x2_storage_t>(w[u][j / 2] >> (16 * (j & 1)));
+                    const float2 f = static_cast<float2>(pair);
+                    v[2 * j] = f.x;
+                    v[2 * j + 1] = f.y;
+                }
+                if (at == 0 && (X == kXGroupScale || step == 0)) {
+                    const int column = X == kXGroupScale ? min(col_base / kStep + step, (p.k - 1) / kStep) : 0;
+                    scale *= p.x_scale[(token0 + token) * p.ldxs + column];
+                }
+            } else {
+                // 2^(14 - (top - 127)), below 2^127; its reciprocal goes to the sum
+                const uint32_t up = min(268u - top[token], 253u);
+                const float f = __uint_as_float(up << 23);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    v[2 * j] = (w[u][j] >> 7 & 0xff) == 0xff ? 0.f : __uint_as_float(w[u][j] << 16) * f;
+                    v[2 * j + 1] = (w[u][j] >> 23 & 0xff) == 0xff ? 0.f : __uint_as_float(w[u][j] & 0xffff0000u) * f;
+                }
+                scale *= __uint_as_float((254u - up) << 23);
+            }
+            constexpr float kSixteenth = 0.0625f;
+            xs[((step * 4 + c) * tokens + token) * 4 + lt] =
+                make_uint4(half_pair(v[0], v[4]), half_pair(v[1] * kSixteenth, v[5] * kSixteenth), half_pair(v[2], v[6]),
+                           half_pair(v[3] * kSixteenth, v[7] * kSixteenth));
+            if (at == 0 && X == kXGroupScale) xscale[step * 8 * NT + token] = scale;
+            if (at == 0 && X != kXGroupScale && step == 0) xscale[token] = scale;
+        }
     }
     return finite;
 }
@@ -345,11 +361,10 @@ struct Cursor {
 // G: columns of a weight's scale.  NT: tokens / 8, rounded up.  GATED: the pair.  X: x's type.
 //
 // A CTA's warps form teams of k_warps; a team takes row tiles in turn and its warps share the
-// tile's units.  Each warp streams its units through a ring of its own in shared memory with
+// tile's units.  Each warp streams its units through a slot of its own in shared memory with
 // 16-byte cp.async, which runs ahead over the ends of tiles; no barrier but the warp's own.
 template <int G, int NT, bool GATED, int X>
-__global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_constant__ Params p) {
-    constexpr int kSlots = slots_of(G, NT);
+__global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __grid_constant__ Params p) {
     constexpr bool kGroupX = X == kXGroupScale;
     constexpr int kPer = G / 32;         // words of a lane in a group
     constexpr int kGroups = kUnit / G;   // of a unit: what a lane fetches the scales of, for one row
@@ -357,7 +372,6 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
     constexpr int kOutRows = GATED ? 16 : 32;
     // z off each weight takes 16 G / 32 instructions a group, off the sums 8 NT
     constexpr bool kLess = 2 * G / 32 <= NT;
-    constexpr bool kHeld = slots_of(G, NT) == 1;
     extern __shared__ __align__(16) uint8_t smem[];
     const int tid = threadIdx.x, warps = blockDim.x >> 5;
     const int warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -372,10 +386,10 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
     const int col_base = unit0 * kUnit;  // the slice's first column
     const int steps = units * (kUnit / kStep);
 
-    // shared memory: the rings, x, its scales and sums, the scales of
+    // shared memory: the slots, x, its scales and sums, the scales of
     // each warp's unit, and the sums that this CTA adds up
-    const uint32_t ring = smem_addr(smem) + warp * kSlots * kUnitBytes;
-    uint4* xs = reinterpret_cast<uint4*>(smem + warps * kSlots * kUnitBytes);
+    const uint32_t slot = smem_addr(smem) + warp * kUnitBytes;
+    uint4* xs = reinterpret_cast<uint4*>(smem + warps * kUnitBytes);
     float* xscale = reinterpret_cast<float*>(xs + static_cast<size_t>(p.slice_units) * (kUnit / 8) * p.tokens);
     float* xsum = xscale + (kGroupX ? p.slice_units * (kUnit / kStep) : 1) * 8 * NT;
 
@@ -387,13 +401,13 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
     const int k_part = warp % k_warps, team = warp / k_warps;
     const int groups = (p.k + G - 1) / G;
 
-    // A slot of the ring holds 32 rows of 128 bytes.  A row's eight 16-byte chunks are swapped by
+    // A slot holds 32 rows of 128 bytes.  A row's eight 16-byte chunks are swapped by
     // swap(row), so that neither the copies (four rows a warp) nor the reads (4, 8 or 16 bytes a
     // lane of eight rows: its part of a group) meet in a bank.
     auto swap = [](uint32_t row) { return (row & 1) << 2 | (row & 2) | (row >> 2 & 1); };
-    auto fetch = [&](const Cursor<GATED>& c, uint32_t slot) {
+    auto fetch = [&](const Cursor<GATED>& c) {
         const int col_u = col_base + c.unit * kUnit;
-        const uint32_t to = ring + slot * kUnitBytes + (lane >> 3) * 128;
+        const uint32_t to = slot + (lane >> 3) * 128;
         // rows lane / 8 + 4i: the swap of i odd differs in its lowest bit
         const uint32_t even = ((lane & 7) ^ swap(lane >> 3)) << 4, odd = even ^ 16;
         const uint8_t *a = c.qa + col_u / 2, *b = c.qb + col_u / 2;
@@ -469,9 +483,9 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
     Cursor<GATED> ahead;  // the unit whose copies are started next
     ahead.at_tile(p, cluster * teams + team, lane);
     ahead.unit = k_part;
-    auto start_next = [&](uint32_t slot) {
+    auto start_next = [&] {
         if (ahead.tile < p.tiles) {
-            fetch(ahead, slot);
+            fetch(ahead);
             fetch_scales(ahead, raw);
             ahead.unit += k_warps;
             if (ahead.unit >= units) {
@@ -481,7 +495,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
         }
         copy_commit();
     };
-    if (mine > 0) start_next(0);
+    if (mine > 0) start_next();
 
     // (a word a token for stage_x: where the units' scales will be)
     const bool finite = stage_x<G, NT, X>(p, xs, xscale, xsum_end, col_base, steps, token0, tokens);
@@ -579,7 +593,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
                     const uint32_t at = team_sums + buffer * buffer_bytes + (rank * k_warps + k_part) * share_bytes +
                                         4 * ((token >> token_bits) * share_rows + row);
                     float v = total[r / 2][j][i + r % 2 * 2];
-                    if (!kGroupX) v *= xscale[token];
+                    if (!kGroupX) v *= load_shared_float(scales_lane - t * 8 + 4 * token);
                     if (X == kXBf16 && odd) {
                         const int64_t n = static_cast<int64_t>(tile) * kOutRows + (GATED ? kind * 8 : r * 8) + g;
                         if (n < p.n) v += odd_part(GATED ? r >> 1 : 0, n, token);
@@ -590,7 +604,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
     };
 
     if (ranks > 1) cluster_wait();
-    uint32_t slot = 0, buffer = 0;
+    uint32_t buffer = 0;
     int before = -1;
     for (int first = cluster * teams; first < p.tiles; first += tile_step) {
         const int tile = first + team;
@@ -616,7 +630,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
             }
             copy_wait<0>();
             __syncwarp();  // the unit is there
-            const uint32_t w_at = ring + slot * kUnitBytes + g * 128;
+            const uint32_t w_at = slot + g * 128;
             // words of rows g, g + 8, g + 16, g + 24 of a group
             auto load_group = [&](int s, int j, uint32_t (&to)[4][kPer]) {
 #pragma unroll
@@ -630,15 +644,11 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
                         load_shared(row + (((4 * s + j) ^ swap(g)) << 4) + t * 4, to[r][0]);
                 }
             };
-            uint32_t w[kHeld ? kGroups : 1][4][kPer];
-            if (kHeld) {
+            uint32_t w[kGroups][4][kPer];
 #pragma unroll
-                for (int f = 0; f < kGroups; ++f) load_group(f / kStepGroups, f % kStepGroups, w[f]);
-                __syncwarp();  // the slot may take the next copies
-            }
-            // (without: the other slot does, which every lane is done with)
-            start_next(kHeld ? 0 : slot ^ 1);
-            if (!kHeld) slot ^= 1;
+            for (int f = 0; f < kGroups; ++f) load_group(f / kStepGroups, f % kStepGroups, w[f]);
+            __syncwarp();  // the slot may take the next copies
+            start_next();
 
             uint32_t x_at = unit * (kUnit / 8) * 16 * tokens;
             uint32_t scale_at = scales_lane + (kGroupX ? unit * (kUnit / kStep) * 32 * NT : 0);
@@ -654,10 +664,9 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
                         xs1[i] = __uint_as_float(e[1]);
                     }
                 }
-#pragma unroll(kHeld ? kStepGroups : 1)
+#pragma unroll
                 for (int j = 0; j < kStepGroups; ++j) {
-                    uint32_t (&ws)[4][kPer] = w[kHeld ? s * kStepGroups + j : 0];
-                    if (!kHeld) load_group(s, j, ws);
+                    const uint32_t (&ws)[4][kPer] = w[s * kStepGroups + j];
                     float acc[2][NT][4];
                     uint32_t row_sz[4], zero[4];  // of rows g, g + 8, g + 16, g + 24
                     load_shared(scales_of_warp + (s * kStepGroups + j) * 128 + g * 16, row_sz[0], row_sz[1], row_sz[2],
@@ -714,7 +723,7 @@ __global__ void __launch_bounds__(32 * warps_of(NT), 1) w4_kernel(const __grid_c
                 scale_at += NT * 32;
                 sums_at += kStepGroups * NT * 32;
             };
-#pragma unroll(kHeld ? kUnit / kStep : 1)
+#pragma unroll
             for (int s = 0; s < kUnit / kStep; ++s) multiply(s);
         }
 
