@@ -199,40 +199,49 @@ gb_status_t clusters_at_once(int cluster, int dev, const DeviceInfo& info, int* 
     return GB_OK;
 }
 
-// The plan of least time by a model of three measured parts: a unit of each of an SM's warps takes
-// 1.4 us (64 KB of weights at its share of the memory's rate), the join of a tile 0.3 us in a CTA
-// and 1.2 us over a cluster, and x's slice 20 ns for each 16 bytes a thread to lay out.
+// The plan of least time by a model fitted to measured plans (GB300, microseconds): a unit takes all
+// of an SM's warps together `unit`, each round's join 1.1, or 1.4 over more than two CTAs, and
+// x's layout 0.45 for each chunk of a thread, half of that where no largest value is looked for.
+// (A round: every team takes one row tile.  Passes of tokens run side by side.)
 gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInfo& info, Plan* out) {
     const int units = std::max(1, static_cast<int>(ceil_div(pr.k, kUnit)));
     const W4Override want = w4_override();
     double best = 0.0;
-    // (with every token in one pass if any plan has room for its x, else fewer at a time)
-    for (int tokens = static_cast<int>(std::min<int64_t>(pr.m, gb::w4::kMaxTokens)); tokens >= 1 && best == 0.0;
-         tokens = tokens > 1 ? (tokens + 1) / 2 : 0) {
-        const int warps = gb::w4::warps_of(pr.group, tiles_of(tokens));
+    int tokens = static_cast<int>(std::min<int64_t>(pr.m, gb::w4::kMaxTokens));
+    for (bool last = false; !last; tokens = (tokens + 1) / 2) {
+        const int nt = tiles_of(tokens), warps = gb::w4::warps_of(pr.group, nt);
+        const int64_t passes = ceil_div(pr.m, tokens);
+        const double unit = nt == 1 ? (pr.group == 128 ? 1.15 : pr.group == 64 ? 1.25 : 1.5)
+                                    : (pr.group == 128 ? 1.7 : pr.group == 64 ? 1.55 : 1.8);
         for (int cluster = 1; cluster <= 8 && (cluster <= units || want.cluster); cluster *= 2) {
             if (want.cluster && cluster != want.cluster) continue;
             const int slice = static_cast<int>(ceil_div(units, cluster));
             const size_t smem = smem_of(slice, tokens, warps, pr.group, cluster, pr.x_type == GB_X_E4M3_GROUP_SCALE);
             if (smem > info.smem_optin) continue;
-            int clusters = 0;
-            const gb_status_t st = clusters_at_once(cluster, dev, info, &clusters);
+            int at_once = 0;
+            const gb_status_t st = clusters_at_once(cluster, dev, info, &at_once);
             if (st != GB_OK) return st;
+            const int64_t clusters = std::max<int64_t>(1, at_once / passes);  // of a pass
+            const double chunks = ceil_div(static_cast<int64_t>(slice) * (kUnit / gb::w4::kStep) * tokens, 2 * warps);
             for (int k_warps = 1; k_warps <= warps; ++k_warps) {
                 if (warps % k_warps || (want.k_warps && k_warps != want.k_warps)) continue;
-                const int64_t rounds = ceil_div(ceil_div(tiles, warps / k_warps), clusters);
-                const double join = cluster > 1 ? 1.2 : k_warps > 1 ? 0.3 : 0.1;
-                const double time = rounds * (ceil_div(slice, k_warps) * 1.4 * warps / 16 + join) +
-                                    0.02 * slice * (kUnit / 8) * tokens / (32 * warps);
+                const int64_t rounds = ceil_div(ceil_div(tiles, warps / k_warps), clusters) * ceil_div(passes, at_once);
+                const double time = rounds * (ceil_div(slice, k_warps) * unit + (cluster > 2 ? 1.4 : 1.1)) +
+                                    chunks * (pr.x_type == GB_X_BF16 ? 0.45 : 0.22);
                 if (best == 0.0 || time < best) {
                     best = time;
-                    *out = Plan{tokens, cluster, clusters, k_warps, warps, slice, smem};
+                    *out = Plan{tokens, cluster, static_cast<int>(clusters), k_warps, warps, slice, smem};
                 }
                 if (k_warps >= slice && !want.k_warps) break;
             }
         }
+        // (as many tokens in a pass as there are, or half of them, or as few as x has room for)
+        last = tokens == 1 || (best != 0.0 && 2 * tokens <= std::min<int64_t>(pr.m, gb::w4::kMaxTokens));
     }
-    if (best == 0.0) return fail(GB_ERR_UNSUPPORTED, "K=%" PRId64 " is too large", pr.k);
+    if (best == 0.0)
+        return want.cluster || want.k_warps
+                   ? fail(GB_ERR_UNSUPPORTED, "no plan has the configured w4_cluster and w4_k_warps")
+                   : fail(GB_ERR_UNSUPPORTED, "K=%" PRId64 " is too large", pr.k);
     if (ceil_div(pr.m, out->tokens) > 65535)
         return fail(GB_ERR_UNSUPPORTED, "M=%" PRId64 " is too large for the few-token product", pr.m);
     return GB_OK;

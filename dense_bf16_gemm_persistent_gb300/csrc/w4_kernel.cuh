@@ -213,9 +213,9 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
     const int at = threadIdx.x & 15, first = threadIdx.x >> 4, stride = blockDim.x >> 4;
     const int group = at / (4 * kPer), lt = at / kPer & 3, c = group * kPer + at % kPer;
     const int total = steps * tokens;  // a step of a token is sixteen threads
-    constexpr int kBatch = NT == 1 ? 2 : 4;  // loads that a thread has on their way
+    constexpr int kBatch = 4;  // loads that a thread has on their way
     bool finite = true;
-    uint32_t kept[4];  // the thread's first chunk, which is often its only one
+    uint32_t kept[kBatch][4];  // the thread's first chunks, which are often its only ones
     if (!X8) {
         // the largest finite exponent of each token's columns
         if (threadIdx.x < tokens) top[threadIdx.x] = 0;
@@ -234,7 +234,7 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
                 uint32_t most = 0;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (at_u == first) kept[j] = w[u][j];
+                    if (i == first) kept[u][j] = w[u][j];
                     const uint32_t lo = w[u][j] >> 7 & 0xff, hi = w[u][j] >> 23 & 0xff;
                     finite = finite && lo != 0xff && hi != 0xff;
                     most = max(most, max(lo == 0xff ? 0u : lo, hi == 0xff ? 0u : hi));
@@ -251,9 +251,9 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int at_u = i + u * stride, token = at_u / steps, col = col_base + (at_u - token * steps) * kStep + at * 8;
-            if (!X8 && at_u == first) {
+            if (!X8 && i == first) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) w[u][j] = kept[j];
+                for (int j = 0; j < 4; ++j) w[u][j] = kept[u][j];
             } else {
                 load_x<X8>(p, wide, token0 + token, col, at_u < total && col < p.k, w[u]);
             }
