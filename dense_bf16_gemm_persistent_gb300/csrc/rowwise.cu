@@ -46,16 +46,27 @@ gb_status_t check_ptr(const char* name, const void* p, uintptr_t align) {
     return GB_OK;
 }
 
+// The generator's keys, and the words that are kept: those of at least p 2^32, or above one less.
 gb_status_t make_drop(double p, uint64_t seed, uint64_t offset, const void* state, Drop* out) {
     if (!(p >= 0.0 && p <= 1.0)) return fail(GB_ERR_INVALID_ARG, "p=%g is not a probability", p);
     if (!aligned_to(state, 8)) return fail(GB_ERR_UNSUPPORTED, "rng_state must be 8-byte aligned");
-    out->threshold = static_cast<uint64_t>(std::llround(p * 4294967296.0));
-    out->seed = seed;
-    out->offset = offset;
+    const uint64_t least = static_cast<uint64_t>(std::llround(p * 4294967296.0));
+    uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+    for (auto& key : out->keys) {
+        key[0] = k0;
+        key[1] = k1;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    out->offset[0] = static_cast<uint32_t>(offset);
+    out->offset[1] = static_cast<uint32_t>(offset >> 32);
     out->state = static_cast<const uint64_t*>(state);
+    out->limit = least > 0 ? static_cast<uint32_t>(least - 1) : 0;
     out->scale = static_cast<float>(1.0 / (1.0 - p));
     return GB_OK;
 }
+
+int drop_kind(double p, const void* state) { return p == 0.0 ? kNoDrop : state ? kState : kKeys; }
 
 // Whether all matrices have the same shift on every row: the same position, in elements,
 // modulo 8 of their bases and of their leading dimensions.
@@ -78,16 +89,30 @@ int64_t chunks_of(const Mat& m, int64_t rows, int64_t cols, bool wide) {
 
 // How the rows of a norm are given to threads.
 struct RowPlan {
-    int chunks_per_thread = 0;  // 1, 2 or 4
+    int chunks_per_thread = 0;  // 2 or 4
     int threads = 0, rows = 1;  // of a block
     bool wide = false;
 };
 
-// Up to `warp_chunks` chunks a row is one warp's, eight rows to a block: no barrier.  Above, it
+// Up to 64 chunks a row is one warp's, eight rows to a block: no barrier.  Above, it
 // is a block's, with two chunks a thread while 512 threads cover it and four beyond.
-constexpr int kWarpChunks = 128, kWarpChunksBwd = 64;
+constexpr int kWarpChunks = 64;
+
+RowPlan plan_chunks(int64_t chunks) {
+    RowPlan pl;
+    if (chunks <= kWarpChunks) {
+        pl.threads = 32;
+        pl.rows = 8;
+        pl.chunks_per_thread = 2;
+    } else {
+        pl.chunks_per_thread = chunks <= 1024 ? 2 : 4;
+        pl.threads = static_cast<int>(ceil_div(chunks, 32 * pl.chunks_per_thread)) * 32;
+    }
+    return pl;
+}
+
 template <size_t N>
-RowPlan plan_rows(const Mat (&mats)[N], int64_t rows, int64_t cols, int warp_chunks) {
+RowPlan plan_rows(const Mat (&mats)[N], int64_t rows, int64_t cols) {
     RowPlan pl;
     pl.wide = same_shift(mats, rows);
     int64_t chunks = chunks_of(mats[0], rows, cols, pl.wide);
@@ -95,14 +120,9 @@ RowPlan plan_rows(const Mat (&mats)[N], int64_t rows, int64_t cols, int warp_chu
         pl.wide = false;
         chunks = ceil_div(cols, 8);
     }
-    if (chunks <= warp_chunks) {
-        pl.threads = 32;
-        pl.rows = 8;
-        pl.chunks_per_thread = chunks <= 32 ? 1 : chunks <= 64 ? 2 : 4;
-    } else {
-        pl.chunks_per_thread = chunks <= 1024 ? 2 : 4;
-        pl.threads = static_cast<int>(ceil_div(chunks, 32 * pl.chunks_per_thread)) * 32;
-    }
+    const bool wide = pl.wide;
+    pl = plan_chunks(chunks);
+    pl.wide = wide;
     return pl;
 }
 
@@ -111,52 +131,73 @@ gb_status_t launched(const char* what) {
     return e == cudaSuccess ? GB_OK : cuda_fail(e, what);
 }
 
-template <int V, bool DROP, int OUT>
-void launch_norm(const NormParams& p, const RowPlan& pl, cudaStream_t stream) {
-    const unsigned grid = static_cast<unsigned>(ceil_div(p.m, pl.rows));
-    const size_t smem = OUT == kGroupScale ? static_cast<size_t>(pl.rows) * ceil_div(p.d, kScaleGroup) * 4 : 0;
-    norm_kernel<V, DROP, OUT><<<grid, dim3(pl.threads, pl.rows), smem, stream>>>(p);
+// More than the default 48 KB of dynamic shared memory, once for each kernel and device.  (Two
+// threads may both set the attribute: to the same value.)
+template <class Kernel>
+gb_status_t allow_smem(Kernel kernel, std::atomic<bool>* ready, int dev, size_t most) {
+    if (ready[dev].load(std::memory_order_acquire)) return GB_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    ready[dev].store(true, std::memory_order_release);
+    return GB_OK;
 }
 
-template <bool DROP, int OUT>
-gb_status_t run_norm(const NormParams& p, const RowPlan& pl, cudaStream_t stream) {
-    if (pl.chunks_per_thread == 1) launch_norm<1, DROP, OUT>(p, pl, stream);
-    else if (pl.chunks_per_thread == 2) launch_norm<2, DROP, OUT>(p, pl, stream);
-    else launch_norm<4, DROP, OUT>(p, pl, stream);
-    note_plan("kernel=add_rms_norm output=%lld dropout=%lld threads=%lld rows=%lld chunks=%lld wide=%lld", OUT, DROP,
-              pl.threads, pl.rows, pl.chunks_per_thread, pl.wide);
+// Blocks that fill the GPU with `per_sm` threads an SM, a multiple of 8 of them (see the kernels'
+// rows); no more than there are rows for.
+int64_t blocks_for(int64_t m, const RowPlan& pl, int per_sm, int sms) {
+    const int64_t full = static_cast<int64_t>(sms) * std::max(1, per_sm / (pl.threads * pl.rows)) / 8 * 8;
+    return std::min(ceil_div(m, pl.rows), std::max<int64_t>(8, full));
+}
+
+template <int V, int DROP, int OUT>
+gb_status_t launch_norm(const NormParams& p, const RowPlan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
+    static std::atomic<bool> ready[64];
+    gb_status_t st = allow_smem(norm_kernel<V, DROP, OUT>, ready, dev, info.smem_optin - 1024);
+    if (st != GB_OK) return st;
+    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : 1024, info.sms);
+    size_t smem = static_cast<size_t>(kRowStages * 2 + 1) * V * 16 * pl.threads * pl.rows;
+    if (OUT == kGroupScale) smem += static_cast<size_t>(pl.rows) * ceil_div(p.d, kScaleGroup) * 4;
+    norm_kernel<V, DROP, OUT><<<static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream>>>(p);
+    note_plan("kernel=add_rms_norm output=%lld dropout=%lld threads=%lld rows=%lld blocks=%lld wide=%lld", OUT, DROP,
+              pl.threads, pl.rows, blocks, pl.wide);
     return launched("add_rms_norm launch");
 }
 
-template <int V, bool DROP>
-gb_status_t launch_bwd(NormBwdParams p, const RowPlan& pl, int blocks, int dev, cudaStream_t stream) {
-    static std::atomic<bool> ready[64];  // (two threads may both set the attribute: to the same value)
-    size_t smem = pl.rows > 1 ? static_cast<size_t>(p.d) * 4 : 0;
-    if (V == 0) {
-        p.per_thread = pl.chunks_per_thread;
-        smem = static_cast<size_t>(pl.threads) * pl.chunks_per_thread * 64;
-        if (!ready[dev].load(std::memory_order_acquire)) {
-            const cudaError_t e = cudaFuncSetAttribute(norm_bwd_kernel<V, DROP>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * 4 * 64);
-            if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-            ready[dev].store(true, std::memory_order_release);
-        }
-    }
+template <int DROP, int OUT>
+gb_status_t run_norm(const NormParams& p, const RowPlan& pl, int dev, const DeviceInfo& info, cudaStream_t stream) {
+    return pl.chunks_per_thread <= 2 ? launch_norm<2, DROP, OUT>(p, pl, dev, info, stream)
+                                     : launch_norm<4, DROP, OUT>(p, pl, dev, info, stream);
+}
+
+template <int V, int DROP>
+gb_status_t launch_bwd(const NormBwdParams& p, const RowPlan& pl, int blocks, int dev, const DeviceInfo& info,
+                       cudaStream_t stream) {
+    static std::atomic<bool> ready[64];
+    gb_status_t st = allow_smem(norm_bwd_kernel<V, DROP>, ready, dev, info.smem_optin - 1024);
+    if (st != GB_OK) return st;
+    // two stages of three matrices, and the weight; and the join of a block's rows
+    size_t smem = static_cast<size_t>(kBwdStages * 3 + 1) * V * 16 * pl.threads * pl.rows;
+    if (pl.rows > 1) smem = std::max(smem, static_cast<size_t>(p.d) * 4);
     norm_bwd_kernel<V, DROP><<<blocks, dim3(pl.threads, pl.rows), smem, stream>>>(p);
     return launched("add_rms_norm_backward launch");
 }
 
-template <bool DROP>
-gb_status_t run_bwd(const NormBwdParams& p, const RowPlan& pl, int blocks, int dev, cudaStream_t stream) {
-    if (pl.chunks_per_thread <= 2) return launch_bwd<2, DROP>(p, pl, blocks, dev, stream);
-    return launch_bwd<0, DROP>(p, pl, blocks, dev, stream);
+template <int DROP>
+gb_status_t run_bwd(const NormBwdParams& p, const RowPlan& pl, int blocks, int dev, const DeviceInfo& info,
+                    cudaStream_t stream) {
+    return pl.chunks_per_thread <= 2 ? launch_bwd<2, DROP>(p, pl, blocks, dev, info, stream)
+                                     : launch_bwd<4, DROP>(p, pl, blocks, dev, info, stream);
 }
 
-// Blocks of the backward pass, at most: each keeps a part of the weight's gradient, so there
-// are no more than two for each SM.  A multiple of 8 (see norm_bwd_kernel's rows).
-int bwd_blocks(int64_t m, int64_t d, int sms) {
-    const int64_t rows_per_block = d <= 8 * kWarpChunksBwd - 7 ? 8 : 1;
-    return static_cast<int>(std::min<int64_t>(ceil_div(m, rows_per_block), std::max(8, 2 * sms / 8 * 8)));
+// Blocks of the backward pass: each keeps a part of the weight's gradient in the workspace.  The
+// workspace's size is asked without the matrices' addresses: with no shift there are most blocks.
+int bwd_blocks(int64_t m, const RowPlan& pl, int sms) {
+    return static_cast<int>(blocks_for(m, pl, pl.chunks_per_thread == 2 ? 768 : 512, sms));
+}
+
+int64_t bwd_workspace(int64_t m, int64_t d, int sms) {
+    const int64_t by_warps = bwd_blocks(m, plan_chunks(ceil_div(d, 8)), sms);
+    return std::max<int64_t>(by_warps, bwd_blocks(m, plan_chunks(ceil_div(d + 7, 8)), sms)) * d * 4;
 }
 
 }  // namespace
@@ -188,8 +229,15 @@ gb_status_t gb_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, d
     prm.n = static_cast<int>(N);
     prm.wide = same_shift(mats, M);
     prm.chunks = static_cast<int>(chunks_of(mats[0], M, N, prm.wide));
-    const int64_t blocks = std::min<int64_t>(ceil_div(M * prm.chunks, kDropoutThreads), 16 * info.sms);
-    dropout_kernel<<<static_cast<unsigned>(blocks), kDropoutThreads, 0, static_cast<cudaStream_t>(stream)>>>(prm);
+    const int64_t blocks = std::min<int64_t>(ceil_div(M * prm.chunks, kDropoutThreads * kDropoutBatch), 8 * info.sms);
+    prm.step_rows = blocks * kDropoutThreads / prm.chunks;
+    prm.step_chunks = static_cast<int>(blocks * kDropoutThreads % prm.chunks);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (drop_kind(p, rng_state)) {
+        case kNoDrop: dropout_kernel<kNoDrop><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, s>>>(prm); break;
+        case kKeys: dropout_kernel<kKeys><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, s>>>(prm); break;
+        default: dropout_kernel<kState><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, s>>>(prm); break;
+    }
     note_plan("kernel=dropout blocks=%lld threads=%lld chunks=%lld wide=%lld residual=%lld state=%lld", blocks,
               kDropoutThreads, prm.chunks, prm.wide, R != nullptr, rng_state != nullptr);
     return launched("dropout launch");
@@ -228,11 +276,15 @@ gb_status_t gb_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t l
     prm.m = static_cast<int>(M);
     prm.d = static_cast<int>(D);
     prm.eps = static_cast<float>(eps);
-    const RowPlan pl = plan_rows(mats, M, D, kWarpChunks);
+    const RowPlan pl = plan_rows(mats, M, D);
     prm.wide = pl.wide;
     prm.wide_weight = aligned_to(weight, 16);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return p > 0.0 ? run_norm<true, kBf16>(prm, pl, s) : run_norm<false, kBf16>(prm, pl, s);
+    switch (drop_kind(p, rng_state)) {
+        case kNoDrop: return run_norm<kNoDrop, kBf16>(prm, pl, dev, info, s);
+        case kKeys: return run_norm<kKeys, kBf16>(prm, pl, dev, info, s);
+        default: return run_norm<kState, kBf16>(prm, pl, dev, info, s);
+    }
 }
 
 gb_status_t gb_add_rms_norm_q8(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight, double eps,
@@ -270,11 +322,12 @@ gb_status_t gb_add_rms_norm_q8(const void* X, int64_t ldx, const void* R, int64_
     prm.m = static_cast<int>(M);
     prm.d = static_cast<int>(D);
     prm.eps = static_cast<float>(eps);
-    const RowPlan pl = plan_rows(mats, M, D, kWarpChunks);
+    const RowPlan pl = plan_rows(mats, M, D);
     prm.wide = pl.wide;
     prm.wide_weight = aligned_to(weight, 16);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return scale_group ? run_norm<false, kGroupScale>(prm, pl, s) : run_norm<false, kRowScale>(prm, pl, s);
+    return scale_group ? run_norm<kNoDrop, kGroupScale>(prm, pl, dev, info, s)
+                       : run_norm<kNoDrop, kRowScale>(prm, pl, dev, info, s);
 }
 
 gb_status_t gb_add_rms_norm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes) {
@@ -287,7 +340,7 @@ gb_status_t gb_add_rms_norm_backward_workspace_bytes(int64_t M, int64_t D, size_
     int dev = 0;
     DeviceInfo info;
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
-    *bytes = static_cast<size_t>(bwd_blocks(M, D, info.sms)) * D * sizeof(float);
+    *bytes = static_cast<size_t>(bwd_workspace(M, D, info.sms));
     return GB_OK;
 }
 
@@ -320,8 +373,7 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int blocks = 0;
     if (M > 0) {
-        blocks = bwd_blocks(M, D, info.sms);
-        const size_t need = static_cast<size_t>(blocks) * D * sizeof(float);
+        const size_t need = static_cast<size_t>(bwd_workspace(M, D, info.sms));
         if (!workspace || workspace_bytes < need)
             return fail(GB_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0),
                         need);
@@ -341,10 +393,15 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
         prm.lddx = lddx;
         prm.m = static_cast<int>(M);
         prm.d = static_cast<int>(D);
-        const RowPlan pl = plan_rows(mats, M, D, kWarpChunksBwd);
+        const RowPlan pl = plan_rows(mats, M, D);
         prm.wide = pl.wide;
         prm.wide_weight = aligned_to(weight, 16);
-        st = drop ? run_bwd<true>(prm, pl, blocks, dev, s) : run_bwd<false>(prm, pl, blocks, dev, s);
+        blocks = bwd_blocks(M, pl, info.sms);
+        switch (drop_kind(p, rng_state)) {
+            case kNoDrop: st = run_bwd<kNoDrop>(prm, pl, blocks, dev, info, s); break;
+            case kKeys: st = run_bwd<kKeys>(prm, pl, blocks, dev, info, s); break;
+            default: st = run_bwd<kState>(prm, pl, blocks, dev, info, s); break;
+        }
         if (st != GB_OK) return st;
         note_plan("kernel=add_rms_norm_backward blocks=%lld dropout=%lld threads=%lld rows=%lld chunks=%lld wide=%lld",
                   blocks, drop, pl.threads, pl.rows, pl.chunks_per_thread, pl.wide);

@@ -27,68 +27,98 @@ namespace rowwise {
 // crosses the products' halves with the others and the key, which then moves on by its Weyl
 // increments.  Element (row, col) of a matrix takes word col % 4 of the counter
 // (col / 4, row, offset low, offset high) under the key `seed`.
-struct Key {
-    uint32_t k0, k1, c2, c3;
-};
-
-__device__ __forceinline__ void philox(uint32_t c0, uint32_t c1, const Key& key, uint32_t (&out)[4]) {
-    uint32_t c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
-#pragma unroll
-    for (int i = 0; i < 10; ++i) {
-        const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-        c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
-        c1 = static_cast<uint32_t>(b);
-        c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
-        c3 = static_cast<uint32_t>(a);
-        k0 += 0x9E3779B9u;
-        k1 += 0xBB67AE85u;
-    }
-    out[0] = c0;
-    out[1] = c1;
-    out[2] = c2;
-    out[3] = c3;
-}
-
-// What dropout needs: an element is kept when its word is at least `threshold` = p 2^32 (64
-// bits: p = 1 keeps nothing), and a kept one is multiplied by `scale` = 1 / (1 - p).
+//
+// The ten rounds' keys come with the launch (constant memory: no instruction and no register), or
+// are made from a seed in device memory.
 struct Drop {
-    uint64_t threshold;
-    uint64_t seed, offset;
-    const uint64_t* state;  // device memory {seed, offset} that takes the place of the two above, or null
-    float scale;
+    uint32_t keys[10][2];
+    uint32_t offset[2];
+    const uint64_t* state;  // device memory {seed, offset} in the place of the two above, or null
+    uint32_t limit;         // kept: words above it
+    float scale;            // of a kept element: 1 / (1 - p)
 };
 
-__device__ __forceinline__ Key drop_key(const Drop& d) {
-    const uint64_t seed = d.state ? d.state[0] : d.seed, offset = d.state ? d.state[1] : d.offset;
-    return Key{static_cast<uint32_t>(seed), static_cast<uint32_t>(seed >> 32), static_cast<uint32_t>(offset),
-               static_cast<uint32_t>(offset >> 32)};
-}
+// What a kernel draws with: kNoDrop nothing, kKeys the launch's keys, kState those of `state`.
+enum { kNoDrop = 0, kKeys = 1, kState = 2 };
 
-// Drop the chunk of `row` that starts at column `col0` (-7 at least).  A dropped element is
-// zero whatever it was (an infinity or a NaN among them), so it is selected, not multiplied.
-__device__ __forceinline__ void drop_chunk(float (&v)[8], int row, int col0, const Drop& d, const Key& key) {
-    // a column below 0 is not an element: its word is not used, and the group -1 or -2 wraps
-    const int phase = col0 & 3;
-    const uint32_t group = static_cast<uint32_t>((col0 - phase) >> 2);
-    uint32_t w[12];
-    auto words = [&](int at) {
-        uint32_t o[4];
-        philox(group + at, static_cast<uint32_t>(row), key, o);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[4 * at + i] = o[i];
-    };
-    words(0);
-    words(1);
-    if (phase) {  // (the same for the whole row)
-        words(2);
-#pragma unroll
-        for (int i = 0; i < 10; ++i) w[i] = phase & 2 ? w[i + 2] : w[i];
-#pragma unroll
-        for (int i = 0; i < 9; ++i) w[i] = phase & 1 ? w[i + 1] : w[i];
+template <int DROP>
+struct Draw {
+    const Drop& d;
+    uint32_t seed[2], offset[2];
+
+    __device__ __forceinline__ explicit Draw(const Drop& drop) : d(drop), seed{0, 0}, offset{0, 0} {
+        if (DROP == kState) {
+            const uint64_t s = drop.state[0], o = drop.state[1];
+            seed[0] = static_cast<uint32_t>(s);
+            seed[1] = static_cast<uint32_t>(s >> 32);
+            offset[0] = static_cast<uint32_t>(o);
+            offset[1] = static_cast<uint32_t>(o >> 32);
+        } else if (DROP == kKeys) {
+            offset[0] = drop.offset[0];
+            offset[1] = drop.offset[1];
+        }
     }
+
+    __device__ __forceinline__ void words(uint32_t group, uint32_t row, uint32_t (&out)[4]) const {
+        uint32_t c0 = group, c1 = row, c2 = offset[0], c3 = offset[1], k0 = seed[0], k1 = seed[1];
+        // (in a form that the compiler does not see to be the same on every call: else it keeps the
+        // twenty keys in registers across the loop over rows)
+        if (DROP == kState) asm volatile("" : "+r"(k0), "+r"(k1));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = w[i] >= d.threshold ? v[i] * d.scale : 0.f;
-}
+        for (int i = 0; i < 10; ++i) {
+            if (DROP == kKeys) {
+                k0 = d.keys[i][0];
+                k1 = d.keys[i][1];
+            }
+            const uint64_t a = static_cast<uint64_t>(c0) * 0xD2511F53u, b = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
+            c0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0;
+            c1 = static_cast<uint32_t>(b);
+            c2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
+            c3 = static_cast<uint32_t>(a);
+            k0 += 0x9E3779B9u;
+            k1 += 0xBB67AE85u;
+        }
+        out[0] = c0;
+        out[1] = c1;
+        out[2] = c2;
+        out[3] = c3;
+    }
+
+    // Which of four elements of a group are kept (bits 0 .. 3).
+    __device__ __forceinline__ uint32_t kept(uint32_t group, int row) const {
+        uint32_t w[4], bits = 0;
+        words(group, static_cast<uint32_t>(row), w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bits |= w[i] > d.limit ? 1u << i : 0u;
+        return bits;
+    }
+
+    // Drop the chunk of `row` at columns col0 .. col0 + 7.  A dropped element is zero whatever it was
+    // (an infinity or a NaN among them): it is selected, not multiplied.  BITS: with fewer registers
+    // and more instructions.
+    template <bool BITS>
+    __device__ __forceinline__ void chunk(float (&v)[8], int row, int col0) const {
+        // a column below 0 is not an element: its word is not used, and the group -1 or -2 wraps
+        const int phase = col0 & 3;  // (the same for the whole row)
+        const uint32_t group = static_cast<uint32_t>((col0 - phase) >> 2);
+        if (!BITS && phase == 0) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[4];
+                words(group + h, static_cast<uint32_t>(row), w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * h + i] = w[i] > d.limit ? v[4 * h + i] * d.scale : 0.f;
+            }
+            return;
+        }
+        uint32_t bits = kept(group, row);
+        bits |= kept(group + 1, row) << 4;
+        if (phase) bits |= kept(group + 2, row) << 8;
+        bits >>= phase;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = bits >> i & 1 ? v[i] * d.scale : 0.f;
+    }
+};
 
 // ---------------------------------------------------------------- chunks
 
@@ -111,21 +141,13 @@ __device__ __forceinline__ uint4 pack(const float (&v)[8]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The chunk's elements of `row` (0 outside the row).  The element-by-element loops are kept
-// rolled: they run on a row's two ends (and on rows whose matrices are not aligned alike).
+// The chunk's elements of `row` (0 outside the row).
 __device__ __forceinline__ uint4 load_chunk(const uint16_t* row, int col0, int cols, bool wide) {
     if (wide && col0 >= 0 && col0 + 8 <= cols) return *reinterpret_cast<const uint4*>(row + col0);
-    uint4 u = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-    for (int i = 7; i >= 0; --i) {
-        const int col = col0 + i;
-        const uint32_t e = col >= 0 && col < cols ? row[col] : 0;
-        u.w = __funnelshift_l(u.z, u.w, 16);
-        u.z = __funnelshift_l(u.y, u.z, 16);
-        u.y = __funnelshift_l(u.x, u.y, 16);
-        u.x = u.x << 16 | e;
-    }
-    return u;
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = col0 + i >= 0 && col0 + i < cols ? row[col0 + i] : 0u;
+    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
 }
 
 __device__ __forceinline__ void store_chunk(uint16_t* row, int col0, int cols, bool wide, uint4 u) {
@@ -148,6 +170,39 @@ __device__ __forceinline__ int row_shift(const uint16_t* row) {
     return static_cast<int>(reinterpret_cast<uintptr_t>(row) >> 1) & 7;
 }
 
+// A chunk on its way to the thread's own 16 bytes of shared memory: a thread reads only what it
+// asked for itself, so that waiting for its own copies is all the order there has to be.  A row's
+// first chunk may start before the row: `inside` says that this is memory of the matrix too (of the
+// row before); what it holds of that is cleared by read_chunk().
+__device__ __forceinline__ void fetch_chunk(uint4* to, const uint16_t* row, int col0, int cols, bool wide, bool inside) {
+    if (wide && col0 < cols && (col0 >= 0 || inside)) {
+        const int bytes = min(16, 2 * (cols - col0));  // (zeros after a row's end)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                     "l"(row + col0), "r"(bytes)
+                     : "memory");
+    } else {
+        *to = load_chunk(row, col0, cols, false);
+    }
+}
+
+__device__ __forceinline__ uint4 read_chunk(const uint4* from, int col0) {
+    uint4 u = *from;
+    if (col0 < 0) {  // (-7 .. -1)
+        const int n = -col0;
+        uint32_t* w = &u.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = n >= 2 * i + 2 ? 0u : n == 2 * i + 1 ? w[i] & 0xffff0000u : w[i];
+    }
+    return u;
+}
+
+__device__ __forceinline__ void fetch_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void fetch_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // ---------------------------------------------------------------- dropout
 
 struct DropoutParams {
@@ -157,31 +212,55 @@ struct DropoutParams {
     int64_t ldx, ldr, ldd;
     int m, n;
     int chunks;  // of a row, its shift counted in
+    int64_t step_rows;  // the grid's threads in rows and chunks
+    int step_chunks;
     int wide;
     Drop drop;
 };
 
-constexpr int kDropoutThreads = 256;
+constexpr int kDropoutThreads = 256, kDropoutBatch = 2;
 
-__global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const DropoutParams p) {
-    const Key key = drop_key(p.drop);
-    const int64_t total = static_cast<int64_t>(p.m) * p.chunks;
-    for (int64_t at = static_cast<int64_t>(blockIdx.x) * kDropoutThreads + threadIdx.x; at < total;
-         at += static_cast<int64_t>(gridDim.x) * kDropoutThreads) {
-        const int row = static_cast<int>(at / p.chunks), j = static_cast<int>(at - static_cast<int64_t>(row) * p.chunks);
-        const uint16_t* x = p.x + row * p.ldx;
-        const int col0 = 8 * j - (p.wide ? row_shift(x) : 0);
-        if (col0 >= p.n) continue;
-        float v[8];
-        unpack(load_chunk(x, col0, p.n, p.wide), v);
-        drop_chunk(v, row, col0, p.drop, key);
-        if (p.r) {
-            float r[8];
-            unpack(load_chunk(p.r + row * p.ldr, col0, p.n, p.wide), r);
+// Threads walk the matrix's chunks a grid's width apart, kDropoutBatch at a time; a step of the
+// walk is `step_rows` rows and `step_chunks` chunks, so that no thread divides again.
+template <int DROP>
+__global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const __grid_constant__ DropoutParams p) {
+    const Draw<DROP> draw(p.drop);
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kDropoutThreads + threadIdx.x;
+    int64_t row = at / p.chunks;
+    int j = static_cast<int>(at - row * p.chunks);
+    while (row < p.m) {
+        uint4 xu[kDropoutBatch], ru[kDropoutBatch];
+        int rows[kDropoutBatch], col0[kDropoutBatch];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] += r[i];
+        for (int u = 0; u < kDropoutBatch; ++u) {
+            rows[u] = static_cast<int>(row);
+            const uint16_t* x = p.x + row * p.ldx;
+            col0[u] = row < p.m ? 8 * j - (p.wide ? row_shift(x) : 0) : p.n;
+            if (col0[u] < p.n) {
+                xu[u] = load_chunk(x, col0[u], p.n, p.wide);
+                if (p.r) ru[u] = load_chunk(p.r + row * p.ldr, col0[u], p.n, p.wide);
+            }
+            row += p.step_rows;
+            j += p.step_chunks;
+            if (j >= p.chunks) {
+                j -= p.chunks;
+                ++row;
+            }
         }
-        store_chunk(p.d + row * p.ldd, col0, p.n, p.wide, pack(v));
+#pragma unroll
+        for (int u = 0; u < kDropoutBatch; ++u) {
+            if (col0[u] >= p.n) continue;
+            float v[8];
+            unpack(xu[u], v);
+            if (DROP) draw.template chunk<false>(v, rows[u], col0[u]);
+            if (p.r) {
+                float r[8];
+                unpack(ru[u], r);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += r[i];
+            }
+            store_chunk(p.d + static_cast<int64_t>(rows[u]) * p.ldd, col0[u], p.n, p.wide, pack(v));
+        }
     }
 }
 
@@ -269,36 +348,57 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int col0, int cols, boo
 }
 
 // h = dropout(x) + r;  rstd = 1 / sqrt(mean(h^2) + eps);  y = h rstd weight, in fp32 from h
-// before its rounding.  V chunks a thread.  Dynamic shared memory: kGroupScale's maxima.
-template <int V, bool DROP, int OUT>
-__global__ void __launch_bounds__(512, 1) norm_kernel(const NormParams p) {
-    __shared__ float sums[32];
-    __shared__ uint32_t maxima[32];
-    extern __shared__ uint32_t group_max[];
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    if (row >= p.m) return;  // (only whole warps of a block of several rows)
-    const uint16_t* x = p.x + row * p.ldx;
-    const int shift = p.wide ? row_shift(x) : 0;
-    const int tid = threadIdx.x, threads = blockDim.x;
-    Key key{};
-    if (DROP) key = drop_key(p.drop);
+// before its rounding.  V chunks a thread.  A block takes the rows row0, row0 + stride, ...:
+// `stride` is a multiple of 8 rows, so a thread's rows all have the same shift and it keeps its
+// part of the weight; kRowStages - 1 rows are on their way beside the one that is worked on.
+// Dynamic shared memory: the rows [stage][x or r][chunk][thread], the weight, kGroupScale's maxima.
+constexpr int kRowStages = 3;
 
-    uint4 xu[V], ru[V];
+template <int V, int DROP, int OUT>
+__global__ void __launch_bounds__(512, V == 4 ? 1 : 2) norm_kernel(const __grid_constant__ NormParams p) {
+    __shared__ float sums[2][32];
+    __shared__ uint32_t maxima[2][32];
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int row0 = blockIdx.x * blockDim.y + threadIdx.y, stride = gridDim.x * blockDim.y;
+    const int shift = p.wide ? row_shift(p.x + row0 * p.ldx) : 0;
+    const int tid = threadIdx.x, threads = blockDim.x, all = blockDim.x * blockDim.y;
+    uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.y * threads + tid;
+    uint32_t* group_max = reinterpret_cast<uint32_t*>(smem + static_cast<size_t>(kRowStages * 2 + 1) * V * all * 16);
+    const Draw<DROP> draw(p.drop);
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < p.m) {
 #pragma unroll
-    for (int k = 0; k < V; ++k) {
-        const int col0 = 8 * (tid + k * threads) - shift;
-        xu[k] = load_chunk(x, col0, p.d, p.wide);
-        if (p.r) ru[k] = load_chunk(p.r + row * p.ldr, col0, p.d, p.wide);
-    }
+            for (int k = 0; k < V; ++k) {
+                const int col0 = 8 * (tid + k * threads) - shift;
+                fetch_chunk(slots + (stage * 2 * V + k) * all, p.x + row * p.ldx, col0, p.d, p.wide, row > 0 && p.ldx >= 8);
+                if (p.r)
+                    fetch_chunk(slots + ((stage * 2 + 1) * V + k) * all, p.r + row * p.ldr, col0, p.d, p.wide,
+                                row > 0 && p.ldr >= 8);
+            }
+        }
+        fetch_commit();
+    };
+#pragma unroll
+    for (int s = 0; s < kRowStages - 1; ++s) fetch(row0 + static_cast<int64_t>(s) * stride, s);
+    uint4* weight = slots + kRowStages * 2 * V * all;  // (the thread's own part of it)
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+        weight[k * all] = load_chunk(p.weight, 8 * (tid + k * threads) - shift, p.d, shift == 0 && p.wide_weight);
+
+    int stage = 0, turn = 0;
+    for (int64_t r = row0; r < p.m; r += stride, turn ^= 1) {
+    const int row = static_cast<int>(r);
+    fetch(r + static_cast<int64_t>(kRowStages - 1) * stride, stage == 0 ? kRowStages - 1 : stage - 1);
+    fetch_wait<kRowStages - 1>();
     float v[V][8], sum = 0.f;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int col0 = 8 * (tid + k * threads) - shift;
-        unpack(xu[k], v[k]);
-        if (DROP && col0 < p.d) drop_chunk(v[k], row, col0, p.drop, key);
+        unpack(read_chunk(slots + (stage * 2 * V + k) * all, col0), v[k]);
+        if (DROP) draw.template chunk<true>(v[k], row, col0);
         if (p.r) {
             float r[8];
-            unpack(ru[k], r);
+            unpack(read_chunk(slots + ((stage * 2 + 1) * V + k) * all, col0), r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[k][i] += r[i];
         }
@@ -306,14 +406,15 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormParams p) {
         for (int i = 0; i < 8; ++i) sum = fmaf(v[k][i], v[k][i], sum);
         if (p.h && col0 < p.d) store_chunk(p.h + row * p.ldh, col0, p.d, p.wide, pack(v[k]));
     }
-    const float rstd = 1.f / sqrtf(row_sum(sum, sums) / static_cast<float>(p.d) + p.eps);
+    stage = stage == kRowStages - 1 ? 0 : stage + 1;
+    const float rstd = 1.f / sqrtf(row_sum(sum, sums[turn]) / static_cast<float>(p.d) + p.eps);
     if (p.rstd && tid == 0) p.rstd[row] = rstd;
 
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int col0 = 8 * (tid + k * threads) - shift;
         float w[8];
-        unpack(load_chunk(p.weight, col0, p.d, shift == 0 && p.wide_weight), w);
+        unpack(weight[k * all], w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[k][i] = v[k][i] * rstd * w[i];
         if (OUT == kBf16 && col0 < p.d) store_chunk(p.y + row * p.ldy, col0, p.d, p.wide, pack(v[k]));
@@ -324,7 +425,7 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormParams p) {
         for (int k = 0; k < V; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[k][i]) & 0x7fffffffu);
-        const float scale = scale_of(row_max(top, maxima));
+        const float scale = scale_of(row_max(top, maxima[turn]));
         if (tid == 0) p.scale[row * p.lds] = scale;
         const float inv = 1.f / scale;
 #pragma unroll
@@ -335,7 +436,25 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormParams p) {
             if (col0 < p.d) store_e4m3(p.q + row * p.ldq, col0, p.d, p.wide, v[k]);
         }
     }
-    if (OUT == kGroupScale) {
+    if (OUT == kGroupScale && shift == 0) {
+        // a group is sixteen lanes' chunks
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int col0 = 8 * (tid + k * threads);
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[k][i]) & 0x7fffffffu);
+#pragma unroll
+            for (int i = 8; i > 0; i >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, i));
+            const float scale = scale_of(top), inv = 1.f / scale;
+            if (col0 >= p.d) continue;
+            if ((tid & 15) == 0) p.scale[row * p.lds + col0 / kScaleGroup] = scale;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[k][i] *= inv;
+            store_e4m3(p.q + row * p.ldq, col0, p.d, p.wide, v[k]);
+        }
+        __syncwarp();
+    } else if (OUT == kGroupScale) {
         // A chunk lies in one group of columns, or in two where the row is shifted: each is
         // joined into the groups' maxima in shared memory (the order does not matter to a maximum).
         const int groups = (p.d + kScaleGroup - 1) / kScaleGroup;
@@ -372,6 +491,9 @@ __global__ void __launch_bounds__(512, 1) norm_kernel(const NormParams p) {
             for (int i = 0; i < 8; ++i) v[k][i] *= col0 + i < cut ? ia : ib;
             store_e4m3(p.q + row * p.ldq, col0, p.d, p.wide, v[k]);
         }
+        if (blockDim.y > 1) __syncwarp();
+        else __syncthreads();  // (the next row clears the maxima)
+    }
     }
 }
 
@@ -389,7 +511,6 @@ struct NormBwdParams {
     int64_t lddy, ldh, lddh, lddr, lddx;
     int m, d;
     int wide, wide_weight;
-    int per_thread;       // chunks a thread, where they are not a constant of the kernel
     Drop drop;
 };
 
@@ -398,117 +519,92 @@ struct NormBwdParams {
 // A block takes the rows row0, row0 + stride, ...: `stride` is a multiple of 8 rows, so a
 // thread's rows all have the same shift and it owns the same columns in each; the weight's
 // gradient stays in its registers until the end.
-// V chunks a thread, in registers; V = 0: p.per_thread chunks, in places of the thread's own in
-// shared memory (four chunks' rows and sums do not fit its registers).
-template <int V, bool DROP>
-__global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdParams p) {
-    constexpr bool kShared = V == 0;
-    constexpr int kHeld = kShared ? 1 : V;
+// V chunks a thread.  The rows come through shared memory as the forward pass's do, in two stages.
+// Dynamic shared memory: the rows [stage][dY, H or dH][chunk][thread], then the weight.
+constexpr int kBwdStages = 2;
+
+template <int V, int DROP>
+__global__ void __maxnreg__(V == 4 ? 128 : 80) norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
     __shared__ float sums[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
     const int row0 = blockIdx.x * blockDim.y + threadIdx.y, stride = gridDim.x * blockDim.y;
     const int shift = p.wide ? row_shift(p.dy + row0 * p.lddy) : 0;
-    const int tid = threadIdx.x, threads = blockDim.x;
-    const int held = kShared ? p.per_thread : V;
-    Key key{};
-    if (DROP) key = drop_key(p.drop);
-    float dw[kHeld][8];
-    uint4 dyu[kHeld], hu[kHeld], wu[kHeld];
-    // kShared: chunk k of thread t has the words 4k .. 4k + 3, `threads` apart: dY, H and the sums
-    uint4* own = reinterpret_cast<uint4*>(smem) + tid;
+    const int tid = threadIdx.x, threads = blockDim.x, all = blockDim.x * blockDim.y;
+    uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.y * threads + tid;
+    uint4* weight = slots + kBwdStages * 3 * V * all;  // (the thread's own part of it)
+    const Draw<DROP> draw(p.drop);
+    auto slot = [&](int stage, int matrix, int k) { return slots + ((stage * 3 + matrix) * V + k) * all; };
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < p.m) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        wu[k] = load_chunk(p.weight, 8 * (tid + k * threads) - shift, p.d, shift == 0 && p.wide_weight);
+            for (int k = 0; k < V; ++k) {
+                const int col0 = 8 * (tid + k * threads) - shift;
+                fetch_chunk(slot(stage, 0, k), p.dy + row * p.lddy, col0, p.d, p.wide, row > 0 && p.lddy >= 8);
+                fetch_chunk(slot(stage, 1, k), p.h + row * p.ldh, col0, p.d, p.wide, row > 0 && p.ldh >= 8);
+                if (p.dh) fetch_chunk(slot(stage, 2, k), p.dh + row * p.lddh, col0, p.d, p.wide, row > 0 && p.lddh >= 8);
+            }
+        }
+        fetch_commit();
+    };
+    fetch(row0, 0);
+    float dw[V][8];
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+        weight[k * all] = load_chunk(p.weight, 8 * (tid + k * threads) - shift, p.d, shift == 0 && p.wide_weight);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[k][i] = 0.f;
     }
-    if (kShared)
-        for (int k = 0; k < held; ++k) own[(4 * k + 2) * threads] = own[(4 * k + 3) * threads] = make_uint4(0, 0, 0, 0);
 
-    int turn = 0;
+    int turn = 0;  // of the stages and of row_sum's places
     for (int64_t r = row0; r < p.m; r += stride, turn ^= 1) {
         const int row = static_cast<int>(r);
         const float rstd = p.rstd[row];
+        fetch(r + stride, turn ^ 1);
+        fetch_wait<1>();
         float sum = 0.f;
-        if (!kShared) {
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) {
-                const int col0 = 8 * (tid + k * threads) - shift;
-                dyu[k] = load_chunk(p.dy + row * p.lddy, col0, p.d, p.wide);
-                hu[k] = load_chunk(p.h + row * p.ldh, col0, p.d, p.wide);
-            }
-        }
-#pragma unroll kHeld
-        for (int k = 0; k < held; ++k) {
-            const int col0 = 8 * (tid + k * threads) - shift, at = kShared ? 0 : k;
-            if (kShared) {
-                own[4 * k * threads] = dyu[0] = load_chunk(p.dy + row * p.lddy, col0, p.d, p.wide);
-                own[(4 * k + 1) * threads] = hu[0] = load_chunk(p.h + row * p.ldh, col0, p.d, p.wide);
-                wu[0] = load_chunk(p.weight, col0, p.d, shift == 0 && p.wide_weight);
-            }
+        for (int k = 0; k < V; ++k) {
+            const int col0 = 8 * (tid + k * threads) - shift;
             float t[8], h[8], w[8];
-            unpack(dyu[at], t);
-            unpack(hu[at], h);
-            unpack(wu[at], w);
+            unpack(read_chunk(slot(turn, 0, k), col0), t);
+            unpack(read_chunk(slot(turn, 1, k), col0), h);
+            unpack(weight[k * all], w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 t[i] *= h[i] * rstd;
                 sum = fmaf(t[i], w[i], sum);
-            }
-            if (kShared) {
-                float4* acc = reinterpret_cast<float4*>(own) + (4 * k + 2) * threads;
-                const float4 a = acc[0], b = acc[threads];
-                acc[0] = make_float4(a.x + t[0], a.y + t[1], a.z + t[2], a.w + t[3]);
-                acc[threads] = make_float4(b.x + t[4], b.y + t[5], b.z + t[6], b.w + t[7]);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) dw[at][i] += t[i];
+                dw[k][i] += t[i];
             }
         }
         const float mean = row_sum(sum, sums[turn]) / static_cast<float>(p.d);
-#pragma unroll kHeld
-        for (int k = 0; k < held; ++k) {
-            const int col0 = 8 * (tid + k * threads) - shift, at = kShared ? 0 : k;
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int col0 = 8 * (tid + k * threads) - shift;
             if (col0 >= p.d) continue;
-            // (one chunk after the other: the generators of several do not fit the registers)
-            if (V > 1) asm volatile("" : "+r"(key.k0) : : "memory");
-            if (kShared) {
-                dyu[0] = own[4 * k * threads];
-                hu[0] = own[(4 * k + 1) * threads];
-                wu[0] = load_chunk(p.weight, col0, p.d, shift == 0 && p.wide_weight);
-            }
             float v[8], h[8], w[8];
-            unpack(dyu[at], v);
-            unpack(hu[at], h);
-            unpack(wu[at], w);
+            unpack(read_chunk(slot(turn, 0, k), col0), v);
+            unpack(read_chunk(slot(turn, 1, k), col0), h);
+            unpack(weight[k * all], w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = rstd * (v[i] * w[i] - h[i] * rstd * mean);
             if (p.dh) {
-                unpack(load_chunk(p.dh + row * p.lddh, col0, p.d, p.wide), h);
+                unpack(read_chunk(slot(turn, 2, k), col0), h);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] += h[i];
             }
             store_chunk(p.dr + row * p.lddr, col0, p.d, p.wide, pack(v));
             if (DROP) {
-                drop_chunk(v, row, col0, p.drop, key);
+                draw.template chunk<true>(v, row, col0);
                 store_chunk(p.dx + row * p.lddx, col0, p.d, p.wide, pack(v));
             }
         }
     }
+    fetch_wait<0>();
 
     float* part = p.partial + static_cast<int64_t>(blockIdx.x) * p.d;
-    if (kShared) {
-        for (int k = 0; k < held; ++k)
-            for (int i = 0; i < 8; ++i) {
-                const int col = 8 * (tid + k * threads) - shift + i;
-                const float* acc = reinterpret_cast<const float*>(own + (4 * k + 2 + i / 4) * threads);
-                if (col >= 0 && col < p.d) part[col] = acc[i & 3];
-            }
-        return;
-    }
     if (blockDim.y == 1) {
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k)
+        for (int k = 0; k < V; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int col = 8 * (tid + k * threads) - shift + i;
@@ -516,14 +612,15 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdParams p)
             }
         return;
     }
-    // several rows a block: the warps add theirs one after the other
+    // several rows a block: the warps add theirs one after the other, where the rows were
+    __syncthreads();
     float* total = reinterpret_cast<float*>(smem);
     for (int c = threadIdx.y * 32 + tid; c < p.d; c += 32 * blockDim.y) total[c] = 0.f;
     for (int w = 0; w < static_cast<int>(blockDim.y); ++w) {
         __syncthreads();
         if (w != static_cast<int>(threadIdx.y)) continue;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k)
+        for (int k = 0; k < V; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int col = 8 * (tid + k * threads) - shift + i;

@@ -270,7 +270,7 @@ GB_API gb_status_t gb_gemm_ffn_gated_w4(const void* X, int64_t ldx, int x_type, 
  *
  *   D[m,n] = bf16( keep[m,n] X[m,n] / (1 - p) + R[m,n] )
  *
- * keep[m,n] = (word >= round(p 2^32)), where word is number n % 4 of the four 32-bit words of
+ * keep[m,n] = (word >= round(p 2^32), at least 1 if p > 0), where word is number n % 4 of the four 32-bit words of
  * Philox4x32 with ten rounds (Salmon et al., SC 2011) under the key `seed` (low word first) at
  * the counter (n / 4, m, offset low, offset high).  The mask depends on nothing else, so it is
  * never stored: the gradient of X is the same call on the gradient of D, without R.  Give each
