@@ -134,8 +134,14 @@ def _mat(t: torch.Tensor | None, name: str, rows: int | None = None, cols: int |
     return t.data_ptr(), max(ld, 1)
 
 
+# the current stream's handle without a Stream object around it (3 us of a small call's time)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -327,5 +333,6 @@ def version() -> str:
     return lib().gb_version().decode()
 
 
+from . import block  # noqa: E402
 from .block import (add_rms_norm, add_rms_norm_backward, add_rms_norm_backward_workspace_bytes,  # noqa: E402
                     add_rms_norm_q8, dropout, ffn_gated_w4, linear_w4)

@@ -1,4 +1,5 @@
-"""Compile the CUDA library (libgbgemm.so) in-tree for sm_103a with nvcc."""
+"""Compile the CUDA library (libgbgemm.so) in-tree for sm_103a with nvcc, and the torch binding of the
+operators around the products (_gbgemm_torch.so) with the host compiler."""
 from __future__ import annotations
 
 import os
@@ -8,6 +9,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgbgemm.so")
+BINDING = os.path.join(PKG, "_gbgemm_torch.so")
 LOG_DIR = os.path.join(PKG, "_build")
 SOURCES = ["gbgemm.cu", "rowwise.cu", "w4.cu"]
 HEADERS = ["gemm_kernel.cuh", "host.h", "ptx.cuh", "probe.cuh", "rowwise.cuh", "w4_kernel.cuh"]
@@ -23,11 +25,11 @@ def _nvcc() -> str:
     return "nvcc"
 
 
-def _stale(lib: str = LIB) -> bool:
+def _stale(lib: str = LIB, files=tuple(SOURCES + HEADERS)) -> bool:
     if not os.path.exists(lib):
         return True
     t = os.path.getmtime(lib)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "gbgemm.h")]
+    deps = [os.path.join(CSRC, f) for f in files] + [os.path.join(ROOT, "include", "gbgemm.h")]
     return any(os.path.getmtime(d) > t for d in deps)
 
 
@@ -100,5 +102,35 @@ def build(force: bool = False, verbose: bool = False, trace: bool = False) -> st
     return out
 
 
+def _binding_command(out: str) -> list:
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    include = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"]]
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[flag for path in include for flag in ("-isystem", path)], os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L" + lib, "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
+def build_binding(force: bool = False) -> str:
+    """Build _gbgemm_torch.so, the operators' binding to torch (argument marshalling only)."""
+    if not force and not _stale(BINDING, ("binding.cpp",)):
+        return BINDING
+    tmp = BINDING + f".tmp{os.getpid()}"
+    try:
+        res = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"the torch binding did not compile ({res.returncode}):\n{res.stderr[-4000:]}")
+        os.replace(tmp, BINDING)
+    finally:
+        if os.path.exists(tmp):
+            os.remove(tmp)
+    return BINDING
+
+
 if __name__ == "__main__":
     print(build(force=True, verbose=True))
+    print(build_binding(force=True))

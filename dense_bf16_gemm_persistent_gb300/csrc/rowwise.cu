@@ -154,7 +154,7 @@ gb_status_t launch_norm(const NormParams& p, const RowPlan& pl, int dev, const D
     static std::atomic<bool> ready[64];
     gb_status_t st = allow_smem(norm_kernel<V, DROP, OUT>, ready, dev, info.smem_optin - 1024);
     if (st != GB_OK) return st;
-    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : 1024, info.sms);
+    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : DROP ? 768 : 1024, info.sms);
     size_t smem = static_cast<size_t>(kRowStages * 2 + 1) * V * 16 * pl.threads * pl.rows;
     if (OUT == kGroupScale) smem += static_cast<size_t>(pl.rows) * ceil_div(p.d, kScaleGroup) * 4;
     norm_kernel<V, DROP, OUT><<<static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream>>>(p);

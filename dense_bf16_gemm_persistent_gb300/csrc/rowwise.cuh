@@ -223,7 +223,7 @@ constexpr int kDropoutThreads = 256, kDropoutBatch = 2;
 // Threads walk the matrix's chunks a grid's width apart, kDropoutBatch at a time; a step of the
 // walk is `step_rows` rows and `step_chunks` chunks, so that no thread divides again.
 template <int DROP>
-__global__ void __launch_bounds__(kDropoutThreads) dropout_kernel(const __grid_constant__ DropoutParams p) {
+__global__ void __launch_bounds__(kDropoutThreads, 5) dropout_kernel(const __grid_constant__ DropoutParams p) {
     const Draw<DROP> draw(p.drop);
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kDropoutThreads + threadIdx.x;
     int64_t row = at / p.chunks;
@@ -355,7 +355,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int col0, int cols, boo
 constexpr int kRowStages = 3;
 
 template <int V, int DROP, int OUT>
-__global__ void __launch_bounds__(512, V == 4 ? 1 : 2) norm_kernel(const __grid_constant__ NormParams p) {
+__global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) norm_kernel(const __grid_constant__ NormParams p) {
     __shared__ float sums[2][32];
     __shared__ uint32_t maxima[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(512, V == 4 ? 1 : 2) norm_kernel(const __grid_
     for (int k = 0; k < V; ++k) {
         const int col0 = 8 * (tid + k * threads) - shift;
         unpack(read_chunk(slots + (stage * 2 * V + k) * all, col0), v[k]);
-        if (DROP) draw.template chunk<true>(v[k], row, col0);
+        if (DROP) draw.template chunk<false>(v[k], row, col0);
         if (p.r) {
             float r[8];
             unpack(read_chunk(slots + ((stage * 2 + 1) * V + k) * all, col0), r);

@@ -121,7 +121,7 @@ gb_status_t launch(const Params& prm, const Plan& pl, int dev, const DeviceInfo&
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = pl.cluster > 1 ? 1 : 0;
     e = cudaLaunchKernelEx(&cfg, kern, prm);
     if (e != cudaSuccess) return cuda_fail(e, "w4 kernel launch");
     note_plan("kernel=w4 group=%lld tokens=%lld cluster=%lld warps=%lld k_warps=%lld clusters=%lld", G, pl.tokens, pl.cluster,
@@ -203,9 +203,9 @@ gb_status_t clusters_at_once(int cluster, int dev, const DeviceInfo& info, int* 
 // of an SM's warps together `unit`, each round's join 1.1, or 1.4 over more than two CTAs, and
 // x's layout 0.45 for each chunk of a thread, half of that where no largest value is looked for.
 // (A round: every team takes one row tile.  Passes of tokens run side by side.)
-gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInfo& info, Plan* out) {
+gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInfo& info, const W4Override& want,
+                      Plan* out) {
     const int units = std::max(1, static_cast<int>(ceil_div(pr.k, kUnit)));
-    const W4Override want = w4_override();
     double best = 0.0;
     int tokens = static_cast<int>(std::min<int64_t>(pr.m, gb::w4::kMaxTokens));
     for (bool last = false; !last; tokens = (tokens + 1) / 2) {
@@ -256,8 +256,25 @@ gb_status_t run(const Problem& pr, void* stream) {
 
     const int out_rows = pr.gated ? kRows / 2 : kRows;
     const int64_t tiles = ceil_div(pr.n, out_rows);
+    // (the last plans of the thread, by what a plan depends on: making one takes microseconds)
+    struct Known {
+        int64_t m = -1, n, k;
+        int group, x_type, gated, dev, cluster, k_warps;
+        Plan plan;
+    };
+    static thread_local Known known[8];
+    static thread_local int turn = 0;
+    const W4Override want = w4_override();
     Plan pl{};
-    if ((st = make_plan(pr, tiles, dev, info, &pl)) != GB_OK) return st;
+    for (const Known& e : known)
+        if (e.m == pr.m && e.n == pr.n && e.k == pr.k && e.group == pr.group && e.x_type == pr.x_type &&
+            e.gated == pr.gated && e.dev == dev && e.cluster == want.cluster && e.k_warps == want.k_warps)
+            pl = e.plan;
+    if (pl.warps == 0) {
+        if ((st = make_plan(pr, tiles, dev, info, want, &pl)) != GB_OK) return st;
+        known[turn] = Known{pr.m, pr.n, pr.k, pr.group, pr.x_type, pr.gated, dev, want.cluster, want.k_warps, pl};
+        turn = (turn + 1) % 8;
+    }
 
     Params prm;
     memset(&prm, 0, sizeof prm);
