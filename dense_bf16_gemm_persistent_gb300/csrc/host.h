@@ -40,6 +40,34 @@ W4Override w4_override();
 // What gb_last_plan() reports: a static format that takes six %lld.
 void note_plan(const char* fmt, long long a, long long b, long long c, long long d, long long e, long long f);
 
+// A launch whose CTAs may be set up while the kernel before it in the stream still runs: the kernel
+// must wait (ptx.cuh: wait_for_earlier_kernels) before it touches global memory.
+struct Launch {
+    cudaLaunchConfig_t config = {};
+    cudaLaunchAttribute attributes[2];
+
+    Launch(dim3 grid, dim3 block, size_t smem, cudaStream_t stream, int cluster = 1) {
+        config.gridDim = grid;
+        config.blockDim = block;
+        config.dynamicSmemBytes = smem;
+        config.stream = stream;
+        config.attrs = attributes;
+        config.numAttrs = cluster > 1 ? 2 : 1;
+        attributes[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attributes[0].val.programmaticStreamSerializationAllowed = 1;
+        attributes[1].id = cudaLaunchAttributeClusterDimension;
+        attributes[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attributes[1].val.clusterDim.y = 1;
+        attributes[1].val.clusterDim.z = 1;
+    }
+
+    template <class Kernel, class... Args>
+    gb_status_t operator()(const char* what, Kernel kernel, Args... args) {
+        const cudaError_t e = cudaLaunchKernelEx(&config, kernel, args...);
+        return e == cudaSuccess ? GB_OK : cuda_fail(e, what);
+    }
+};
+
 inline bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

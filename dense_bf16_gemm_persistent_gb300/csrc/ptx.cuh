@@ -502,6 +502,16 @@ __device__ __forceinline__ void setmaxnreg_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ---------------------------------------------------------------- dependent launches
+
+// Wait until the kernels before this one in the stream have finished and their writes are visible;
+// to come before the first access to global memory of a kernel launched early (host.h: Launch).
+__device__ __forceinline__ void wait_for_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Let the next kernel of the stream be launched once every CTA has come here: it waits, in turn, for
+// this one to finish.
+__device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- misc
 
 __device__ __forceinline__ void named_barrier_sync(uint32_t id, uint32_t nthreads) {

@@ -126,11 +126,6 @@ RowPlan plan_rows(const Mat (&mats)[N], int64_t rows, int64_t cols) {
     return pl;
 }
 
-gb_status_t launched(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? GB_OK : cuda_fail(e, what);
-}
-
 // More than the default 48 KB of dynamic shared memory, once for each kernel and device.  (Two
 // threads may both set the attribute: to the same value.)
 template <class Kernel>
@@ -157,10 +152,10 @@ gb_status_t launch_norm(const NormParams& p, const RowPlan& pl, int dev, const D
     const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : DROP ? 768 : 1024, info.sms);
     size_t smem = static_cast<size_t>(kRowStages * 2 + 1) * V * 16 * pl.threads * pl.rows;
     if (OUT == kGroupScale) smem += static_cast<size_t>(pl.rows) * ceil_div(p.d, kScaleGroup) * 4;
-    norm_kernel<V, DROP, OUT><<<static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream>>>(p);
     note_plan("kernel=add_rms_norm output=%lld dropout=%lld threads=%lld rows=%lld blocks=%lld wide=%lld", OUT, DROP,
               pl.threads, pl.rows, blocks, pl.wide);
-    return launched("add_rms_norm launch");
+    return Launch(static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream)(
+        "add_rms_norm launch", norm_kernel<V, DROP, OUT>, p);
 }
 
 template <int DROP, int OUT>
@@ -178,8 +173,8 @@ gb_status_t launch_bwd(const NormBwdParams& p, const RowPlan& pl, int blocks, in
     // two stages of three matrices, and the weight; and the join of a block's rows
     size_t smem = static_cast<size_t>(kBwdStages * 3 + 1) * V * 16 * pl.threads * pl.rows;
     if (pl.rows > 1) smem = std::max(smem, static_cast<size_t>(p.d) * 4);
-    norm_bwd_kernel<V, DROP><<<blocks, dim3(pl.threads, pl.rows), smem, stream>>>(p);
-    return launched("add_rms_norm_backward launch");
+    return Launch(blocks, dim3(pl.threads, pl.rows), smem, stream)("add_rms_norm_backward launch",
+                                                                   norm_bwd_kernel<V, DROP>, p);
 }
 
 template <int DROP>
@@ -233,14 +228,11 @@ gb_status_t gb_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, d
     prm.step_rows = blocks * kDropoutThreads / prm.chunks;
     prm.step_chunks = static_cast<int>(blocks * kDropoutThreads % prm.chunks);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    switch (drop_kind(p, rng_state)) {
-        case kNoDrop: dropout_kernel<kNoDrop><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, s>>>(prm); break;
-        case kKeys: dropout_kernel<kKeys><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, s>>>(prm); break;
-        default: dropout_kernel<kState><<<static_cast<unsigned>(blocks), kDropoutThreads, 0, s>>>(prm); break;
-    }
     note_plan("kernel=dropout blocks=%lld threads=%lld chunks=%lld wide=%lld residual=%lld state=%lld", blocks,
               kDropoutThreads, prm.chunks, prm.wide, R != nullptr, rng_state != nullptr);
-    return launched("dropout launch");
+    const int kind = drop_kind(p, rng_state);
+    const auto kernel = kind == kNoDrop ? dropout_kernel<kNoDrop> : kind == kKeys ? dropout_kernel<kKeys> : dropout_kernel<kState>;
+    return Launch(static_cast<unsigned>(blocks), kDropoutThreads, 0, s)("dropout launch", kernel, prm);
 }
 
 gb_status_t gb_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight, double eps,
@@ -406,9 +398,9 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
         note_plan("kernel=add_rms_norm_backward blocks=%lld dropout=%lld threads=%lld rows=%lld chunks=%lld wide=%lld",
                   blocks, drop, pl.threads, pl.rows, pl.chunks_per_thread, pl.wide);
     }
-    join_kernel<<<static_cast<unsigned>(ceil_div(D, kJoinColumns)), dim3(kJoinColumns, kJoinParts), 0, s>>>(
-        static_cast<const float*>(workspace), blocks, static_cast<int>(D), dweight);
-    return launched("add_rms_norm_backward join launch");
+    return Launch(static_cast<unsigned>(ceil_div(D, kJoinColumns)), dim3(kJoinColumns, kJoinParts), 0, s)(
+        "add_rms_norm_backward join launch", join_kernel, static_cast<const float*>(workspace), blocks, static_cast<int>(D),
+        dweight);
 }
 
 }  // extern "C"

@@ -17,6 +17,8 @@
 
 #include <cstdint>
 
+#include "ptx.cuh"
+
 namespace gb {
 namespace rowwise {
 
@@ -224,6 +226,8 @@ constexpr int kDropoutThreads = 256, kDropoutBatch = 2;
 // walk is `step_rows` rows and `step_chunks` chunks, so that no thread divides again.
 template <int DROP>
 __global__ void __launch_bounds__(kDropoutThreads, 5) dropout_kernel(const __grid_constant__ DropoutParams p) {
+    allow_next_kernel();
+    wait_for_earlier_kernels();
     const Draw<DROP> draw(p.drop);
     const int64_t at = static_cast<int64_t>(blockIdx.x) * kDropoutThreads + threadIdx.x;
     int64_t row = at / p.chunks;
@@ -356,6 +360,8 @@ constexpr int kRowStages = 3;
 
 template <int V, int DROP, int OUT>
 __global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) norm_kernel(const __grid_constant__ NormParams p) {
+    allow_next_kernel();
+    wait_for_earlier_kernels();
     __shared__ float sums[2][32];
     __shared__ uint32_t maxima[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
@@ -525,6 +531,8 @@ constexpr int kBwdStages = 2;
 
 template <int V, int DROP>
 __global__ void __maxnreg__(V == 4 ? 128 : 80) norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
+    allow_next_kernel();
+    wait_for_earlier_kernels();
     __shared__ float sums[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
     const int row0 = blockIdx.x * blockDim.y + threadIdx.y, stride = gridDim.x * blockDim.y;
@@ -635,6 +643,8 @@ __global__ void __maxnreg__(V == 4 ? 128 : 80) norm_bwd_kernel(const __grid_cons
 constexpr int kJoinColumns = 32, kJoinParts = 16;
 __global__ void __launch_bounds__(kJoinColumns * kJoinParts) join_kernel(const float* partial, int parts, int d,
                                                                          float* dweight) {
+    allow_next_kernel();
+    wait_for_earlier_kernels();
     __shared__ float sum[kJoinParts][kJoinColumns];
     const int c = blockIdx.x * kJoinColumns + threadIdx.x;
     float v = 0.f;

@@ -110,20 +110,9 @@ gb_status_t launch(const Params& prm, const Plan& pl, int dev, const DeviceInfo&
     }
     const int64_t groups = ceil_div(prm.tiles, pl.warps / pl.k_warps);
     const int64_t clusters = std::min<int64_t>(groups, pl.clusters);
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(static_cast<unsigned>(clusters * pl.cluster), static_cast<unsigned>(ceil_div(prm.m, pl.tokens)), 1);
-    cfg.blockDim = dim3(32 * pl.warps, 1, 1);
-    cfg.dynamicSmemBytes = pl.smem;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = pl.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = pl.cluster > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, kern, prm);
-    if (e != cudaSuccess) return cuda_fail(e, "w4 kernel launch");
+    const dim3 grid(static_cast<unsigned>(clusters * pl.cluster), static_cast<unsigned>(ceil_div(prm.m, pl.tokens)));
+    const gb_status_t st = Launch(grid, 32 * pl.warps, pl.smem, stream, pl.cluster)("w4 kernel launch", kern, prm);
+    if (st != GB_OK) return st;
     note_plan("kernel=w4 group=%lld tokens=%lld cluster=%lld warps=%lld k_warps=%lld clusters=%lld", G, pl.tokens, pl.cluster,
               pl.warps, pl.k_warps, clusters);
     return GB_OK;

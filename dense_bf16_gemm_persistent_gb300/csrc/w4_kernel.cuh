@@ -379,6 +379,8 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
     uint32_t ranks;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
     if (ranks > 1) cluster_arrive();  // (waited for before the first store to another CTA)
+    allow_next_kernel();
+    wait_for_earlier_kernels();
     const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
     const int token0 = blockIdx.y * p.tokens, tokens = min(p.tokens, p.m - token0);
     const int unit0 = rank * p.slice_units;
