@@ -200,8 +200,8 @@ gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInf
     for (bool last = false; !last; tokens = (tokens + 1) / 2) {
         const int nt = tiles_of(tokens), warps = gb::w4::warps_of(pr.group, nt);
         const int64_t passes = ceil_div(pr.m, tokens);
-        const double unit = nt == 1 ? (pr.group == 128 ? 1.15 : pr.group == 64 ? 1.25 : 1.5)
-                                    : (pr.group == 128 ? 1.7 : pr.group == 64 ? 1.55 : 1.8);
+        const double unit = nt == 1 ? (pr.group == 128 ? 1.5 : pr.group == 64 ? 1.6 : 1.9)
+                                    : (pr.group == 128 ? 1.85 : pr.group == 64 ? 1.7 : 2.0);
         for (int cluster = 1; cluster <= 8 && (cluster <= units || want.cluster); cluster *= 2) {
             if (want.cluster && cluster != want.cluster) continue;
             const int slice = static_cast<int>(ceil_div(units, cluster));

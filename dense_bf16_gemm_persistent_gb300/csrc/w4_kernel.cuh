@@ -328,6 +328,23 @@ __device__ __forceinline__ void sum_x(const uint4* xs, float* xsum, int groups, 
     }
 }
 
+// What a token's infinities and NaN add to row n of matrix `from`: those of `units` units of columns,
+// the first at `first` and the others `step` apart.
+template <int G>
+__device__ __noinline__ float odd_part(const Params& p, int from, int64_t n, int64_t token, int first, int units, int step) {
+    float sum = 0.f;
+    for (int i = 0; i < units; ++i, first += step)
+        for (int col = first; col < min(first + kUnit, p.k); ++col) {
+            const uint32_t x = static_cast<const uint16_t*>(p.x)[token * p.ldx + col];
+            if ((x >> 7 & 0xff) != 0xff) continue;
+            const int q = p.q[from][n * p.ldq[from] + col / 2] >> (4 * (col & 1)) & 15;
+            const int z = p.z[from] ? p.z[from][n * p.ldz[from] + col / G] : 8;
+            const float s = __uint_as_float(static_cast<uint32_t>(p.s[from][n * p.lds[from] + col / G]) << 16);
+            sum += __uint_as_float(x << 16) * (static_cast<float>(q - z) * s);
+        }
+    return sum;
+}
+
 // A warp's place in its sequence of (row tile, unit), and the addresses that go with it.
 template <bool GATED>
 struct Cursor {
@@ -564,22 +581,6 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
         }
         __syncwarp();
     };
-    // What a token's infinities and NaN in the warp's units add to row n of matrix `from`.
-    auto odd_part = [&](int from, int64_t n, int token) {
-        float sum = 0.f;
-        for (int i = 0; i < mine; ++i) {
-            const int first = col_base + (k_part + i * k_warps) * kUnit;
-            for (int col = first; col < min(first + kUnit, p.k); ++col) {
-                const uint32_t x = static_cast<const uint16_t*>(p.x)[(token0 + token) * p.ldx + col];
-                if ((x >> 7 & 0xff) != 0xff) continue;
-                const int q = p.q[from][n * p.ldq[from] + col / 2] >> (4 * (col & 1)) & 15;
-                const int z = p.z[from] ? p.z[from][n * p.ldz[from] + col / G] : 8;
-                const float s = __uint_as_float(static_cast<uint32_t>(p.s[from][n * p.lds[from] + col / G]) << 16);
-                sum += __uint_as_float(x << 16) * (static_cast<float>(q - z) * s);
-            }
-        }
-        return sum;
-    };
     auto leave = [&](int tile, const float (&total)[2][NT][4], uint32_t buffer) {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
@@ -598,7 +599,9 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
                     if (!kGroupX) v *= load_shared_float(scales_lane - t * 8 + 4 * token);
                     if (X == kXBf16 && odd) {
                         const int64_t n = static_cast<int64_t>(tile) * kOutRows + (GATED ? kind * 8 : r * 8) + g;
-                        if (n < p.n) v += odd_part(GATED ? r >> 1 : 0, n, token);
+                        if (n < p.n)
+                            v += odd_part<G>(p, GATED ? r >> 1 : 0, n, token0 + token, col_base + k_part * kUnit, mine,
+                                             k_warps * kUnit);
                     }
                     store_cluster(mapa_shared(at, owner0 + (token & ((1 << token_bits) - 1))), v);
                 }
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
                 }
 #pragma unroll
                 for (int j = 0; j < kStepGroups; ++j) {
-                    const uint32_t (&ws)[4][kPer] = w[s * kStepGroups + j];
+                    const uint32_t (&ws)[4][kPer] = w[j];
                     float acc[2][NT][4];
                     uint32_t row_sz[4], zero[4];  // of rows g, g + 8, g + 16, g + 24
                     load_shared(scales_of_warp + (s * kStepGroups + j) * 128 + g * 16, row_sz[0], row_sz[1], row_sz[2],
@@ -725,8 +728,17 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
                 scale_at += NT * 32;
                 sums_at += kStepGroups * NT * 32;
             };
+            // (rolled where it fits the registers: fewer instructions to fetch)
+#pragma unroll(G == 32 ? 2 : 1)
+            for (int s = 0; s < kUnit / kStep; ++s) {
+                multiply(s);
 #pragma unroll
-            for (int s = 0; s < kUnit / kStep; ++s) multiply(s);
+                for (int f = 0; f + kStepGroups < kGroups; ++f)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int c = 0; c < kPer; ++c) w[f][r][c] = w[f + kStepGroups][r][c];
+            }
         }
 
         if (before >= 0) {
