@@ -397,7 +397,6 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
     if (ranks > 1) cluster_arrive();  // (waited for before the first store to another CTA)
     allow_next_kernel();
-    wait_for_earlier_kernels();
     const int cluster = blockIdx.x / ranks, clusters = gridDim.x / ranks;
     const int token0 = blockIdx.y * p.tokens, tokens = min(p.tokens, p.m - token0);
     const int unit0 = rank * p.slice_units;
@@ -502,6 +501,16 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
     Cursor<GATED> ahead;  // the unit whose copies are started next
     ahead.at_tile(p, cluster * teams + team, lane);
     ahead.unit = k_part;
+    // While the kernels before still run: the first unit's rows (one a lane) to L2, where a later
+    // write of theirs would be seen all the same.
+    if (mine > 0 && ahead.tile < p.tiles) {
+        const int64_t first = static_cast<int64_t>(ahead.tile) * kOutRows;
+        const int64_t row = min(first + (GATED ? lane & 15 : lane), static_cast<int64_t>(p.n - 1));
+        const int from = lane >> 4;
+        const uint8_t* line = p.q[from] + row * p.ldq[from] + (col_base + k_part * kUnit) / 2;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+    }
+    wait_for_earlier_kernels();
     auto start_next = [&] {
         if (ahead.tile < p.tiles) {
             fetch(ahead);
