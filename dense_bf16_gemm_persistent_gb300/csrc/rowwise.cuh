@@ -602,7 +602,7 @@ __global__ void __maxnreg__(V == 4 ? 128 : 80) norm_bwd_kernel(const __grid_cons
             }
             store_chunk(p.dr + row * p.lddr, col0, p.d, p.wide, pack(v));
             if (DROP) {
-                draw.template chunk<true>(v, row, col0);
+                draw.template chunk<false>(v, row, col0);
                 store_chunk(p.dx + row * p.lddx, col0, p.d, p.wide, pack(v));
             }
         }
