@@ -15,8 +15,9 @@
 // q 2^-20 for the nibble one higher; five instructions widen eight weights.  The zero point is
 // taken off the group's sum instead of off each weight,
 //     sum (q - z) x = sum q x - z sum x,
-// with sum x from the same instructions in the same order, so that weights equal to a zero point
-// that is a power of two (8 without zeros) leave exactly nothing.  x becomes fp16 too: e4m3 values
+// with sum x from the same instructions in the same order on weights of 8, so that weights at the
+// zero point 8 (all there is without zeros) leave exactly nothing; weights at another zero point leave
+// 2^-24 of z s sum |x| (measured).  x becomes fp16 too: e4m3 values
 // are fp16 values as they are, and a token's bf16 values are first scaled by a power of two, so that
 // the largest (of the CTA's columns) is in [2^14, 2^15); what is then lost, below 2^-39 of the
 // largest, is under fp32's own rounding of the sum.  Products are summed in fp32 within a group, and the
@@ -298,8 +299,8 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
     return finite;
 }
 
-// Sums of x over a group, in `xsum` [group][token of NT eights]: the group's products with weights of q = 1, by the
-// instructions and in the order of the products with the weights.
+// Sums of x over a group, in `xsum` [group][token of NT eights]: an eighth of the group's products
+// with weights of q = 8, by the instructions and in the order of the products with the weights.
 template <int G, int NT>
 __device__ __forceinline__ void sum_x(const uint4* xs, float* xsum, int groups, int tokens) {
     constexpr int kPer = G / 32, kStepGroups = kStep / G;
@@ -313,16 +314,16 @@ __device__ __forceinline__ void sum_x(const uint4* xs, float* xsum, int groups, 
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const uint4 x = xs[((chunk + c) * tokens + min(g + 8 * j, tokens - 1)) * 4 + t];
-                const uint32_t one = 0x00010001u, one16 = 0x00100010u;
-                if (c == 0) mma16816_first(acc[j], one, one, one16, one16, x.x, x.y);
-                else mma16816(acc[j], one, one, one16, one16, x.x, x.y);
-                mma16816(acc[j], one, one, one16, one16, x.z, x.w);
+                const uint32_t eight = 0x00080008u, eight16 = 0x00800080u;
+                if (c == 0) mma16816_first(acc[j], eight, eight, eight16, eight16, x.x, x.y);
+                else mma16816(acc[j], eight, eight, eight16, eight16, x.x, x.y);
+                mma16816(acc[j], eight, eight, eight16, eight16, x.z, x.w);
             }
         if (g == 0) {
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                xsum[i * 8 * NT + 8 * j + 2 * t] = acc[j][0];
-                xsum[i * 8 * NT + 8 * j + 2 * t + 1] = acc[j][1];
+                xsum[i * 8 * NT + 8 * j + 2 * t] = acc[j][0] * 0.125f;
+                xsum[i * 8 * NT + 8 * j + 2 * t + 1] = acc[j][1] * 0.125f;
             }
         }
     }

@@ -501,3 +501,161 @@ def test_norm_feeds_the_products(seed):
     # the pair's error is bounded in test_ffn_gated_w4; here 2^-16 of the largest covers its fp32 part
     assert_within(act, want, HALF_BF16 * want.abs() + 2.0 ** -16 * want.abs().max() + TINY)
     check_linear_result(out, act, None, w2[0], w2[1], w2[2], None, h, "none", group)
+
+
+# ---------------------------------------------------------------------------------- plans
+
+@pytest.fixture
+def config():
+    yield gb.set_config
+    gb.set_config(None)
+
+
+@pytest.mark.parametrize("m", [1, 3, 8, 16])
+@pytest.mark.parametrize("gated", [False, True])
+def test_w4_every_plan_gives_the_result(config, m, gated):
+    """Columns over 1, 2, 4 and 8 CTAs and any number of a CTA's warps: rows, tokens and columns end inside."""
+    n, k, group = 77, 2400, 32
+    q, s, z = w4_weights(n, k, group, True, 3)
+    q3, s3, z3 = w4_weights(n, k, group, True, 7)
+    x, r = normal(m, k, seed=4), normal(m, n, seed=5)
+    plans = set()
+    for cluster in (1, 2, 4, 8):
+        for k_warps in (1, 2, 4, 8, 16):
+            config(f"w4_cluster={cluster},w4_k_warps={k_warps}")
+            try:
+                if gated:
+                    d = gb.ffn_gated_w4(x, q, s, q3, s3, zeros1=z, zeros3=z3, group=group)
+                else:
+                    d = gb.linear_w4(x, q, s, R=r, zeros=z, group=group)
+            except gb.GBError as e:
+                assert e.status == 2 and "w4_cluster" in str(e)
+                continue
+            plans.add(gb.last_plan())
+            if gated:
+                a, off_a = ref.w4_products(x, None, ref.unpack_w4(q, s, z, group, k))
+                b, off_b = ref.w4_products(x, None, ref.unpack_w4(q3, s3, z3, group, k))
+                gate = ref.act(a, "silu")
+                tol = (1.13 * off_a + 2.0 ** -20 * a.abs()) * (b.abs() + off_b) + gate.abs() * off_b
+                assert_within(d, gate * b, tol * (1 + HALF_BF16) + HALF_BF16 * (gate * b).abs() + TINY, gb.last_plan())
+            else:
+                check_linear_result(d, x, None, q, s, z, None, r, "none", group, gb.last_plan())
+    assert len(plans) >= 12
+
+
+def test_w4_config_refuses_what_no_plan_has(config):
+    q, s, _ = w4_weights(8, 128, 128, False, 1)
+    for bad in ("w4_cluster=3", "w4_k_warps=17", "w4_cluster=16"):
+        with pytest.raises(gb.GBError):
+            config(bad)
+    config("w4_k_warps=5")
+    with pytest.raises(gb.GBError, match="w4_k_warps"):
+        gb.linear_w4(normal(1, 128, seed=1), q, s)
+
+
+def test_w4_weights_at_their_zero_point_leave_nothing():
+    """q = z = 8 everywhere: every output is exactly its residual, whatever x is."""
+    q = torch.full((50, 1024), 0x88, dtype=torch.uint8, device=DEV)
+    for group in (32, 64, 128):
+        s = torch.full((50, 2048 // group), 3.0, dtype=BF16, device=DEV)
+        for m in (1, 7, 16):
+            assert not gb.linear_w4(normal(m, 2048, seed=m, std=100.0), q, s, group=group).any()
+
+
+@pytest.mark.parametrize("m", [2, 12])
+def test_w4_wide_range_of_x(m):
+    """Channels of very different size, values at bf16's ends, rows of zeros."""
+    q, s, z = w4_weights(64, 1024, 64, True, 5)
+    x = normal(m, 1024, seed=6)
+    x[0] = 0
+    x[1, ::7] *= 2.0 ** 20
+    x[1, ::11] *= 2.0 ** -60
+    if m > 2:
+        x[2] *= 2.0 ** -120
+        x[3] *= 2.0 ** 110
+        x[4] = torch.finfo(BF16).tiny
+    d = gb.linear_w4(x, q, s, zeros=z, group=64)
+    check_linear_result(d, x, None, q, s, z, None, None, "none", 64)
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 40, 700), (16, 33, 2048), (1, 5, 64)])
+def test_w4_infinities_and_nan_anywhere(m, n, k):
+    """Several a row, in every part of the columns; a weight at its zero point makes NaN of an infinity."""
+    k = k // 32 * 32
+    q, s, z = w4_weights(n, k, 32, True, 5)
+    x = normal(m, k, seed=6)
+    x[0, 0], x[0, k - 1] = float("inf"), float("inf")
+    x[m // 2, k // 2] = float("-inf")
+    x[m - 1, k // 3] = float("nan")
+    d = gb.linear_w4(x, q, s, zeros=z, group=32)
+    w = ref.unpack_w4(q, s, z, 32, k)
+    fine = torch.isfinite(x)
+    v, off = ref.w4_products(torch.where(fine, x, torch.zeros_like(x)), None, w)
+    odd = torch.zeros_like(v)
+    for i, j in (~fine).nonzero().tolist():
+        odd[i] += x[i, j].double() * w[:, j]
+    want = v + odd
+    assert_within(d, want, torch.where(torch.isfinite(want), 1.0 * off + HALF_BF16 * want.abs() * 1.01 + TINY,
+                                       torch.zeros_like(want)))
+
+
+# ---------------------------------------------------------------------------------- calls one after another
+
+def test_calls_back_to_back_see_each_other():
+    """Kernels are set up while the one before runs: a chain of calls through the same buffers gives what the
+    same calls give with a wait after each."""
+    d = 512
+    w = normal(d, seed=1)
+    ws = [w4_weights(d, d, 64, True, 10 + i) for i in range(3)]
+
+    def chain(wait):
+        x, r = normal(4, d, seed=2), normal(4, d, seed=3)
+        q8 = torch.empty(4, d, dtype=torch.float8_e4m3fn, device=DEV)
+        for i in range(60):
+            q, scale, r = gb.add_rms_norm_q8(x, w, r, out=q8, h=r)
+            wait()
+            gb.linear_w4(q, *ws[i % 3][:2], R=r, zeros=ws[i % 3][2], group=64, x_scale=scale, out=x, act="silu")
+            wait()
+            gb.dropout(x, 0.2, 5, i, out=x)
+            wait()
+            y, _, rstd = gb.add_rms_norm(x, w)
+            wait()
+            dx, _, dw = gb.add_rms_norm_backward(y, x, w, rstd, p=0.1, seed=i)
+            wait()
+            x = gb.dropout(dx, 0.0, 0, R=x)
+            wait()
+        return x, r, dw
+    fast = chain(lambda: None)
+    for a, b in zip(fast, chain(torch.cuda.synchronize)):
+        assert torch.equal(a, b)
+
+
+def test_binding_refuses_wrong_tensors():
+    x, w = normal(4, 64, seed=1), normal(64, seed=2)
+    q, s, z = w4_weights(8, 64, 64, True, 1)
+    for error, call in (
+            (TypeError, lambda: gb.linear_w4(x, q.float(), s, group=64)),
+            (TypeError, lambda: gb.linear_w4(x, q, s.float(), group=64)),
+            (TypeError, lambda: gb.linear_w4(x, q.cpu(), s, group=64)),
+            (ValueError, lambda: gb.linear_w4(x[:, :32], q, s, group=64)),
+            (ValueError, lambda: gb.linear_w4(x, q, s, group=32)),
+            (ValueError, lambda: gb.linear_w4(x, q, s, group=64, zeros=z[:4])),
+            (ValueError, lambda: gb.linear_w4(x, q, s, group=64, R=x)),
+            (ValueError, lambda: gb.linear_w4(x, q.t().contiguous().t(), s, group=64)),
+            (TypeError, lambda: gb.linear_w4(x.tolist(), q, s, group=64)),
+            (ValueError, lambda: gb.dropout(x[0], 0.1, 1)),
+            (ValueError, lambda: gb.dropout(x.t(), 0.1, 1)),
+            (TypeError, lambda: gb.dropout(x, 0.1, 1.5)),
+            (TypeError, lambda: gb.dropout(x, 0.1, torch.zeros(2, device=DEV))),
+            (ValueError, lambda: gb.dropout(x, 0.1, torch.zeros(3, dtype=torch.int64, device=DEV))),
+            (gb.GBError, lambda: gb.dropout(x, 1.5, 1)),
+            (ValueError, lambda: gb.add_rms_norm(x, w[:32])),
+            (TypeError, lambda: gb.add_rms_norm(x.float(), w)),
+            (gb.GBError, lambda: gb.add_rms_norm(x, w, eps=-1.0)),
+            (gb.GBError, lambda: gb.add_rms_norm_q8(x, w, scale_group=64)),
+            (gb.GBError, lambda: gb.add_rms_norm(normal(1, 16400, seed=1), normal(16400, seed=2))),
+            (ValueError, lambda: gb.add_rms_norm_backward(x, x, w, torch.ones(3, device=DEV))),
+            (TypeError, lambda: gb.add_rms_norm_backward(x, x, w, torch.ones(4, device=DEV), workspace=x.cpu()))):
+        with pytest.raises(error):
+            call()
+    gb.device_status()
