@@ -17,12 +17,12 @@
 //     sum (q - z) x = sum q x - z sum x,
 // with sum x from the same instructions in the same order on weights of 8, so that weights at the
 // zero point 8 (all there is without zeros) leave exactly nothing; weights at another zero point leave
-// 2^-24 of z s sum |x| (measured).  x becomes fp16 too: e4m3 values
-// are fp16 values as they are, and a token's bf16 values are first scaled by a power of two, so that
-// the largest (of the CTA's columns) is in [2^14, 2^15); what is then lost, below 2^-39 of the
-// largest, is under fp32's own rounding of the sum.  Products are summed in fp32 within a group, and the
-// group's sum is multiplied by its scales in fp32: no weight is ever rounded.  What x holds
-// of infinities and NaN is added one by one, slowly (sum x would make NaN of an infinity).
+// 2^-24 of z s sum |x| (measured).  x becomes fp16 too: e4m3 values are fp16 values as they are, and a
+// token's bf16 values are first scaled by a power of two, so that the largest (of the CTA's columns)
+// is in [2^14, 2^15); what is then lost, below 2^-35 of the largest, is under fp32's own rounding of
+// the sum.  Products are summed in fp32 within a group, and the group's sum is multiplied by its
+// scales in fp32: no weight is ever rounded.  What x holds of infinities and NaN is added one by one,
+// slowly (sum x would make NaN of an infinity).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -526,6 +526,8 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
     };
     if (mine > 0) start_next();
 
+    // (a CTA past the last column has nothing, times nothing)
+    if (steps == 0 && !kGroupX && tid < 8 * NT) xscale[tid] = 0.f;
     // (a word a token for stage_x: where the units' scales will be)
     const bool finite = stage_x<G, NT, X>(p, xs, xscale, xsum_end, col_base, steps, token0, tokens);
     bool odd = false;

@@ -226,8 +226,8 @@ GB_API gb_status_t gb_gemm_linear_dact(const void* dY, int64_t lddy, const void*
  *   W[n,k] = (q[n,k] - z[n,k/group]) * s[n,k/group]
  *   D[m,n] = bf16( act( sum_k X[m,k] W[n,k] + bias[n] ) + R[m,n] )
  *
- * No weight is rounded: the products with the integers q - z are summed in fp32 within a group,
- * and the sums are scaled in fp32.
+ * No weight is rounded: the integers' products with X are summed in fp32 within a group, as
+ * sum q x - z sum x, and the sums are scaled in fp32.
  *   X       [M,K], leading dimension ldx (elements); x_type is a gb_x_type_t:
  *           GB_X_BF16              bf16; x_scale is not read
  *           GB_X_E4M3_ROW_SCALE    e4m3, row m times x_scale[m*ldxs]
@@ -235,7 +235,7 @@ GB_API gb_status_t gb_gemm_linear_dact(const void* dY, int64_t lddy, const void*
  *           (the two outputs of gb_add_rms_norm_q8)
  *   Wq      [N,K/2] bytes, row n at Wq + n*ldq (ldq in BYTES): the low nibble of byte j is
  *           q[n,2j], the high one q[n,2j+1]
- *   scales  [N,ceil(K/group)] bf16 (lds elements)
+ *   scales  [N,ceil(K/group)] bf16 (lds elements), below 2^115 in size
  *   zeros   [N,ceil(K/group)] bytes of 0..15 (ldz bytes), or NULL: z = 8 everywhere
  *   group   32, 64 or 128 columns; the last group of a row may be shorter
  *   bias, R, act, D  as gb_gemm_linear (any 2-byte alignment and leading dimension)

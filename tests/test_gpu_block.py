@@ -543,6 +543,20 @@ def test_w4_every_plan_gives_the_result(config, m, gated):
     assert len(plans) >= 12
 
 
+def test_w4_columns_that_end_before_the_last_cta(config):
+    """CTAs of a cluster without any columns add nothing, whatever an earlier kernel left in shared memory."""
+    config("w4_cluster=8,w4_k_warps=2")
+    m, n, group = 4, 100, 64
+    long_q, long_s, _ = w4_weights(n, 4096, group, False, 1)
+    x8, xs = w4_input(m, 4096, "row", 2)
+    for k in (2304, 256, 0):
+        q, s, z = w4_weights(n, k, group, True, 3)
+        x, r = normal(m, k, seed=4), normal(m, n, seed=5)
+        assert gb.linear_w4(x8, long_q, long_s, group=group, x_scale=xs * float("nan")).isnan().all()
+        d = gb.linear_w4(x, q, s, R=r, zeros=z, group=group)
+        check_linear_result(d, x, None, q, s, z, None, r, "none", group, str(k))
+
+
 def test_w4_config_refuses_what_no_plan_has(config):
     q, s, _ = w4_weights(8, 128, 128, False, 1)
     for bad in ("w4_cluster=3", "w4_k_warps=17", "w4_cluster=16"):
