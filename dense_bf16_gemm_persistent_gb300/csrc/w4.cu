@@ -148,11 +148,11 @@ int share_tokens(int tokens, int cluster) {
     return static_cast<int>(ceil_div(tokens, by_token)) * by_token;
 }
 
-size_t smem_of(int slice_units, int tokens, int warps, int group, int cluster, bool group_x) {
+size_t smem_of(int slice_units, int tokens, int warps, int group, int cluster, bool step_scale) {
     const size_t nt = tiles_of(tokens), units = slice_units;
     return static_cast<size_t>(warps) * gb::w4::kUnitBytes +                        // slots
            units * (kUnit / 8) * tokens * 16 +                                    // x
-           ((group_x ? units * (kUnit / gb::w4::kStep) : 1) + units * (kUnit / group)) * 8 * nt * 4 +  // its scales and sums
+           ((step_scale ? units * (kUnit / gb::w4::kStep) : 1) + units * (kUnit / group)) * 8 * nt * 4 +  // its scales and sums
            static_cast<size_t>(2) * warps * share_tokens(tokens, cluster) * kRows * 4 +  // the warps' sums
            static_cast<size_t>(warps) * (kUnit / group) * 128;                      // their units' scales
 }
@@ -205,7 +205,7 @@ gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInf
         for (int cluster = 1; cluster <= 8 && (cluster <= units || want.cluster); cluster *= 2) {
             if (want.cluster && cluster != want.cluster) continue;
             const int slice = static_cast<int>(ceil_div(units, cluster));
-            const size_t smem = smem_of(slice, tokens, warps, pr.group, cluster, pr.x_type == GB_X_E4M3_GROUP_SCALE);
+            const size_t smem = smem_of(slice, tokens, warps, pr.group, cluster, pr.x_type != GB_X_E4M3_ROW_SCALE);
             if (smem > info.smem_optin) continue;
             int at_once = 0;
             const gb_status_t st = clusters_at_once(cluster, dev, info, &at_once);

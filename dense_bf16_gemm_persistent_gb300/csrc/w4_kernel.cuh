@@ -17,9 +17,9 @@
 //     sum (q - z) x = sum q x - z sum x,
 // with sum x from the same instructions in the same order on weights of 8, so that weights at the
 // zero point 8 (all there is without zeros) leave exactly nothing; weights at another zero point leave
-// 2^-24 of z s sum |x| (measured).  x becomes fp16 too: e4m3 values are fp16 values as they are, and a
-// token's bf16 values are first scaled by a power of two, so that the largest (of the CTA's columns)
-// is in [2^14, 2^15); what is then lost, below 2^-35 of the largest, is under fp32's own rounding of
+// 2^-24 of z s sum |x| (measured).  x becomes fp16 too: e4m3 values are fp16 values as they are, and bf16
+// values are first scaled by a power of two for each 128 columns of a token, so that the largest is in
+// [2^14, 2^15); what is then lost, below 2^-35 of the largest, is under fp32's own rounding of
 // the sum.  Products are summed in fp32 within a group, and the group's sum is multiplied by its
 // scales in fp32: no weight is ever rounded.  What x holds of infinities and NaN is added one by one,
 // slowly (sum x would make NaN of an infinity).
@@ -203,66 +203,30 @@ __device__ __forceinline__ void load_x(const Params& p, bool wide, int token, in
 
 // x of a CTA's slice to shared memory: 16-byte chunks [step][c][token][t], in each the pairs
 // (i, i + 4) of eight columns as widen() gives the weights'; and what the sums are to be multiplied
-// by, in `xscale` [token of NT eights] or, with kXGroupScale, [step][token].  bf16 values that
-// are not finite are left out (as zeros); returns whether the thread had none.  `top`: a word for each token.  Barriers inside.
+// by, in `xscale` [step][token of NT eights], or with kXRowScale [token].  bf16 values that are not
+// finite are left out (as zeros); returns whether the thread had none.
 template <int G, int NT, int X>
-__device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscale, uint32_t* top, int col_base, int steps,
-                                        int token0, int tokens) {
+__device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscale, int col_base, int steps, int token0,
+                                        int tokens) {
     constexpr int kPer = G / 32;
     constexpr bool X8 = X != kXBf16;
     const bool wide = (reinterpret_cast<uintptr_t>(p.x) & (X8 ? 7 : 15)) == 0 && (p.ldx & 7) == 0;
-    const int at = threadIdx.x & 15, first = threadIdx.x >> 4, stride = blockDim.x >> 4;
+    const int at = threadIdx.x & 15, stride = blockDim.x >> 4;
     const int group = at / (4 * kPer), lt = at / kPer & 3, c = group * kPer + at % kPer;
-    const int total = steps * tokens;  // a step of a token is sixteen threads
-    constexpr int kBatch = 4;  // loads that a thread has on their way
+    const int total = steps * tokens;  // a step of a token is sixteen lanes, which agree on its scale
+    constexpr int kBatch = 4;          // loads that a thread has on their way
     bool finite = true;
-    uint32_t kept[kBatch][4];  // the thread's first chunks, which are often its only ones
-    if (!X8) {
-        // the largest finite exponent of each token's columns
-        if (threadIdx.x < tokens) top[threadIdx.x] = 0;
-        __syncthreads();
-        for (int i = first; (i & ~1) < total; i += kBatch * stride) {
-            uint32_t w[kBatch][4];
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int at_u = i + u * stride, token = at_u / steps, col = col_base + (at_u - token * steps) * kStep + at * 8;
-                load_x<X8>(p, wide, token0 + token, col, at_u < total && col < p.k, w[u]);
-            }
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) {
-                const int at_u = i + u * stride;
-                if ((at_u & ~1) >= total) break;
-                uint32_t most = 0;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (i == first) kept[u][j] = w[u][j];
-                    const uint32_t lo = w[u][j] >> 7 & 0xff, hi = w[u][j] >> 23 & 0xff;
-                    finite = finite && lo != 0xff && hi != 0xff;
-                    most = max(most, max(lo == 0xff ? 0u : lo, hi == 0xff ? 0u : hi));
-                }
-#pragma unroll
-                for (int d = 8; d > 0; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
-                if (at_u < total && at == 0) atomicMax(&top[at_u / steps], most);
-            }
-        }
-        __syncthreads();
-    }
-    for (int i = first; i < total; i += kBatch * stride) {
+    for (int i = threadIdx.x >> 4; (i & ~1) < total; i += kBatch * stride) {
         uint32_t w[kBatch][4];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int at_u = i + u * stride, token = at_u / steps, col = col_base + (at_u - token * steps) * kStep + at * 8;
-            if (!X8 && i == first) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) w[u][j] = kept[u][j];
-            } else {
-                load_x<X8>(p, wide, token0 + token, col, at_u < total && col < p.k, w[u]);
-            }
+            load_x<X8>(p, wide, token0 + token, col, at_u < total && col < p.k, w[u]);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int at_u = i + u * stride, token = at_u / steps, step = at_u - token * steps;
-            if (at_u >= total) break;
+            if ((at_u & ~1) >= total) break;  // (of the whole warp)
             float v[8], scale = kHalfShift;
             if (X8) {
 #pragma unroll
@@ -273,27 +237,36 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
                     v[2 * j] = f.x;
                     v[2 * j + 1] = f.y;
                 }
-                if (at == 0 && (X == kXGroupScale || step == 0)) {
+                if (at == 0 && at_u < total && (X == kXGroupScale || step == 0)) {
                     const int column = X == kXGroupScale ? min(col_base / kStep + step, (p.k - 1) / kStep) : 0;
                     scale *= p.x_scale[(token0 + token) * p.ldxs + column];
                 }
             } else {
-                // 2^(14 - (top - 127)), below 2^127; its reciprocal goes to the sum
-                const uint32_t up = min(268u - top[token], 253u);
-                const float f = __uint_as_float(up << 23);
+                uint32_t top = 0;  // the largest finite exponent
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    v[2 * j] = (w[u][j] >> 7 & 0xff) == 0xff ? 0.f : __uint_as_float(w[u][j] << 16) * f;
-                    v[2 * j + 1] = (w[u][j] >> 23 & 0xff) == 0xff ? 0.f : __uint_as_float(w[u][j] & 0xffff0000u) * f;
+                    const uint32_t lo = w[u][j] >> 7 & 0xff, hi = w[u][j] >> 23 & 0xff;
+                    finite = finite && lo != 0xff && hi != 0xff;
+                    top = max(top, max(lo == 0xff ? 0u : lo, hi == 0xff ? 0u : hi));
+                    v[2 * j] = lo == 0xff ? 0.f : __uint_as_float(w[u][j] << 16);
+                    v[2 * j + 1] = hi == 0xff ? 0.f : __uint_as_float(w[u][j] & 0xffff0000u);
                 }
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                // 2^(14 - (top - 127)), below 2^127; its reciprocal goes to the sum
+                const uint32_t up = min(268u - top, 253u);
+                const float f = __uint_as_float(up << 23);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[j] *= f;
                 scale *= __uint_as_float((254u - up) << 23);
             }
+            if (at_u >= total) continue;
             constexpr float kSixteenth = 0.0625f;
             xs[((step * 4 + c) * tokens + token) * 4 + lt] =
                 make_uint4(half_pair(v[0], v[4]), half_pair(v[1] * kSixteenth, v[5] * kSixteenth), half_pair(v[2], v[6]),
                            half_pair(v[3] * kSixteenth, v[7] * kSixteenth));
-            if (at == 0 && X == kXGroupScale) xscale[step * 8 * NT + token] = scale;
-            if (at == 0 && X != kXGroupScale && step == 0) xscale[token] = scale;
+            if (at == 0 && X != kXRowScale) xscale[step * 8 * NT + token] = scale;
+            if (at == 0 && X == kXRowScale && step == 0) xscale[token] = scale;
         }
     }
     return finite;
@@ -383,7 +356,7 @@ struct Cursor {
 // 16-byte cp.async, which runs ahead over the ends of tiles; no barrier but the warp's own.
 template <int G, int NT, bool GATED, int X>
 __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __grid_constant__ Params p) {
-    constexpr bool kGroupX = X == kXGroupScale;
+    constexpr bool kStepScale = X != kXRowScale;  // x has a scale for each step
     constexpr int kPer = G / 32;         // words of a lane in a group
     constexpr int kGroups = kUnit / G;   // of a unit: what a lane fetches the scales of, for one row
     constexpr int kStepGroups = kStep / G;
@@ -410,10 +383,9 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
     const uint32_t slot = smem_addr(smem) + warp * kUnitBytes;
     uint4* xs = reinterpret_cast<uint4*>(smem + warps * kUnitBytes);
     float* xscale = reinterpret_cast<float*>(xs + static_cast<size_t>(p.slice_units) * (kUnit / 8) * p.tokens);
-    float* xsum = xscale + (kGroupX ? p.slice_units * (kUnit / kStep) : 1) * 8 * NT;
+    float* xsum = xscale + (kStepScale ? p.slice_units * (kUnit / kStep) : 1) * 8 * NT;
 
-    uint32_t* xsum_end = reinterpret_cast<uint32_t*>(xsum + p.slice_units * kGroups * 8 * NT);
-    const uint32_t all_scales = smem_addr(xsum_end);
+    const uint32_t all_scales = smem_addr(xsum + p.slice_units * kGroups * 8 * NT);
     const uint32_t scales_of_warp = all_scales + warp * kGroups * 128, sums = all_scales + warps * kGroups * 128;
 
     const int k_warps = p.k_warps, teams = warps / k_warps;
@@ -527,9 +499,8 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
     if (mine > 0) start_next();
 
     // (a CTA past the last column has nothing, times nothing)
-    if (steps == 0 && !kGroupX && tid < 8 * NT) xscale[tid] = 0.f;
-    // (a word a token for stage_x: where the units' scales will be)
-    const bool finite = stage_x<G, NT, X>(p, xs, xscale, xsum_end, col_base, steps, token0, tokens);
+    if (steps == 0 && !kStepScale && tid < 8 * NT) xscale[tid] = 0.f;
+    const bool finite = stage_x<G, NT, X>(p, xs, xscale, col_base, steps, token0, tokens);
     bool odd = false;
     if constexpr (X != kXBf16) __syncthreads();  // (a vote on a constant is not a barrier to rely on)
     else odd = __syncthreads_or(!finite);
@@ -608,7 +579,7 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
                     const uint32_t at = team_sums + buffer * buffer_bytes + (rank * k_warps + k_part) * share_bytes +
                                         4 * ((token >> token_bits) * share_rows + row);
                     float v = total[r / 2][j][i + r % 2 * 2];
-                    if (!kGroupX) v *= load_shared_float(scales_lane - t * 8 + 4 * token);
+                    if (!kStepScale) v *= load_shared_float(scales_lane - t * 8 + 4 * token);
                     if (X == kXBf16 && odd) {
                         const int64_t n = static_cast<int64_t>(tile) * kOutRows + (GATED ? kind * 8 : r * 8) + g;
                         if (n < p.n)
@@ -668,11 +639,11 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
             start_next();
 
             uint32_t x_at = unit * (kUnit / 8) * 16 * tokens;
-            uint32_t scale_at = scales_lane + (kGroupX ? unit * (kUnit / kStep) * 32 * NT : 0);
+            uint32_t scale_at = scales_lane + (kStepScale ? unit * (kUnit / kStep) * 32 * NT : 0);
             uint32_t sums_at = sums_lane + unit * kGroups * 32 * NT;
             auto multiply = [&](int s) {
                 float xs0[NT], xs1[NT];  // x's scales of the step, for the lane's two tokens of each eight
-                if (kGroupX) {
+                if (kStepScale) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         uint32_t e[2];
@@ -731,7 +702,7 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
                                 float v = acc[r / 2][i][r % 2 * 2 + e];
                                 if (!kLess) v = fmaf(-z, __uint_as_float(sum[e]), v);
                                 float& to = total[r / 2][i][r % 2 * 2 + e];
-                                to = fmaf(kGroupX ? scale * (e ? xs1[i] : xs0[i]) : scale, v, to);
+                                to = fmaf(kStepScale ? scale * (e ? xs1[i] : xs0[i]) : scale, v, to);
                             }
                         }
                     }
