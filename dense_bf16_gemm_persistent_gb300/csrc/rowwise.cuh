@@ -226,8 +226,8 @@ constexpr int kDropoutThreads = 256, kDropoutBatch = 2;
 // walk is `step_rows` rows and `step_chunks` chunks, so that no thread divides again.
 //
 // Four words take twenty 32 x 32 -> 64 bit multiplications: at 8192 x 14336 the multiplier's pipe is
-// busy 58 % and the logic's 54 % of the time, and the generator, not the memory, is the bound: 119 us
-// for 470 MB (3.9 TB/s, 0.58 of the copy bandwidth), 132 us for 705 MB with a residual (5.3 TB/s,
+// busy 62 % and the logic's 55 % of the time (4096 rows), and the generator, not the memory, is the bound:
+// 120 us for 470 MB (3.9 TB/s, 0.58 of the copy bandwidth), 133 us for 705 MB with a residual (5.3 TB/s,
 // 0.78) on a GB300.  One chunk at a time took 138 us, three 139, 40 registers instead of 48 took 142,
 // and blocks that walk rows 150.
 template <int DROP>
@@ -363,10 +363,10 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int col0, int cols, boo
 // part of the weight; kRowStages - 1 rows are on their way beside the one that is worked on.
 // Dynamic shared memory: the rows [stage][x or r][chunk][thread], the weight, kGroupScale's maxima.
 //
-// 8192 x 4096 with a residual on a GB300: 46 us, 5.8 TB/s (0.86 of the copy bandwidth); with dropout
-// 57 us, bound by the generator's instructions (64 % of issue slots used); 8-bit output 47 us with a
-// scale a row (0.73), 54 us for each 128 columns.  Blocks that each load one row and end took 85 us
-// with dropout: nothing was on its way while they drew.
+// 8192 x 4096 with a residual on a GB300: 45 to 46 us, 5.9 TB/s (0.87 of the copy bandwidth); with
+// dropout 57 us, bound by the generator's instructions (64 % of issue slots used); 8-bit output 46 us
+// with a scale a row (0.75), 54 us for each 128 columns.  The first kernel, blocks that each load one
+// row and end, took 85 us with dropout; rows ahead of their turn and keys in constant memory 66.
 constexpr int kRowStages = 3;
 
 template <int V, int DROP, int OUT>
@@ -539,10 +539,10 @@ struct NormBwdParams {
 // V chunks a thread.  The rows come through shared memory as the forward pass's do, in two stages.
 // Dynamic shared memory: the rows [stage][dY, H or dH][chunk][thread], then the weight.
 //
-// 8192 x 4096 with dH on a GB300, the join of the weight's gradient with it: 52.6 us, 5.1 TB/s (0.75 of
-// the copy bandwidth), and 78 us with dropout (10 bytes an element and the generator; 0.64).  The rows
-// in registers instead of shared memory left two blocks an SM and took 110 us; 512 threads an SM
-// take 107 us, or 82 with a third stage, where 768 take 78.
+// 8192 x 4096 with dH on a GB300, the join of the weight's gradient with it: 51.2 us, 5.2 TB/s (0.77 of
+// the copy bandwidth), and 78 us with dropout (10 bytes an element and the generator; 0.63).  The first
+// kernel, with its rows in registers and two blocks an SM, took 110 us; 512 threads an SM take 107 us,
+// or 82 with a third stage, where 768 take 78.
 constexpr int kBwdStages = 2;
 
 template <int V, int DROP>
