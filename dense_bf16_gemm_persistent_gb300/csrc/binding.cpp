@@ -175,6 +175,9 @@ Activations activations(const at::Tensor& X, PyObject* x_scale, int64_t M, int64
     if (s.dim() == 1) {
         check_type(s, "x_scale", at::kFloat);
         if (s.size(0) != M) raise(PyExc_ValueError, "x_scale: expected shape (" + std::to_string(M) + ",), got " + shape_of(s.sizes()));
+        // (an expanded scale has a stride of 0: its storage ends after one element)
+        if (M > 1 && s.stride(0) < 1)
+            raise(PyExc_ValueError, "x_scale: expected a scale of its own for each row, got stride " + std::to_string(s.stride(0)));
         a.scale = {s.data_ptr(), std::max<int64_t>(s.stride(0), 1)};  // (a row's scale each stride)
         return a;
     }
