@@ -13,7 +13,10 @@ tokens), add_rms_norm (and its 8-bit and backward forms), dropout.
 
 Tensors are torch CUDA bf16 tensors, 2-D with a contiguous last dimension
 (bias: contiguous 1-D).  Work is enqueued on ``torch.cuda.current_stream()``
-unless a stream is given.
+unless a stream is given (a torch stream or a cudaStream_t's number).  Outputs and
+workspaces that a call makes are the memory of the stream it runs on; with a stream
+given, the caller orders it after what wrote the inputs, and the current stream after
+it before the outputs are used there.
 """
 from __future__ import annotations
 
@@ -146,6 +149,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream, call, *args):
+    """call(*args) with `stream` as the current one, for a call that was given a stream.  What the call allocates is
+    then that stream's memory: a workspace that is dropped when the call returns can only be given to later work of the
+    same stream, and no tensor made here lies where work queued on the current stream still reads or writes.  The
+    results are recorded on the current stream, where they are used and may be dropped."""
+    handle = _stream(stream)
+    if handle == _stream(None):
+        return call(*args)
+    here = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):
+        # (0 and 1 are the legacy default stream's numbers)
+        stream = torch.cuda.default_stream() if handle in (0, 1) else torch.cuda.ExternalStream(handle)
+    with torch.cuda.stream(stream):
+        result = call(*args)
+    for t in result if isinstance(result, tuple) else (result,):
+        t.record_stream(here)
+    return result
+
+
 def splitk_workspace_bytes(M: int, N: int, K: int, splits: int = 0, ffn: bool = False) -> int:
     """Bytes of workspace the split-K call needs on the current device (0: no split)."""
     n = ctypes.c_size_t(0)
@@ -170,6 +192,8 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, R
 
     split_k: None (never split), "auto", or a number of K ranges; the fp32 partials
     go to `workspace` (a CUDA tensor, allocated here when not given)."""
+    if stream is not None:
+        return _on(stream, linear, A, B, bias, R, act, out, None, split_k, workspace)
     M, K = A.shape
     N = B.shape[0]
     if act not in ACT:
@@ -185,11 +209,11 @@ def linear(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, R
     pd, ldd = _mat(out, "out", M, N)
     pbias = bias.data_ptr() if bias is not None else None
     if split_k is None:
-        _check(lib().gb_gemm_linear(pa, lda, pb, ldb, pbias, pr, ldr, ACT[act], pd, ldd, M, N, K, _stream(stream)))
+        _check(lib().gb_gemm_linear(pa, lda, pb, ldb, pbias, pr, ldr, ACT[act], pd, ldd, M, N, K, _stream(None)))
     else:
         splits, ws = _workspace(split_k, workspace, M, N, K, False, A.device)
         _check(lib().gb_gemm_linear_splitk(pa, lda, pb, ldb, pbias, pr, ldr, ACT[act], pd, ldd, M, N, K, splits,
-                                           ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+                                           ws.data_ptr(), ws.numel() * ws.element_size(), _stream(None)))
     return out
 
 
@@ -197,6 +221,8 @@ def linear_preact(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = 
                   act: str = "none", out: torch.Tensor | None = None, preact: torch.Tensor | None = None,
                   stream=None) -> tuple[torch.Tensor, torch.Tensor]:
     """(D, Z): D as linear(), Z = bf16(A @ B.T + bias), the pre-activation, from the same pass."""
+    if stream is not None:
+        return _on(stream, linear_preact, A, B, bias, R, act, out, preact)
     M, K = A.shape
     N = B.shape[0]
     if act not in ACT:
@@ -214,7 +240,7 @@ def linear_preact(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = 
     pd, ldd = _mat(out, "out", M, N)
     pz, ldz = _mat(preact, "preact", M, N)
     _check(lib().gb_gemm_linear_preact(pa, lda, pb, ldb, bias.data_ptr() if bias is not None else None, pr, ldr,
-                                       ACT[act], pd, ldd, pz, ldz, M, N, K, _stream(stream)))
+                                       ACT[act], pd, ldd, pz, ldz, M, N, K, _stream(None)))
     return out, preact
 
 
@@ -222,6 +248,8 @@ def matmul(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, R
            act: str = "none", out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """D = bf16(act(A @ B + bias) + R) on the GPU with B in its [K,N] layout (A [M,K], B [K,N],
     bias [N], R [M,N])."""
+    if stream is not None:
+        return _on(stream, matmul, A, B, bias, R, act, out)
     M, K = A.shape
     N = B.shape[1]
     if act not in ACT:
@@ -236,7 +264,7 @@ def matmul(A: torch.Tensor, B: torch.Tensor, bias: torch.Tensor | None = None, R
         out = torch.empty((M, N), dtype=torch.bfloat16, device=A.device)
     pd, ldd = _mat(out, "out", M, N)
     _check(lib().gb_gemm_matmul(pa, lda, pb, ldb, bias.data_ptr() if bias is not None else None, pr, ldr, ACT[act],
-                                pd, ldd, M, N, K, _stream(stream)))
+                                pd, ldd, M, N, K, _stream(None)))
     return out
 
 
@@ -244,6 +272,8 @@ def linear_dact(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor, act: str = "
                 out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """D = bf16((dY @ W) * act'(Z)) on the GPU: dY [M,N], W [N,K] (the layer's weight as linear()
     takes it), Z [M,K] (the stored pre-activation); D [M,K]."""
+    if stream is not None:
+        return _on(stream, linear_dact, dY, W, Z, act, out)
     M, N = dY.shape
     K = W.shape[1]
     if act not in ACT:
@@ -254,13 +284,15 @@ def linear_dact(dY: torch.Tensor, W: torch.Tensor, Z: torch.Tensor, act: str = "
     if out is None:
         out = torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
     pd, ldd = _mat(out, "out", M, K)
-    _check(lib().gb_gemm_linear_dact(py, ldy, pw, ldw, pz, ldz, ACT[act], pd, ldd, M, N, K, _stream(stream)))
+    _check(lib().gb_gemm_linear_dact(py, ldy, pw, ldw, pz, ldz, ACT[act], pd, ldd, M, N, K, _stream(None)))
     return out
 
 
 def ffn_gated(X: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, out: torch.Tensor | None = None,
               stream=None, split_k=None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """D = bf16(silu(X @ W1.T) * (X @ W3.T)) on the GPU (X [M,K], W1/W3 [N,K]); split_k as in linear()."""
+    if stream is not None:
+        return _on(stream, ffn_gated, X, W1, W3, out, None, split_k, workspace)
     M, K = X.shape
     N = W1.shape[0]
     px, ldx = _mat(X, "X", M, K)
@@ -270,11 +302,11 @@ def ffn_gated(X: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, out: torch.Te
         out = torch.empty((M, N), dtype=torch.bfloat16, device=X.device)
     pd, ldd = _mat(out, "out", M, N)
     if split_k is None:
-        _check(lib().gb_gemm_ffn_gated(px, ldx, p1, ld1, p3, ld3, pd, ldd, M, N, K, _stream(stream)))
+        _check(lib().gb_gemm_ffn_gated(px, ldx, p1, ld1, p3, ld3, pd, ldd, M, N, K, _stream(None)))
     else:
         splits, ws = _workspace(split_k, workspace, M, N, K, True, X.device)
         _check(lib().gb_gemm_ffn_gated_splitk(px, ldx, p1, ld1, p3, ld3, pd, ldd, M, N, K, splits, ws.data_ptr(),
-                                              ws.numel() * ws.element_size(), _stream(stream)))
+                                              ws.numel() * ws.element_size(), _stream(None)))
     return out
 
 

@@ -20,7 +20,7 @@ import os
 
 import torch
 
-from . import _PKG, ACT, GBError, _check, _lock, _stream, lib
+from . import _PKG, ACT, GBError, _check, _lock, _on, _stream, lib
 
 _module = None
 
@@ -53,17 +53,20 @@ def linear_w4(X: torch.Tensor, Wq: torch.Tensor, scales: torch.Tensor, bias: tor
     X [M,K] bf16, or float8_e4m3fn with x_scale ([M] or [M,1]: a row's; [M,ceil(K/128)]: of 128 columns); Wq
     [N,K/2] uint8 (the low nibble is the even column); scales [N,ceil(K/group)] bf16; zeros uint8 of the same
     shape (None: 8); bias [N], R [M,N] as in linear()."""
+    if stream is not None:
+        return _on(stream, linear_w4, X, Wq, scales, bias, R, act, zeros, group, x_scale, out)
     if act not in ACT:
         raise ValueError(f"act must be one of {sorted(ACT)}")
-    return (_module or binding()).linear_w4(X, Wq, scales, bias, R, ACT[act], zeros, group, x_scale, out, stream)
+    return (_module or binding()).linear_w4(X, Wq, scales, bias, R, ACT[act], zeros, group, x_scale, out)
 
 
 def ffn_gated_w4(X: torch.Tensor, W1q: torch.Tensor, scales1: torch.Tensor, W3q: torch.Tensor, scales3: torch.Tensor,
                  zeros1: torch.Tensor | None = None, zeros3: torch.Tensor | None = None, group: int = 128,
                  x_scale: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """D = bf16(silu(X @ W1.T) * (X @ W3.T)) for a few tokens, the weights as in linear_w4()."""
-    return (_module or binding()).ffn_gated_w4(X, W1q, scales1, W3q, scales3, zeros1, zeros3, group, x_scale, out,
-                                               stream)
+    if stream is not None:
+        return _on(stream, ffn_gated_w4, X, W1q, scales1, W3q, scales3, zeros1, zeros3, group, x_scale, out)
+    return (_module or binding()).ffn_gated_w4(X, W1q, scales1, W3q, scales3, zeros1, zeros3, group, x_scale, out)
 
 
 def dropout(X: torch.Tensor, p: float, seed, offset: int = 0, R: torch.Tensor | None = None,
@@ -71,7 +74,9 @@ def dropout(X: torch.Tensor, p: float, seed, offset: int = 0, R: torch.Tensor | 
     """D = bf16(keep * X / (1 - p) + R); keep is drawn from (seed, offset) and the element's place alone, so the
     gradient of X is dropout(dD, p, seed, offset).  `seed`: a number, or a CUDA int64 tensor {seed, offset} that
     is read when the kernel runs (a replayed graph then draws what the tensor holds)."""
-    return (_module or binding()).dropout(X, p, seed, offset, R, out, stream)
+    if stream is not None:
+        return _on(stream, dropout, X, p, seed, offset, R, out)
+    return (_module or binding()).dropout(X, p, seed, offset, R, out)
 
 
 def add_rms_norm(X: torch.Tensor, weight: torch.Tensor, R: torch.Tensor | None = None, eps: float = 1e-6,
@@ -79,7 +84,9 @@ def add_rms_norm(X: torch.Tensor, weight: torch.Tensor, R: torch.Tensor | None =
                  h: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(Y, H, rstd): H = dropout(X) + R (p, seed, offset as in dropout()), rstd = 1 / sqrt(mean(H^2) + eps) of
     each row, Y = H * rstd * weight from H before its rounding.  Without R and dropout H is X itself."""
-    return (_module or binding()).add_rms_norm(X, weight, R, eps, p, seed, offset, out, h, stream)
+    if stream is not None:
+        return _on(stream, add_rms_norm, X, weight, R, eps, p, seed, offset, out, h)
+    return (_module or binding()).add_rms_norm(X, weight, R, eps, p, seed, offset, out, h)
 
 
 def add_rms_norm_q8(X: torch.Tensor, weight: torch.Tensor, R: torch.Tensor | None = None, eps: float = 1e-6,
@@ -87,7 +94,9 @@ def add_rms_norm_q8(X: torch.Tensor, weight: torch.Tensor, R: torch.Tensor | Non
                     stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(Q, scale, H): the norm's output in float8_e4m3fn, Q * scale = Y.  scale is [M,1] (scale_group = 0) or
     [M,ceil(D/128)] (scale_group = 128), as linear_w4() and ffn_gated_w4() take it."""
-    return (_module or binding()).add_rms_norm_q8(X, weight, R, eps, scale_group, out, h, stream)
+    if stream is not None:
+        return _on(stream, add_rms_norm_q8, X, weight, R, eps, scale_group, out, h)
+    return (_module or binding()).add_rms_norm_q8(X, weight, R, eps, scale_group, out, h)
 
 
 def add_rms_norm_backward_workspace_bytes(M: int, D: int) -> int:
@@ -103,5 +112,6 @@ def add_rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tenso
                           stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """(dX, dR, dweight) of add_rms_norm() from the gradient dY of Y and (optionally) dH of H, with H and rstd as
     it returned them and the same p, seed and offset.  Without dropout dX is dR; dweight [D] is fp32."""
-    return (_module or binding()).add_rms_norm_backward(dY, H, weight, rstd, dH, p, seed, offset, workspace,
-                                                        stream)
+    if stream is not None:
+        return _on(stream, add_rms_norm_backward, dY, H, weight, rstd, dH, p, seed, offset, workspace)
+    return (_module or binding()).add_rms_norm_backward(dY, H, weight, rstd, dH, p, seed, offset, workspace)

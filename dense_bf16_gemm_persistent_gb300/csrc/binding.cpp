@@ -25,7 +25,7 @@ decltype(&gb_add_rms_norm_backward) f_norm_bwd;
 decltype(&gb_add_rms_norm_backward_workspace_bytes) f_norm_bwd_ws;
 decltype(&gb_last_error) f_last_error;
 PyObject* g_error;   // the package's GBError
-PyObject* g_stream;  // and its _stream(): a stream's handle, None: the current one's
+PyObject* g_stream;  // and its _stream(): a stream's handle, None: the current one's, on which every call runs
 
 constexpr auto kBf16 = at::kBFloat16;
 constexpr auto kE4m3 = at::kFloat8_e4m3fn;
@@ -205,8 +205,8 @@ int64_t group_of(PyObject* o) {
 
 void* address(PyObject* o) { return reinterpret_cast<void*>(static_cast<uintptr_t>(word(o))); }
 
-void* stream_of(PyObject* o) {
-    PyObject* handle = PyObject_CallOneArg(g_stream, o);
+void* current_stream() {
+    PyObject* handle = PyObject_CallOneArg(g_stream, Py_None);
     if (!handle) throw Raised{};
     const uint64_t v = PyLong_AsUnsignedLongLongMask(handle);
     Py_DECREF(handle);
@@ -221,9 +221,9 @@ void expect(Py_ssize_t n) {
 
 using Args = PyObject* const*;
 
-// X, Wq, scales, bias, R, act, zeros, group, x_scale, out, stream
+// X, Wq, scales, bias, R, act, zeros, group, x_scale, out
 PyObject* linear_w4(Args a, Py_ssize_t n) {
-    expect<11>(n);
+    expect<10>(n);
     const at::Tensor& X = tensor(a[0], "X");
     const auto [M, K] = sizes(X, "X");
     const int64_t N = sizes(tensor(a[1], "Wq"), "Wq").first, group = group_of(a[7]);
@@ -234,13 +234,13 @@ PyObject* linear_w4(Args a, Py_ssize_t n) {
     Out out(a[9], "out", kBf16, M, N, X);
     check(f_linear_w4(x.x.p, x.x.ld, x.type, static_cast<float*>(x.scale.p), x.scale.ld, w.q.p, w.q.ld, w.s.p, w.s.ld,
                       w.z.p, w.z.ld, static_cast<int>(group), bias, r.p, r.ld, static_cast<int>(number(a[5])), out.arg.p,
-                      out.arg.ld, M, N, K, stream_of(a[10])));
+                      out.arg.ld, M, N, K, current_stream()));
     return out.object();
 }
 
-// X, W1q, scales1, W3q, scales3, zeros1, zeros3, group, x_scale, out, stream
+// X, W1q, scales1, W3q, scales3, zeros1, zeros3, group, x_scale, out
 PyObject* ffn_gated_w4(Args a, Py_ssize_t n) {
-    expect<11>(n);
+    expect<10>(n);
     const at::Tensor& X = tensor(a[0], "X");
     const auto [M, K] = sizes(X, "X");
     const int64_t N = sizes(tensor(a[1], "W1q"), "W1q").first, group = group_of(a[7]), groups = (K + group - 1) / group;
@@ -250,20 +250,20 @@ PyObject* ffn_gated_w4(Args a, Py_ssize_t n) {
     Out out(a[9], "out", kBf16, M, N, X);
     check(f_ffn_gated_w4(x.x.p, x.x.ld, x.type, static_cast<float*>(x.scale.p), x.scale.ld, u.q.p, u.q.ld, u.s.p, u.s.ld,
                          u.z.p, u.z.ld, v.q.p, v.q.ld, v.s.p, v.s.ld, v.z.p, v.z.ld, static_cast<int>(group), out.arg.p,
-                         out.arg.ld, M, N, K, stream_of(a[10])));
+                         out.arg.ld, M, N, K, current_stream()));
     return out.object();
 }
 
-// X, p, seed, offset, R, out, stream
+// X, p, seed, offset, R, out
 PyObject* dropout(Args a, Py_ssize_t n) {
-    expect<7>(n);
+    expect<6>(n);
     const at::Tensor& X = tensor(a[0], "X");
     const auto [M, N] = sizes(X, "X");
     const Arg x = matrix(X, "X", kBf16, M, N), r = matrix(a[4], "R", kBf16, M, N);
     const Seed seed(a[2], a[3]);
     Out out(a[5], "out", kBf16, M, N, X);
     check(f_dropout(x.p, x.ld, r.p, r.ld, real(a[1]), seed.seed, seed.offset, seed.state, out.arg.p, out.arg.ld, M, N,
-                    stream_of(a[6])));
+                    current_stream()));
     return out.object();
 }
 
@@ -281,9 +281,9 @@ PyObject* three(PyObject* a, PyObject* b, PyObject* c) {
     return t;
 }
 
-// X, weight, R, eps, p, seed, offset, out, h, stream
+// X, weight, R, eps, p, seed, offset, out, h
 PyObject* add_rms_norm(Args a, Py_ssize_t n) {
-    expect<10>(n);
+    expect<9>(n);
     const at::Tensor& X = tensor(a[0], "X");
     const auto [M, D] = sizes(X, "X");
     const Arg x = matrix(X, "X", kBf16, M, D), r = matrix(a[2], "R", kBf16, M, D);
@@ -295,13 +295,13 @@ PyObject* add_rms_norm(Args a, Py_ssize_t n) {
     Out h(same ? a[0] : a[8], "h", kBf16, M, D, X);
     at::Tensor rstd = make({M}, at::kFloat, X);
     check(f_norm(x.p, x.ld, r.p, r.ld, w, real(a[3]), p, seed.seed, seed.offset, seed.state, same ? nullptr : h.arg.p,
-                 h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(rstd.data_ptr()), M, D, stream_of(a[9])));
+                 h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(rstd.data_ptr()), M, D, current_stream()));
     return three(out.object(), h.object(), THPVariable_Wrap(std::move(rstd)));
 }
 
-// X, weight, R, eps, scale_group, out, h, stream
+// X, weight, R, eps, scale_group, out, h
 PyObject* add_rms_norm_q8(Args a, Py_ssize_t n) {
-    expect<8>(n);
+    expect<7>(n);
     const at::Tensor& X = tensor(a[0], "X");
     const auto [M, D] = sizes(X, "X");
     const Arg x = matrix(X, "X", kBf16, M, D), r = matrix(a[2], "R", kBf16, M, D);
@@ -313,13 +313,13 @@ PyObject* add_rms_norm_q8(Args a, Py_ssize_t n) {
     at::Tensor scale = make({M, scales}, at::kFloat, X);
     check(f_norm_q8(x.p, x.ld, r.p, r.ld, w, real(a[3]), static_cast<int>(group), same ? nullptr : h.arg.p, h.arg.ld,
                     out.arg.p, out.arg.ld, static_cast<float*>(scale.data_ptr()), std::max<int64_t>(scales, 1), M, D,
-                    stream_of(a[7])));
+                    current_stream()));
     return three(out.object(), THPVariable_Wrap(std::move(scale)), h.object());
 }
 
-// dY, H, weight, rstd, dH, p, seed, offset, workspace, stream
+// dY, H, weight, rstd, dH, p, seed, offset, workspace
 PyObject* add_rms_norm_backward(Args a, Py_ssize_t n) {
-    expect<10>(n);
+    expect<9>(n);
     const at::Tensor& dY = tensor(a[0], "dY");
     const auto [M, D] = sizes(dY, "dY");
     const Arg dy = matrix(dY, "dY", kBf16, M, D), h = matrix(tensor(a[1], "H"), "H", kBf16, M, D);
@@ -345,7 +345,7 @@ PyObject* add_rms_norm_backward(Args a, Py_ssize_t n) {
     const int64_t ld = std::max<int64_t>(D, 1);
     check(f_norm_bwd(dy.p, dy.ld, h.p, h.ld, w, static_cast<const float*>(rstd), dh.p, dh.ld, p, seed.seed, seed.offset,
                      seed.state, dR.data_ptr(), ld, dX.data_ptr(), ld, static_cast<float*>(dweight.data_ptr()),
-                     workspace.data_ptr(), workspace.nbytes(), M, D, stream_of(a[9])));
+                     workspace.data_ptr(), workspace.nbytes(), M, D, current_stream()));
     PyObject* x = THPVariable_Wrap(dX);
     return three(x, p > 0.0 ? THPVariable_Wrap(dR) : Py_XNewRef(x), THPVariable_Wrap(std::move(dweight)));
 }

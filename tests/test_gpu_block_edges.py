@@ -1,0 +1,125 @@
+"""Calls around the products that were once answered wrongly, refused or unsafe, each against its definition in
+64 bits (block_ref.py)."""
+import pytest
+import torch
+
+import dense_bf16_gemm_persistent_gb300 as gb
+from tests import block_ref as ref
+from tests.block_ref import HALF_BF16, TINY, assert_within
+from tests.test_gpu_block import BF16, DEV, check_linear_result, normal, w4_input, w4_weights
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------------------------- scales of 8-bit rows
+
+def test_w4_row_scales_in_one_dimension():
+    """[M] scales, contiguous and with a stride, are the [M,1] ones."""
+    m, n, k, group = 9, 70, 288, 64
+    q, s, z = w4_weights(n, k, group, True, 1)
+    x, xs = w4_input(m, k, "row", 2)
+    xs = xs * torch.arange(1, m + 1, device=DEV)[:, None]  # (each row's own)
+    want = gb.linear_w4(x, q, s, zeros=z, group=group, x_scale=xs)
+    check_linear_result(want, x, xs, q, s, z, None, None, "none", group)
+    apart = torch.full((m, 3), float("nan"), device=DEV)
+    apart[:, 1] = xs[:, 0]
+    for scale in (xs[:, 0], xs.reshape(m).clone(), apart[:, 1]):
+        assert scale.dim() == 1
+        assert torch.equal(gb.linear_w4(x, q, s, zeros=z, group=group, x_scale=scale), want)
+    one = gb.linear_w4(x[:1], q, s, zeros=z, group=group, x_scale=xs[0].expand(1))
+    assert torch.equal(one, gb.linear_w4(x[:1], q, s, zeros=z, group=group, x_scale=xs[:1]))
+
+
+def test_w4_refuses_a_scale_expanded_over_the_rows():
+    """One element of storage for all rows: no row but the first has a scale in memory."""
+    m, k = 4, 64
+    q, s, z = w4_weights(8, k, 64, False, 1)
+    x, xs = w4_input(m, k, "row", 2)
+    for scale in (xs[0].expand(m), xs[:1].expand(m, 1)):
+        with pytest.raises((ValueError, gb.GBError), match="x_scale|ldxs"):
+            gb.linear_w4(x, q, s, group=64, x_scale=scale)
+        with pytest.raises((ValueError, gb.GBError), match="x_scale|ldxs"):
+            gb.ffn_gated_w4(x, q, s, q, s, group=64, x_scale=scale)
+
+
+# ---------------------------------------------------------------------------------- memory on a stream that is given
+
+def every_call():
+    """Name and call of every operator, each of a stream and with everything made by the call."""
+    x, w, r = normal(32, 512, seed=1), normal(96, 512, seed=2), normal(32, 96, seed=3)
+    weight, rstd = normal(512, seed=4), torch.rand(32, device=DEV) + 0.5
+    q, s, z = w4_weights(96, 512, 64, True, 5)
+    return {
+        "linear": lambda st: gb.linear(x, w, stream=st),
+        "linear split": lambda st: gb.linear(x, w, split_k=4, stream=st),
+        "linear_preact": lambda st: gb.linear_preact(x, w, act="silu", stream=st),
+        "matmul": lambda st: gb.matmul(r, w, stream=st),
+        "linear_dact": lambda st: gb.linear_dact(r, w, x, act="silu", stream=st),
+        "ffn_gated": lambda st: gb.ffn_gated(x, w, w, stream=st),
+        "ffn_gated split": lambda st: gb.ffn_gated(x, w, w, split_k=4, stream=st),
+        "linear_w4": lambda st: gb.linear_w4(x, q, s, zeros=z, group=64, stream=st),
+        "ffn_gated_w4": lambda st: gb.ffn_gated_w4(x, q, s, q, s, group=64, stream=st),
+        "dropout": lambda st: gb.dropout(x, 0.1, 5, stream=st),
+        "add_rms_norm": lambda st: gb.add_rms_norm(x, weight, x, p=0.1, seed=1, stream=st),
+        "add_rms_norm_q8": lambda st: gb.add_rms_norm_q8(x, weight, x, stream=st),
+        "add_rms_norm_backward": lambda st: gb.add_rms_norm_backward(x, x, weight, rstd, p=0.1, seed=1, stream=st),
+    }
+
+
+def tensors(result):
+    return result if isinstance(result, tuple) else (result,)
+
+
+@pytest.mark.parametrize("form", ["stream", "number"])
+def test_what_a_call_makes_is_memory_of_its_stream(form):
+    """The allocator's own record: nothing that a call on a side stream makes comes from another stream's memory."""
+    calls, side = every_call(), torch.cuda.Stream()
+    given = side if form == "stream" else side.cuda_stream
+    torch.cuda.synchronize()
+    for name, call in calls.items():
+        want = [t.clone() for t in tensors(call(None))]
+        torch.cuda.synchronize()
+        torch.cuda.memory._record_memory_history(max_entries=1000)
+        try:
+            got = tensors(call(given))
+            trace = torch.cuda.memory._snapshot()["device_traces"][torch.cuda.current_device()]
+        finally:
+            torch.cuda.memory._record_memory_history(enabled=None)
+        made = [e["stream"] for e in trace if e["action"] == "alloc"]
+        assert len(made) >= len({t.data_ptr() for t in got}) and set(made) == {side.cuda_stream}, (name, made)
+        side.synchronize()
+        for a, b in zip(got, want):
+            if a.dtype == torch.float8_e4m3fn:
+                a, b = a.view(torch.uint8), b.view(torch.uint8)
+            assert torch.equal(a, b), name
+
+
+@pytest.mark.parametrize("number", [0, 1])
+def test_default_stream_by_its_number(number):
+    x = normal(8, 64, seed=1)
+    want = gb.dropout(x, 0.3, 1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        got = gb.dropout(x, 0.3, 1, stream=number)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_workspace_of_a_busy_side_stream_is_not_given_away():
+    """The call returns long before its kernels run; what the current stream allocates and writes then is not theirs."""
+    m, d = 900, 2100
+    dy, h, w = normal(m, d, seed=1), normal(m, d, seed=2), normal(d, seed=3)
+    rstd = (h.float().square().mean(dim=1) + 1e-6).rsqrt()
+    want = [t.clone() for t in gb.add_rms_norm_backward(dy, h, w, rstd, p=0.1, seed=5)]
+    need, side = gb.add_rms_norm_backward_workspace_bytes(m, d), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+    got = gb.add_rms_norm_backward(dy, h, w, rstd, p=0.1, seed=5, stream=side)
+    gb.add_rms_norm_backward(dy, h, w, rstd, p=0.1, seed=6, stream=side)  # (its outputs are dropped at once)
+    others = [torch.full((need,), 255, dtype=torch.uint8, device=DEV) for _ in range(8)]
+    others += [torch.full((m, d), float("nan"), dtype=BF16, device=DEV) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all((t == 255).all() for t in others[:8]) and all(t.isnan().all() for t in others[8:])
