@@ -17,7 +17,7 @@
 //     sum (q - z) x = sum q x - z sum x,
 // with sum x from the same instructions in the same order on weights of 8, so that weights at the
 // zero point 8 (all there is without zeros) leave exactly nothing; weights at another zero point leave
-// 2^-24 of z s sum |x| (measured).  x becomes fp16 too: e4m3 values are fp16 values as they are, and bf16
+// 2^-24 of z s sum |x| (measured).  x becomes fp16 too: e4m3 values exactly (times 2^4), and bf16
 // values are first scaled by a power of two for each 128 columns of a token, so that the largest is in
 // [2^14, 2^15); what is then lost, below 2^-35 of the largest, is under fp32's own rounding of
 // the sum.  Products are summed in fp32 within a group, and the group's sum is multiplied by its
@@ -119,9 +119,10 @@ __device__ __forceinline__ void widen_less(uint32_t w, uint32_t zero, uint32_t (
         out[i] = *reinterpret_cast<const uint32_t*>(&v);
     }
 }
-// What the products are short of for that: 2^24, half of it in the weights' scale and half in x's
-// (so that neither overflows), and 2^-4 in the odd columns of x.
-constexpr float kHalfShift = 4096.f;
+// What the products are short of for that: 2^24, and 2^-4 in the odd columns of x.  Half of the 2^24 is
+// in the weights' scale and half in x's, so that neither overflows; the scales of e4m3 values, which
+// may be as large as 2^119, have 2^8 of theirs, and the values themselves 2^4.
+constexpr float kHalfShift = 4096.f, kX8Shift = 256.f;
 
 __device__ __forceinline__ float activate(float v, int act) {
     if (act == 1) {
@@ -235,7 +236,7 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
         for (int u = 0; u < kBatch; ++u) {
             const int at_u = i + u * stride, token = at_u / steps, step = at_u - token * steps;
             if ((at_u & ~1) >= total) break;  // (of the whole warp)
-            float v[8], scale = kHalfShift;
+            float v[8], scale = X8 ? kX8Shift : kHalfShift;
             if (X8) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -269,10 +270,10 @@ __device__ __forceinline__ bool stage_x(const Params& p, uint4* xs, float* xscal
                 scale *= __uint_as_float((254u - up) << 23);
             }
             if (at_u >= total) continue;
-            constexpr float kSixteenth = 0.0625f;
+            constexpr float kEven = X8 ? kHalfShift / kX8Shift : 1.f, kOdd = kEven / 16.f;
             xs[((step * 4 + c) * tokens + token) * 4 + lt] =
-                make_uint4(half_pair(v[0], v[4]), half_pair(v[1] * kSixteenth, v[5] * kSixteenth), half_pair(v[2], v[6]),
-                           half_pair(v[3] * kSixteenth, v[7] * kSixteenth));
+                make_uint4(half_pair(v[0] * kEven, v[4] * kEven), half_pair(v[1] * kOdd, v[5] * kOdd),
+                           half_pair(v[2] * kEven, v[6] * kEven), half_pair(v[3] * kOdd, v[7] * kOdd));
             if (at == 0 && X != kXRowScale) xscale[step * 8 * NT + token] = scale;
             if (at == 0 && X == kXRowScale && step == 0) xscale[token] = scale;
         }
@@ -710,7 +711,10 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
                                 float v = acc[r / 2][i][r % 2 * 2 + e];
                                 if (!kLess) v = fmaf(-z, __uint_as_float(sum[e]), v);
                                 float& to = total[r / 2][i][r % 2 * 2 + e];
-                                to = fmaf(kStepScale ? scale * (e ? xs1[i] : xs0[i]) : scale, v, to);
+                                // (x's scale first: at most 15 * 128 of x's largest, over 2^12, is a finite
+                                // number, where the two scales' product need not be)
+                                if (kStepScale) v *= e ? xs1[i] : xs0[i];
+                                to = fmaf(scale, v, to);
                             }
                         }
                     }

@@ -123,3 +123,32 @@ def test_workspace_of_a_busy_side_stream_is_not_given_away():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     assert all((t == 255).all() for t in others[:8]) and all(t.isnan().all() for t in others[8:])
+
+
+# ---------------------------------------------------------------------------------- sizes of x and of the scales
+
+@pytest.mark.parametrize("x8", ["no", "row", "group"])
+@pytest.mark.parametrize("m,group", [(1, 128), (5, 64), (16, 32), (12, 128)])
+@pytest.mark.parametrize("x_exp,s_exp", [(126, -20), (121, -2), (60, 58), (20, 98), (-30, 90), (-100, 90), (-115, 98)])
+def test_w4_finite_results_of_large_factors(x_exp, s_exp, m, group, x8):
+    """x near bf16's largest value, scales near 2^100: what the product of the two is, and nothing else.  Weights one
+    step from the zero point at most, so that results are finite; rows and a group of weights at it, which add nothing."""
+    n, k = 48, 800
+    g = torch.Generator(device=DEV).manual_seed(7)
+    q = torch.randint(7, 10, (n, k), generator=g, device=DEV, dtype=torch.int64)
+    q[:4] = 8
+    q[:, 128:256] = 8
+    packed = (q[:, 0::2] | q[:, 1::2] << 4).to(torch.uint8)
+    groups = -(-k // group)
+    s = ((torch.rand((n, groups), generator=g, device=DEV) + 0.5) * 2.0 ** s_exp).to(BF16)
+    v = torch.randn((m, k), generator=g, device=DEV).clamp(-1.9, 1.9)
+    if x8 == "no":
+        x, xs = (v.double() * 2.0 ** x_exp).to(BF16), None
+    else:
+        x = (v * 200).to(torch.float8_e4m3fn)
+        xs = torch.full((m, 1 if x8 == "row" else -(-k // 128)), 2.0 ** x_exp / 200, dtype=torch.float64, device=DEV).float()
+    d = gb.linear_w4(x, packed, s, group=group, x_scale=xs)
+    assert d.isfinite().all() and not d[:, :4].any()
+    check_linear_result(d, x, xs, packed, s, None, None, None, "none", group)
+    zeros = torch.full((n, groups), 8, dtype=torch.uint8, device=DEV)
+    assert torch.equal(gb.linear_w4(x, packed, s, zeros=zeros, group=group, x_scale=xs), d)
