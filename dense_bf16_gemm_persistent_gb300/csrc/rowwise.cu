@@ -14,6 +14,9 @@ using namespace gb::host;
 using namespace gb::rowwise;
 
 constexpr int kMaxNormColumns = 16384;  // 512 threads x 4 chunks of 8
+// The kernels count columns in 32 bits: a chunk's first column and 8 have to be a number of theirs, for the
+// last chunk of a row that is shifted by up to 7.
+constexpr int64_t kMaxColumns = (int64_t(1) << 31) - 16;
 
 // One matrix of a call, by its name in the messages.
 struct Mat {
@@ -207,6 +210,7 @@ gb_status_t gb_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, d
     if ((st = check_sizes(M, N)) != GB_OK) return st;
     DropoutParams prm{};
     if ((st = make_drop(p, seed, offset, rng_state, &prm.drop)) != GB_OK) return st;
+    if (N > kMaxColumns) return fail(GB_ERR_UNSUPPORTED, "rows of %" PRId64 " columns: at most 2^31 - 16", N);
     if (M == 0 || N == 0) return GB_OK;
     const Mat mats[] = {{"X", X, ldx, 2}, {"D", D, ldd, 2}, {"R", R, ldr, 2}};
     for (const Mat& m : mats)

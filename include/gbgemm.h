@@ -280,8 +280,8 @@ GB_API gb_status_t gb_gemm_ffn_gated_w4(const void* X, int64_t ldx, int x_type, 
  *   rng_state  NULL, or device memory of two 64-bit words {seed, offset} (8-byte aligned) read
  *              when the kernel runs, in the place of the two arguments: a captured graph draws
  *              new masks when the program moves the offset between replays
- * M == 0 or N == 0 is a no-op.  D == X or D == R (same pointer and leading dimension) is
- * allowed, other overlaps are not.  Rows move in 16-byte words when every matrix has its rows at
+ * M == 0 or N == 0 is a no-op; N at most 2^31 - 16.  D == X or D == R (same pointer and leading
+ * dimension) is allowed, other overlaps are not.  Rows move in 16-byte words when every matrix has its rows at
  * the same addresses modulo 16 bytes (any width), else element by element.
  */
 GB_API gb_status_t gb_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, double p, uint64_t seed,
