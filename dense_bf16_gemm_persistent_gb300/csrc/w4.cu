@@ -231,8 +231,6 @@ gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInf
         return want.cluster || want.k_warps
                    ? fail(GB_ERR_UNSUPPORTED, "no plan has the configured w4_cluster and w4_k_warps")
                    : fail(GB_ERR_UNSUPPORTED, "K=%" PRId64 " is too large", pr.k);
-    if (ceil_div(pr.m, out->tokens) > 65535)
-        return fail(GB_ERR_UNSUPPORTED, "M=%" PRId64 " is too large for the few-token product", pr.m);
     return GB_OK;
 }
 
@@ -267,8 +265,6 @@ gb_status_t run(const Problem& pr, void* stream) {
 
     Params prm;
     memset(&prm, 0, sizeof prm);
-    prm.x = pr.x;
-    prm.x_scale = pr.x_scale;
     prm.ldx = pr.ldx;
     prm.ldxs = pr.ldxs;
     for (int i = 0; i < 2; ++i) {
@@ -289,11 +285,8 @@ gb_status_t run(const Problem& pr, void* stream) {
             prm.wide_scales = 0;
     }
     prm.bias = static_cast<const uint16_t*>(pr.bias);
-    prm.r = static_cast<const uint16_t*>(pr.r);
-    prm.d = static_cast<uint16_t*>(pr.d);
     prm.ldr = pr.ldr;
     prm.ldd = pr.ldd;
-    prm.m = static_cast<int>(pr.m);
     prm.n = static_cast<int>(pr.n);
     prm.k = static_cast<int>(pr.k);
     prm.act = pr.act;
@@ -303,7 +296,17 @@ gb_status_t run(const Problem& pr, void* stream) {
     prm.k_warps = pl.k_warps;
     prm.tokens = pl.tokens;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return pr.gated ? launch_g<true>(prm, pl, pr.group, dev, info, s) : launch_g<false>(prm, pl, pr.group, dev, info, s);
+    // a launch has at most 65535 passes
+    const int64_t most = int64_t(65535) * pl.tokens, x_bytes = pr.x_type == GB_X_BF16 ? 2 : 1;
+    for (int64_t at = 0; at < pr.m && st == GB_OK; at += most) {
+        prm.m = static_cast<int>(std::min(pr.m - at, most));
+        prm.x = static_cast<const uint8_t*>(pr.x) + at * pr.ldx * x_bytes;
+        prm.x_scale = pr.x_scale ? pr.x_scale + at * pr.ldxs : nullptr;
+        prm.r = pr.r ? static_cast<const uint16_t*>(pr.r) + at * pr.ldr : nullptr;
+        prm.d = static_cast<uint16_t*>(pr.d) + at * pr.ldd;
+        st = pr.gated ? launch_g<true>(prm, pl, pr.group, dev, info, s) : launch_g<false>(prm, pl, pr.group, dev, info, s);
+    }
+    return st;
 }
 
 }  // namespace

@@ -181,3 +181,25 @@ def test_dropout_of_the_longest_row(offset, p, residual):
             keep = torch.stack([torch.from_numpy((w >= round(p * 2 ** 32))) for w in words], dim=1).reshape(-1)
             keep = keep[:min(64, n - first)].to(DEV)
             assert torch.equal(out[0, first:first + keep.numel()] != 0, keep)
+
+
+# ---------------------------------------------------------------------------------- many tokens
+
+@pytest.mark.parametrize("x8", ["no", "row", "group"])
+@pytest.mark.parametrize("m", [(1 << 20) - 1, (1 << 20) + 35])
+def test_w4_more_tokens_than_one_launch_has_passes_for(m, x8):
+    n, k, group = 9, 160, 32
+    q, s, z = w4_weights(n, k, group, True, 1)
+    x, xs = w4_input(m, k, x8, 2)
+    r = normal(m, n, seed=3)
+    d = gb.linear_w4(x, q, s, R=r, zeros=z, group=group, x_scale=xs)
+    check_linear_result(d, x, xs, q, s, z, None, r, "none", group)
+    d = gb.ffn_gated_w4(x, q, s, q, s, zeros1=z, group=group, x_scale=xs)
+    few = gb.ffn_gated_w4(x[-40:], q, s, q, s, zeros1=z, group=group, x_scale=None if xs is None else xs[-40:])
+    a, off_a = ref.w4_products(x, xs, ref.unpack_w4(q, s, z, group, k))
+    b, off_b = ref.w4_products(x, xs, ref.unpack_w4(q, s, None, group, k))
+    gate = ref.act(a, "silu")
+    tol = (1.13 * off_a + 2.0 ** -20 * a.abs()) * (b.abs() + off_b) + gate.abs() * off_b
+    tol = tol * (1 + HALF_BF16) + HALF_BF16 * (gate * b).abs() + TINY
+    assert_within(d, gate * b, tol)
+    assert_within(few, (gate * b)[-40:], tol[-40:])
