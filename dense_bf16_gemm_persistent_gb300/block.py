@@ -52,7 +52,7 @@ def linear_w4(X: torch.Tensor, Wq: torch.Tensor, scales: torch.Tensor, bias: tor
 
     X [M,K] bf16, or float8_e4m3fn with x_scale ([M] or [M,1]: a row's; [M,ceil(K/128)]: of 128 columns); Wq
     [N,K/2] uint8 (the low nibble is the even column); scales [N,ceil(K/group)] bf16; zeros uint8 of the same
-    shape (None: 8); bias [N], R [M,N] as in linear()."""
+    shape, their low four bits (None: 8); bias [N], R [M,N] as in linear()."""
     if stream is not None:
         return _on(stream, linear_w4, X, Wq, scales, bias, R, act, zeros, group, x_scale, out)
     if act not in ACT:

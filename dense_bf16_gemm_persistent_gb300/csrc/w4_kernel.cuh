@@ -321,7 +321,7 @@ __device__ __noinline__ float odd_part(const Params& p, int from, int64_t n, int
             const uint32_t x = static_cast<const uint16_t*>(p.x)[token * p.ldx + col];
             if ((x >> 7 & 0xff) != 0xff) continue;
             const int q = p.q[from][n * p.ldq[from] + col / 2] >> (4 * (col & 1)) & 15;
-            const int z = p.z[from] ? p.z[from][n * p.ldz[from] + col / G] : 8;
+            const int z = p.z[from] ? p.z[from][n * p.ldz[from] + col / G] & 15 : 8;
             const float s = __uint_as_float(static_cast<uint32_t>(p.s[from][n * p.lds[from] + col / G]) << 16);
             sum += __uint_as_float(x << 16) * (static_cast<float>(q - z) * s);
         }
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
             __syncwarp();  // (every lane is done with the last unit)
 #pragma unroll
             for (int i = 0; i < kGroups; ++i) {
-                const uint32_t pair = raw.s[i / 2], z = raw.z[i / 4] >> (8 * (i & 3)) & 0xff;
+                const uint32_t pair = raw.s[i / 2], z = raw.z[i / 4] >> (8 * (i & 3)) & 15;
                 const float scale = __uint_as_float(i & 1 ? pair & 0xffff0000u : pair << 16) * kHalfShift;
                 store_shared(scales_of_warp + i * 128 + (lane & 7) * 16 + (lane >> 3) * 4,
                              __float_as_uint(scale) | __float_as_uint(static_cast<float>(z)) >> 16);

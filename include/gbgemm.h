@@ -237,7 +237,8 @@ GB_API gb_status_t gb_gemm_linear_dact(const void* dY, int64_t lddy, const void*
  *           q[n,2j], the high one q[n,2j+1]
  *   scales  [N,ceil(K/group)] bf16 (lds elements), below 2^100 in size (a group's integers are
  *           summed first, then times X's scale, then times this: no factor overflows before D does)
- *   zeros   [N,ceil(K/group)] bytes of 0..15 (ldz bytes), or NULL: z = 8 everywhere
+ *   zeros   [N,ceil(K/group)] bytes (ldz bytes) of which the low four bits are z, or NULL:
+ *           z = 8 everywhere
  *   group   32, 64 or 128 columns; the last group of a row may be shorter
  *   bias, R, act, D  as gb_gemm_linear (any 2-byte alignment and leading dimension)
  * K a multiple of 32; Wq's base and ldq multiples of 16 bytes (16-byte loads).  The weights are

@@ -203,3 +203,25 @@ def test_w4_more_tokens_than_one_launch_has_passes_for(m, x8):
     tol = tol * (1 + HALF_BF16) + HALF_BF16 * (gate * b).abs() + TINY
     assert_within(d, gate * b, tol)
     assert_within(few, (gate * b)[-40:], tol[-40:])
+
+
+# ---------------------------------------------------------------------------------- zero points
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m", [1, 8, 12])
+def test_w4_zero_points_are_the_low_four_bits(m, group):
+    """In every variant (z off the sums, z off each weight, infinities added one by one): the same as without the rest."""
+    n, k = 70, 416
+    q, s, z = w4_weights(n, k, group, True, 1)
+    high = torch.randint(0, 16, z.shape, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV).to(torch.uint8) << 4
+    x, r = normal(m, k, seed=3), normal(m, n, seed=4)
+    for odd in (False, True):
+        if odd:
+            x[0, 7] = float("inf")
+        want = gb.linear_w4(x, q, s, R=r, zeros=z, group=group)
+        assert torch.equal(gb.linear_w4(x, q, s, R=r, zeros=z | high, group=group).nan_to_num(), want.nan_to_num())
+        pair = gb.ffn_gated_w4(x, q, s, q, s, zeros1=z, zeros3=z, group=group)
+        got = gb.ffn_gated_w4(x, q, s, q, s, zeros1=z | high, zeros3=z | high, group=group)
+        assert torch.equal(got.nan_to_num(), pair.nan_to_num())
+    check_linear_result(gb.linear_w4(x[1:], q, s, zeros=z | high, group=group) if m > 1 else want[1:], x[1:], None, q, s, z,
+                        None, None, "none", group)
