@@ -138,7 +138,7 @@ struct Config {
     // L2 eviction hints for the TMA traffic of A, B, R and D (and Z): -1 = default,
     // 0 = none, 1 = evict first, 2 = evict last
     int hint_a = -1, hint_b = -1, hint_r = -1, hint_d = -1;
-    int mc = -1;         // A multicast between two CTA pairs (4-CTA clusters): -1 auto, 0 off, 1 on
+    int mc = -1;         // two CTA pairs to a cluster, on neighbouring tile-columns: -1 auto, 0 off, 1 on
     int issue = -1;      // MMA issue loop: -1 auto, 0 rebuild, 1 lean, 2 lean with look-ahead wait
     int prod = 0;        // producer threads: 0 auto, 1 or 2 (A and B loads issued by different warps)
     int r_async = -1;    // unaligned R rows (no split): -1 auto, 0 synchronous loads at use, 1 cp.async queue
@@ -276,7 +276,7 @@ struct Variant {
                 if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
                 if (n < 1) return fail(GB_ERR_UNSUPPORTED, "no CTA pair fits on this device");
                 units[dev] = n;
-                // clusters of two CTA pairs (A multicast); 0 if none fits
+                // clusters of two CTA pairs; 0 if none fits
                 attr[0].val.clusterDim.x = 4;
                 cfg.gridDim = dim3(4 * (info.sms / 4), 1, 1);
                 int n4 = 0;
@@ -490,8 +490,8 @@ gb_status_t plan_and_launch(const Problem& pr, const Config& cfg, int bn, int de
     prm.num_m_blocks = static_cast<int32_t>(cdiv(pr.m, V::kTileM));
     prm.num_n_blocks = static_cast<int32_t>(cdiv(pr.n, bn));
     prm.num_k_blocks = static_cast<int32_t>(cdiv(pr.k, gb::kBK));
-    // A multicast between two CTA pairs: on request, for CTA-pair variants without a
-    // split, when 4-CTA clusters fit; a work item is then one tile-row x two tile-columns.
+    // Two CTA pairs to a cluster: on request, for CTA-pair variants without a split, when
+    // 4-CTA clusters fit; a work item is then one tile-row x two tile-columns.
     const bool mc = V::kPair && V::kEpi != 4 && cfg.mc == 1 && max_units_mc > 0 && !(sr.allowed) && pr.k > 0;
     prm.mc = mc ? 1 : 0;
     prm.sched_n_blocks = mc ? static_cast<int32_t>(cdiv(prm.num_n_blocks, 2)) : prm.num_n_blocks;
@@ -640,8 +640,8 @@ gb_status_t plan_and_launch(const Problem& pr, const Config& cfg, int bn, int de
         if ((st = make_tmap(&prm.tm_a, pr.a, pr.k, pr.m, pr.lda * 2, gb::kBK, gb::kBM, CU_TENSOR_MAP_SWIZZLE_128B)) !=
             GB_OK)
             return st;
-        if ((mc || prm.prod == 3) && (st = make_tmap(&prm.tm_a_half, pr.a, pr.k, pr.m, pr.lda * 2, gb::kBK, gb::kBM / 2,
-                                                    CU_TENSOR_MAP_SWIZZLE_128B)) != GB_OK)
+        if (prm.prod == 3 && (st = make_tmap(&prm.tm_a_half, pr.a, pr.k, pr.m, pr.lda * 2, gb::kBK, gb::kBM / 2,
+                                             CU_TENSOR_MAP_SWIZZLE_128B)) != GB_OK)
             return st;
         if (pr.b_mn) {
             // B [k rows (contraction), n columns]: boxes of 64 columns x 64 rows

@@ -162,10 +162,9 @@ struct GemmParams {  // the CUtensorMap members give it their 64-byte alignment
     // L2 eviction hints (l2_policy codes: 0 none, 1 evict first, 2 evict last) for the
     // TMA loads of A, of B (W1/W3), of R, and the TMA stores of D and Z.
     uint32_t hint_a, hint_b, hint_r, hint_d;
-    // A multicast between two CTA pairs (4-CTA clusters, CTA-pair variants only): a work
-    // item is one tile-row x 2 tile-columns; pair q of the cluster computes tile-column
-    // 2 * item + q, and each CTA loads half of its A tile and multicasts it to the CTA
-    // of the other pair that needs the same rows (tm_a_half: box {64, 64}).
+    // Two CTA pairs to a cluster (4-CTA clusters, CTA-pair variants only): a work item is
+    // one tile-row x 2 tile-columns; pair q of the cluster computes tile-column 2 * item + q.
+    // Each pair loads its own operands: the two read the same A tile at the same time.
     int32_t mc;
     int32_t sched_n_blocks;  // tile-columns of the work-item grid (num_n_blocks, or half of it with mc)
     // MMA issue loop: 0 descriptors rebuilt per k-block; 1 lean (descriptors advanced
@@ -326,8 +325,8 @@ __device__ __forceinline__ void tile_coords(int32_t tile, const GemmParams& p, i
     if (group & 1) nb = p.sched_n_blocks - 1 - nb;
 }
 
-// The tile this CTA computes for work-item tile index `tile`: with A multicast, pair
-// `pairi` of the cluster takes tile-column 2 * item-column + pairi.
+// The tile this CTA computes for work-item tile index `tile`: with two pairs to a cluster,
+// pair `pairi` takes tile-column 2 * item-column + pairi.
 __device__ __forceinline__ void work_tile(int32_t tile, const GemmParams& p, uint32_t pairi, int32_t& mb,
                                           int32_t& nb) {
     tile_coords(tile, p, mb, nb);
@@ -817,9 +816,8 @@ __device__ __forceinline__ void stage_descs(uint32_t ring0, uint32_t slot, uint3
 // The MMA issuer's loop over one item's k-blocks for the common operand forms: the
 // descriptor steps, the instruction descriptor and the commit mask are compile-time
 // constants, and nothing but the stage wait runs between k-blocks.  `s`, `ph` and `it`
-// carry the ring position across items (it == 0: nothing consumed yet).  Without A
-// multicast the cluster is the CTA pair itself, so the stage is freed in ranks 0 and 1
-// (kMask 0x3); with A multicast between two pairs, in all four CTAs (0xF).
+// carry the ring position across items (it == 0: nothing consumed yet).  The stage is freed in
+// both CTAs of the pair: ranks 0 and 1 (kMask 0x3), or 2 and 3 for the second pair of a cluster (0xC).
 // Returns false if a wait gave up.
 template <int CG, uint32_t kStageBytes, uint32_t kABytes, uint32_t kIdescK, bool BMN, uint16_t kMask = 0x3>
 __device__ __forceinline__ bool issue_kblocks(uint32_t d_tmem, int32_t nkb, uint64_t* full, uint64_t* empty,
@@ -991,7 +989,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
 #endif
     const uint32_t crank = PAIR ? cluster_ctarank() : 0u;  // position in the cluster (pair, or two pairs)
     const uint32_t rank = crank & 1u;                      // position in the CTA pair
-    const uint32_t pairi = crank >> 1;                     // which pair of the cluster (A multicast)
+    const uint32_t pairi = crank >> 1;                     // which pair of the cluster
     const uint32_t lead = crank & ~1u;                     // cluster rank of this pair's leader
     const bool leader = rank == 0;
     const bool mc = PAIR && p.mc != 0;
@@ -1007,8 +1005,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < stages; ++s) {
             mbar_init(smem_addr(&full[s]), 1);
-            // with A multicast a stage is free once both pairs' MMAs have read it
-            mbar_init(smem_addr(&empty[s]), mc ? 2 : 1);
+            mbar_init(smem_addr(&empty[s]), 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&ctl->acc_full[b]), 1);
@@ -1026,7 +1023,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
     }
     if (warp == 0 && lane == 0) {
         if (p.num_k_blocks > 0) {
-            tma_prefetch_desc(mc ? &p.tm_a_half : &p.tm_a);
+            tma_prefetch_desc(&p.tm_a);
             tma_prefetch_desc(&p.tm_b0);
             if (NUM_B == 2) tma_prefetch_desc(&p.tm_b1);
         }
@@ -1064,7 +1061,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
             // the leader's expected byte count), warp 2 the B tile.  Both wait for the stage
             // to be free; the full barrier completes when all of the stage's bytes have landed.
             // prod == 3: warps 0 and 2 load the upper and lower halves of the A tile, warp 3 B
-            const bool split_a = p.prod == 3 && !mc;
+            const bool split_a = p.prod == 3;
             const bool do_a = warp == 0 || (split_a && warp == 2);
             const bool do_b = p.prod == 1 || (p.prod == 2 && (warp == 2 || (b_par && warp == 3))) ||
                               (p.prod == 3 && warp == 3);
@@ -1076,19 +1073,15 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                 const uint64_t pol_a = l2_policy(p.hint_a);
                 const uint64_t pol_b = l2_policy(p.hint_b);
                 TraceAcc tr_empty;
-                // Lean loop for the common form (K-major B, A by warp 0 and B by warp 2, no A
-                // multicast, no test hook): per k-block only the stage wait, the byte count and
-                // this thread's one box, with the box's map, rows and offset fixed per tile.
+                // Lean loop for the common form (K-major B, A by warp 0 and B by warp 2, no test
+                // hook): per k-block only the stage wait, the byte count and this thread's one box, with the box's map, rows and offset fixed per tile.
                 // Measured on GB300: the same loads issued from the general loop below, which
                 // branches per k-block on those options, leave the tensor pipe idle longer (MLP
                 // launch 0.678 -> 0.601 ms with this loop alone, one CTA pair 1.69 -> 1.44 ms).
-                const bool lean_loads = !mc && !(p.flags & kFlagBMn) && p.prod == 2 && p.inject == 0;
+                const bool lean_loads = !(p.flags & kFlagBMn) && p.prod == 2 && p.inject == 0;
                 // the same for an MN-major B (two boxes per stage; warps 2 and 3 take the B
                 // boxes of alternate stages)
-                const bool lean_mn = !mc && b_par && NUM_B == 1 && p.inject == 0;
-                // and with A multicast between two pairs (4-CTA clusters): warp 0 loads its
-                // 64-row half of the A tile into its own and the other pair's same-rank CTA
-                const bool lean_mc = mc && !(p.flags & kFlagBMn) && p.prod == 2 && p.inject == 0;
+                const bool lean_mn = b_par && NUM_B == 1 && p.inject == 0;
                 const bool is_a = warp == 0;
                 for (int32_t w = unit; lean_loads && ok && w < num_work; w += units, ++local) {
                     const int32_t tile = w / p.splits;
@@ -1161,41 +1154,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                         }
                     }
                 }
-                if constexpr (PAIR) {
-                    const uint16_t mc_mask = static_cast<uint16_t>((1u << rank) | (1u << (2 + rank)));
-                    for (int32_t w = unit; lean_mc && ok && w < num_work; w += units, ++local) {
-                        const int32_t tile = w / p.splits;
-                        const int32_t kb0 = (w - tile * p.splits) * p.kb_per_split;
-                        const int32_t nkb = min(p.num_k_blocks - kb0, p.kb_per_split);
-                        int32_t mb, nb;
-                        work_tile(tile, p, pairi, mb, nb);
-                        const bool reverse = p.zigzag && (local & 1);
-                        const CUtensorMap* map = is_a ? &p.tm_a_half : (NUM_B == 2 && !leader) ? &p.tm_b1 : &p.tm_b0;
-                        const int32_t row = is_a ? mb * S::kTileM + static_cast<int32_t>(rank) * kBM +
-                                                       static_cast<int32_t>(pairi) * (kBM / 2)
-                                                 : nb * BN + (NUM_B == 1 ? static_cast<int32_t>(rank) * S::kBRows : 0);
-                        const uint32_t off = is_a ? pairi * (S::kABytes / 2) : static_cast<uint32_t>(S::kABytes);
-                        for (int32_t kk = 0; kk < nkb; ++kk, ++it) {
-                            const int32_t kb = kb0 + (reverse ? nkb - 1 - kk : kk);
-                            if (it > 0 && ++s == stages) {
-                                s = 0;
-                                ph ^= 1u;
-                            }
-                            if (!wait_bar<kRingSuspendNs>(smem_addr(&empty[s]), ph ^ 1u, abort_flag, p.timeout_ns, kRoleProducer, s,
-                                                          &tr_empty)) {
-                                ok = false;
-                                break;
-                            }
-                            const uint32_t own_full = smem_addr(&full[s]);
-                            if (leader && is_a) mbar_arrive_expect_tx(own_full, S::kTxBytes);
-                            const uint32_t dst = smem_addr(ring + s * S::kStageBytes) + off;
-                            const uint32_t fb = mapa_shared(own_full, lead);
-                            if (is_a) tma_load_2d_pair_multicast(dst, map, fb, kb * kBK, row, mc_mask);
-                            else tma_load_op<true>(dst, map, fb, kb * kBK, row, pol_b);
-                        }
-                    }
-                }
-                for (int32_t w = unit; !lean_loads && !lean_mn && !lean_mc && ok && w < num_work; w += units, ++local) {
+                for (int32_t w = unit; !lean_loads && !lean_mn && ok && w < num_work; w += units, ++local) {
                     const int32_t tile = w / p.splits;
                     const int32_t kb0 = (w - tile * p.splits) * p.kb_per_split;
                     const int32_t nkb = min(p.num_k_blocks - kb0, p.kb_per_split);
@@ -1223,14 +1182,6 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                         const uint32_t own_full = smem_addr(&full[s]);
                         if (leader && warp == 0) mbar_arrive_expect_tx(own_full, S::kTxBytes);
                         uint8_t* sb = st + S::kABytes;
-                        if (mc && do_a) {
-                            // A multicast: this CTA loads rows [pairi * 64, +64) of its 128-row A
-                            // tile into that offset of its own and the other pair's same-rank CTA
-                            const uint32_t fb = mapa_shared(own_full, lead);
-                            tma_load_2d_pair_multicast(smem_addr(st + pairi * (S::kABytes / 2)), &p.tm_a_half, fb,
-                                                       kb * kBK, a_row + static_cast<int32_t>(pairi) * (kBM / 2),
-                                                       static_cast<uint16_t>((1u << rank) | (1u << (2 + rank))));
-                        }
                         if (NUM_B == 1 && (p.flags & kFlagBMn)) {
                             // MN-major B (a row-major [K, N] matrix): boxes of 64 output columns
                             // x 64 contraction rows, one after the other along N
@@ -1239,7 +1190,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                                 const int32_t half = warp == 0 ? 0 : 1;
                                 tma_load_op<PAIR>(smem_addr(st + half * (S::kABytes / 2)), &p.tm_a_half, fb, kb * kBK,
                                                   a_row + half * (kBM / 2), pol_a);
-                            } else if (!mc && do_a) {
+                            } else if (do_a) {
                                 tma_load_op<PAIR>(smem_addr(st), &p.tm_a, fb, kb * kBK, a_row, pol_a);
                             }
                             if (do_b) {
@@ -1254,7 +1205,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                                 const int32_t half = warp == 0 ? 0 : 1;
                                 tma_load_op<true>(smem_addr(st + half * (S::kABytes / 2)), &p.tm_a_half, fb, kb * kBK,
                                                   a_row + half * (kBM / 2), pol_a);
-                            } else if (!mc && do_a) {
+                            } else if (do_a) {
                                 tma_load_op<true>(smem_addr(st), &p.tm_a, fb, kb * kBK, a_row, pol_a);
                             }
                             if (do_b) {
@@ -1343,7 +1294,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                         const bool kb_ok =
                             b_mn ? issue_kblocks<CG, S::kStageBytes, S::kABytes, S::kIdesc, true>(
                                        d_tmem, nkb, full, empty, ring, stages, s, ph, it, abort_flag, p.timeout_ns, tr_full, issued)
-                            : mc ? issue_kblocks<CG, S::kStageBytes, S::kABytes, S::kIdesc, false, 0xF>(
+                            : lead ? issue_kblocks<CG, S::kStageBytes, S::kABytes, S::kIdesc, false, 0xC>(
                                        d_tmem, nkb, full, empty, ring, stages, s, ph, it, abort_flag, p.timeout_ns, tr_full, issued)
                                  : issue_kblocks<CG, S::kStageBytes, S::kABytes, S::kIdesc, false>(
                                        d_tmem, nkb, full, empty, ring, stages, s, ph, it, abort_flag, p.timeout_ns, tr_full, issued);
@@ -1361,7 +1312,7 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                         // fence run while this k-block's third MMA executes.
                         if (!issue_tile_lean<CG, S::kStageBytes, S::kABytes>(
                                 p, d_tmem, nkb, full, empty, ring, stages, s, ph, it, b_mn, idesc, bstep,
-                                mc ? static_cast<uint16_t>(0xF) : pair_mask, abort_flag, p.timeout_ns, tr_full, issued)) {
+                                pair_mask, abort_flag, p.timeout_ns, tr_full, issued)) {
                             ok = false;
                             break;
                         }
@@ -1419,9 +1370,8 @@ __global__ void __launch_bounds__(128 * (1 + EPI), 1) gemm_persistent_kernel(con
                                             bdesc3, idesc, kk > 0 ? 1u : 0u);
                         }
                         issued = true;
-                        // the stage is free in this pair (and, with A multicast, in the other pair's
-                        // view too: its producers write A halves into this pair's stage)
-                        if constexpr (PAIR) mma_commit_multicast2(smem_addr(&empty[s]), mc ? 0xF : pair_mask);
+                        // the stage is free in this pair
+                        if constexpr (PAIR) mma_commit_multicast2(smem_addr(&empty[s]), pair_mask);
                         else mma_commit<1>(smem_addr(&empty[s]));
                     }
                     if (!ok) break;

@@ -117,20 +117,6 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* tmap,
         : "memory");
 }
 
-// As tma_load_2d_pair, multicast: the box lands at the same shared-memory offset
-// in every CTA of the cluster whose bit is set in `cta_mask`, and each destination's
-// byte count is signalled on the mbarrier at `bar`'s offset in that destination's
-// pair leader (`bar` is the issuing CTA's pair-leader barrier, a shared::cluster
-// address from mapa).
-__device__ __forceinline__ void tma_load_2d_pair_multicast(uint32_t dst, const void* tmap, uint32_t bar, int32_t c0,
-                                                           int32_t c1, uint16_t cta_mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster.cta_group::2"
-        " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "h"(cta_mask)
-        : "memory");
-}
-
 // Untiled bulk copy global -> this CTA's shared memory (both addresses 16-byte
 // aligned, size a multiple of 16), completion counted in bytes on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {

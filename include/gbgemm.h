@@ -424,8 +424,8 @@ GB_API const char* gb_last_error(void);
  * boxes, 2 = 32x64 D and 32x32 R boxes; -1 = auto: 1, or 2 on the lean
  * kernel), r_async (R rows that are not 16-byte aligned, without split: 1 =
  * per-lane cp.async word copies into a prefetch queue, 0 or -1 = synchronous
- * loads at use), mc (1 = A multicast between two CTA pairs in 4-CTA clusters,
- * without split), issue (MMA issue loop variant 0..3), prod (producer threads:
+ * loads at use), mc (1 = two CTA pairs on neighbouring tile-columns to a 4-CTA
+ * cluster, without split), issue (MMA issue loop variant 0..3), prod (producer threads:
  * 1, 2 or 3; the lean loads need 2),
  * hint_a, hint_b, hint_r, hint_d (L2 eviction policy of the TMA loads of A,
  * of B / W1 / W3, of R, and of the TMA stores of D and Z: 0 = none, 1 = evict
