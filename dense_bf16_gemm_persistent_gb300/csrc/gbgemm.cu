@@ -83,6 +83,12 @@ void note_plan(const char* fmt, long long a, long long b, long long c, long long
     t_note = PlanNote{fmt, {a, b, c, d, e, f}};
 }
 
+void note_empty() {
+    t_plan = "empty (no launch)";
+    t_plan_rec.valid = false;
+    t_note.fmt = nullptr;
+}
+
 // ---------------------------------------------------------------- device properties
 
 static std::mutex g_dev_mu;
@@ -748,9 +754,7 @@ gb_status_t run(const Problem& pr, void* stream_ptr, const SplitReq& sr = SplitR
     gb_status_t st = validate(pr);
     if (st != GB_OK) return st;
     if (pr.m == 0 || pr.n == 0) {
-        t_plan = "empty (no launch)";
-        t_plan_rec.valid = false;
-        t_note.fmt = nullptr;
+        gb::host::note_empty();
         if (sr.query_only) *sr.ws_needed = 0;
         return GB_OK;
     }
@@ -1108,9 +1112,7 @@ gb_status_t gb_gemm_linear_splitk_noalloc(const void* A, int64_t lda, const void
     gb_status_t st = validate(pr);
     if (st != GB_OK) return st;
     if (pr.m == 0 || pr.n == 0) {
-        t_plan = "empty (no launch)";
-        t_plan_rec.valid = false;
-        t_note.fmt = nullptr;
+        gb::host::note_empty();
         return GB_OK;
     }
     int dev = 0;

@@ -39,6 +39,8 @@ W4Override w4_override();
 
 // What gb_last_plan() reports: a static format that takes six %lld.
 void note_plan(const char* fmt, long long a, long long b, long long c, long long d, long long e, long long f);
+// The same of a call that had nothing to do.
+void note_empty();
 
 // A launch whose CTAs may be set up while the kernel before it in the stream still runs: the kernel
 // must wait (ptx.cuh: wait_for_earlier_kernels) before it touches global memory.

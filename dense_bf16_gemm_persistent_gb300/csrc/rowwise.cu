@@ -211,7 +211,10 @@ gb_status_t gb_dropout(const void* X, int64_t ldx, const void* R, int64_t ldr, d
     DropoutParams prm{};
     if ((st = make_drop(p, seed, offset, rng_state, &prm.drop)) != GB_OK) return st;
     if (N > kMaxColumns) return fail(GB_ERR_UNSUPPORTED, "rows of %" PRId64 " columns: at most 2^31 - 16", N);
-    if (M == 0 || N == 0) return GB_OK;
+    if (M == 0 || N == 0) {
+        note_empty();
+        return GB_OK;
+    }
     const Mat mats[] = {{"X", X, ldx, 2}, {"D", D, ldd, 2}, {"R", R, ldr, 2}};
     for (const Mat& m : mats)
         if ((m.p || m.name[0] != 'R') && (st = check_mat(m, N)) != GB_OK) return st;
@@ -248,7 +251,10 @@ gb_status_t gb_add_rms_norm(const void* X, int64_t ldx, const void* R, int64_t l
     NormParams prm{};
     if ((st = make_drop(p, seed, offset, rng_state, &prm.drop)) != GB_OK) return st;
     if (!(eps >= 0.0 && std::isfinite(eps))) return fail(GB_ERR_INVALID_ARG, "eps=%g is not a finite number >= 0", eps);
-    if (M == 0 || D == 0) return GB_OK;
+    if (M == 0 || D == 0) {
+        note_empty();
+        return GB_OK;
+    }
     const Mat mats[] = {{"X", X, ldx, 2}, {"Y", Y, ldy, 2}, {"R", R, ldr, 2}, {"H", H, ldh, 2}};
     for (const Mat& m : mats)
         if ((m.p || m.name[0] == 'X' || m.name[0] == 'Y') && (st = check_mat(m, D)) != GB_OK) return st;
@@ -292,7 +298,10 @@ gb_status_t gb_add_rms_norm_q8(const void* X, int64_t ldx, const void* R, int64_
     if (!(eps >= 0.0 && std::isfinite(eps))) return fail(GB_ERR_INVALID_ARG, "eps=%g is not a finite number >= 0", eps);
     if (scale_group != 0 && scale_group != kScaleGroup)
         return fail(GB_ERR_INVALID_ARG, "scale_group=%d: 0 (a scale for each row) or %d columns", scale_group, kScaleGroup);
-    if (M == 0 || D == 0) return GB_OK;
+    if (M == 0 || D == 0) {
+        note_empty();
+        return GB_OK;
+    }
     const Mat mats[] = {{"X", X, ldx, 2}, {"Q", Q, ldq, 1}, {"R", R, ldr, 2}, {"H", H, ldh, 2}};
     for (const Mat& m : mats)
         if ((m.p || m.name[0] == 'X' || m.name[0] == 'Q') && (st = check_mat(m, D)) != GB_OK) return st;
@@ -350,7 +359,10 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
     if ((st = check_sizes(M, D)) != GB_OK) return st;
     NormBwdParams prm{};
     if ((st = make_drop(p, seed, offset, rng_state, &prm.drop)) != GB_OK) return st;
-    if (D == 0) return GB_OK;
+    if (D == 0) {
+        note_empty();
+        return GB_OK;
+    }
     const bool drop = p > 0.0;
     if ((st = check_ptr("dweight", dweight, 4)) != GB_OK) return st;
     const Mat mats[] = {{"dY", dY, lddy, 2}, {"H", H, ldh, 2}, {"dR", dR, lddr, 2}, {"dH", dH, lddh, 2},
@@ -368,6 +380,7 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     int blocks = 0;
+    RowPlan pl;
     if (M > 0) {
         const size_t need = static_cast<size_t>(bwd_workspace(M, D, info.sms));
         if (!workspace || workspace_bytes < need)
@@ -389,7 +402,7 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
         prm.lddx = lddx;
         prm.m = static_cast<int>(M);
         prm.d = static_cast<int>(D);
-        const RowPlan pl = plan_rows(mats, M, D);
+        pl = plan_rows(mats, M, D);
         prm.wide = pl.wide;
         prm.wide_weight = aligned_to(weight, 16);
         blocks = bwd_blocks(M, pl, info.sms);
@@ -399,9 +412,9 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
             default: st = run_bwd<kState>(prm, pl, blocks, dev, info, s); break;
         }
         if (st != GB_OK) return st;
-        note_plan("kernel=add_rms_norm_backward blocks=%lld dropout=%lld threads=%lld rows=%lld chunks=%lld wide=%lld",
-                  blocks, drop, pl.threads, pl.rows, pl.chunks_per_thread, pl.wide);
     }
+    note_plan("kernel=add_rms_norm_backward blocks=%lld dropout=%lld threads=%lld rows=%lld chunks=%lld wide=%lld", blocks,
+              drop, pl.threads, pl.rows, pl.chunks_per_thread, pl.wide);
     return Launch(static_cast<unsigned>(ceil_div(D, kJoinColumns)), dim3(kJoinColumns, kJoinParts), 0, s)(
         "add_rms_norm_backward join launch", join_kernel, static_cast<const float*>(workspace), blocks, static_cast<int>(D),
         dweight);

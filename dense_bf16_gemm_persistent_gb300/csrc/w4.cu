@@ -236,7 +236,11 @@ gb_status_t make_plan(const Problem& pr, int64_t tiles, int dev, const DeviceInf
 
 gb_status_t run(const Problem& pr, void* stream) {
     gb_status_t st = validate(pr);
-    if (st != GB_OK || pr.m == 0 || pr.n == 0) return st;
+    if (st != GB_OK) return st;
+    if (pr.m == 0 || pr.n == 0) {
+        note_empty();
+        return GB_OK;
+    }
     int dev = 0;
     DeviceInfo info;
     if ((st = device_info(&dev, &info)) != GB_OK) return st;

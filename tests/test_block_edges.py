@@ -1,7 +1,10 @@
 """Calls around the products that were once accepted or answered wrongly, as far as the CPU shows it."""
+import ctypes
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 
-from tests.test_block_abi import GB_ERR_UNSUPPORTED, L, drop  # noqa: F401
+from tests.test_block_abi import GB_ERR_UNSUPPORTED, GB_OK, L, bwd, drop, norm, norm_q8, w4  # noqa: F401
 
 
 @pytest.mark.parametrize("n", [(1 << 31) - 15, (1 << 31) - 8, (1 << 31) - 1])
@@ -20,3 +23,17 @@ def test_last_chunks_columns_are_32_bit_numbers():
         chunks = -(-(cols + (7 if shift else 0)) // 8)
         for j in (0, 1, chunks - 2, chunks - 1):
             assert 8 * j < 1 << 31 and 8 * j - shift + 8 < 1 << 31
+
+
+def test_a_call_without_work_says_so_in_its_plan(L):  # noqa: F811
+    def after(call):  # (in a thread of its own: the plan is the calling thread's)
+        def run():
+            buf = ctypes.create_string_buffer(256)
+            assert call() == GB_OK and L.gb_last_plan(buf, 256) == GB_OK
+            return buf.value.decode()
+        with ThreadPoolExecutor(1) as pool:
+            return pool.submit(run).result()
+    for call in (lambda: w4(L, X=None, W=None, s=None, D=None, M=0), lambda: drop(L, X=None, D=None, N=0),
+                 lambda: norm(L, X=None, Y=None, w=None, M=0), lambda: norm_q8(L, X=None, Q=None, scale=None, D=0),
+                 lambda: bwd(L, dY=None, H=None, w=None, rstd=None, dR=None, dw=None, D=0)):
+        assert after(call) == "empty (no launch)"

@@ -225,3 +225,20 @@ def test_w4_zero_points_are_the_low_four_bits(m, group):
         assert torch.equal(got.nan_to_num(), pair.nan_to_num())
     check_linear_result(gb.linear_w4(x[1:], q, s, zeros=z | high, group=group) if m > 1 else want[1:], x[1:], None, q, s, z,
                         None, None, "none", group)
+
+
+# ---------------------------------------------------------------------------------- the plan that is reported
+
+def test_plan_of_a_call_without_work():
+    """Not the plan of the call before it."""
+    w = normal(64, seed=1)
+    empty = torch.empty(0, 64, dtype=BF16, device=DEV)
+    q, s, _ = w4_weights(8, 64, 64, False, 1)
+    for call in (lambda: gb.dropout(empty, 0.1, 1), lambda: gb.add_rms_norm(empty, w), lambda: gb.add_rms_norm_q8(empty, w),
+                 lambda: gb.linear_w4(empty, q, s, group=64), lambda: gb.ffn_gated_w4(empty, q, s, q, s, group=64)):
+        gb.dropout(normal(3, 64, seed=2), 0.1, 1)
+        assert "kernel=dropout" in gb.last_plan()
+        call()
+        assert gb.last_plan() == "empty (no launch)"
+    gb.add_rms_norm_backward(empty, empty, w, torch.empty(0, device=DEV))  # (dweight is written)
+    assert "kernel=add_rms_norm_backward blocks=0" in gb.last_plan()
