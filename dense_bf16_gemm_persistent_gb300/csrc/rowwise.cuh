@@ -96,14 +96,12 @@ struct Draw {
     }
 
     // Drop the chunk of `row` at columns col0 .. col0 + 7.  A dropped element is zero whatever it was
-    // (an infinity or a NaN among them): it is selected, not multiplied.  BITS: with fewer registers
-    // and more instructions.
-    template <bool BITS>
+    // (an infinity or a NaN among them): it is selected, not multiplied.
     __device__ __forceinline__ void chunk(float (&v)[8], int row, int col0) const {
         // a column below 0 is not an element: its word is not used, and the group -1 or -2 wraps
         const int phase = col0 & 3;  // (the same for the whole row)
         const uint32_t group = static_cast<uint32_t>((col0 - phase) >> 2);
-        if (!BITS && phase == 0) {
+        if (phase == 0) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 uint32_t w[4];
@@ -262,7 +260,7 @@ __global__ void __launch_bounds__(kDropoutThreads, 5) dropout_kernel(const __gri
             if (col0[u] >= p.n) continue;
             float v[8];
             unpack(xu[u], v);
-            if (DROP) draw.template chunk<false>(v, rows[u], col0[u]);
+            if (DROP) draw.chunk(v, rows[u], col0[u]);
             if (p.r) {
                 float r[8];
                 unpack(ru[u], r);
@@ -412,7 +410,7 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) norm_kernel(const __g
     for (int k = 0; k < V; ++k) {
         const int col0 = 8 * (tid + k * threads) - shift;
         unpack(read_chunk(slots + (stage * 2 * V + k) * all, col0), v[k]);
-        if (DROP) draw.template chunk<false>(v[k], row, col0);
+        if (DROP) draw.chunk(v[k], row, col0);
         if (p.r) {
             float r[8];
             unpack(read_chunk(slots + ((stage * 2 + 1) * V + k) * all, col0), r);
@@ -618,7 +616,7 @@ __global__ void __maxnreg__(V == 4 ? 128 : 80) norm_bwd_kernel(const __grid_cons
             }
             store_chunk(p.dr + row * p.lddr, col0, p.d, p.wide, pack(v));
             if (DROP) {
-                draw.template chunk<false>(v, row, col0);
+                draw.chunk(v, row, col0);
                 store_chunk(p.dx + row * p.lddx, col0, p.d, p.wide, pack(v));
             }
         }
