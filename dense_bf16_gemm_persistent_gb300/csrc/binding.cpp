@@ -10,6 +10,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <climits>
 #include <string>
 
 #include "../../include/gbgemm.h"
@@ -306,7 +308,8 @@ PyObject* add_rms_norm_q8(Args a, Py_ssize_t n) {
     const auto [M, D] = sizes(X, "X");
     const Arg x = matrix(X, "X", kBf16, M, D), r = matrix(a[2], "R", kBf16, M, D);
     const void* w = vector(a[1], "weight", kBf16, D);
-    const int64_t group = number(a[4]), scales = group > 0 ? (D + group - 1) / group : 1;
+    // (what is no int is no group either: the C call refuses it)
+    const int64_t group = std::clamp<int64_t>(number(a[4]), -1, INT_MAX), scales = group > 0 ? (D + group - 1) / group : 1;
     Out out(a[5], "out", kE4m3, M, D, X);
     const bool same = a[6] == Py_None && a[2] == Py_None;  // H is X itself
     Out h(same ? a[0] : a[6], "h", kBf16, M, D, X);

@@ -242,3 +242,13 @@ def test_plan_of_a_call_without_work():
         assert gb.last_plan() == "empty (no launch)"
     gb.add_rms_norm_backward(empty, empty, w, torch.empty(0, device=DEV))  # (dweight is written)
     assert "kernel=add_rms_norm_backward blocks=0" in gb.last_plan()
+
+
+# ---------------------------------------------------------------------------------- arguments
+
+def test_norm_q8_refuses_a_scale_group_that_is_no_int():
+    """Cut to 32 bits, these would be 0 and 128."""
+    x, w = normal(4, 96, seed=1), normal(96, seed=2)
+    for group in (1 << 32, (1 << 32) + 128, -(1 << 32), (1 << 63) - 1):
+        with pytest.raises(gb.GBError, match="scale_group"):
+            gb.add_rms_norm_q8(x, w, scale_group=group)
