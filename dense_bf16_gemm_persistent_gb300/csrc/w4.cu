@@ -81,7 +81,7 @@ gb_status_t validate(const Problem& pr) {
         if (w.lds < groups || (w.z && w.ldz < groups))
             return fail(GB_ERR_INVALID_ARG, "leading dimension of %s's scales or zeros is below its %" PRId64 " groups",
                         w.name, groups);
-        if (!aligned_to(w.q, 16) || w.ldq % 16)
+        if (!aligned_to(w.q, 16) || (pr.n > 1 && w.ldq % 16))  // (one row has no next one)
             return fail(GB_ERR_UNSUPPORTED, "%s: base address and leading dimension must be multiples of 16 bytes", w.name);
         if (!aligned_to(w.s, 2)) return fail(GB_ERR_UNSUPPORTED, "%s's scales must be 2-byte aligned", w.name);
     }

@@ -241,7 +241,7 @@ GB_API gb_status_t gb_gemm_linear_dact(const void* dY, int64_t lddy, const void*
  *           z = 8 everywhere
  *   group   32, 64 or 128 columns; the last group of a row may be shorter
  *   bias, R, act, D  as gb_gemm_linear (any 2-byte alignment and leading dimension)
- * K a multiple of 32; Wq's base and ldq multiples of 16 bytes (16-byte loads).  The weights are
+ * K a multiple of 32; Wq's base and (for N > 1) ldq multiples of 16 bytes (16-byte loads).  The weights are
  * read again for every 16 tokens (fewer where K is long), so that the call's time grows with M as
  * if there were a call for each: it is meant for few.  M == 0 or N == 0 is a no-op; K == 0 gives D = act(bias) + R.  D must not
  * overlap X or the weights; D == R is allowed.  Results are the same on every run.

@@ -252,3 +252,23 @@ def test_norm_q8_refuses_a_scale_group_that_is_no_int():
     for group in (1 << 32, (1 << 32) + 128, -(1 << 32), (1 << 63) - 1):
         with pytest.raises(gb.GBError, match="scale_group"):
             gb.add_rms_norm_q8(x, w, scale_group=group)
+
+
+@pytest.mark.parametrize("m", [1, 5, 16])
+def test_w4_one_row_of_weights_with_any_stride(m):
+    """A row cut out of a wider buffer: its stride leads to no row, and may be no multiple of 16 bytes."""
+    k, group = 96, 32
+    q, s, z = w4_weights(2, k, group, True, 1)
+    buf = torch.zeros(2, k // 2 + 5, dtype=torch.uint8, device=DEV)
+    assert buf.data_ptr() % 16 == 0
+    buf[:1, :k // 2] = q[:1]
+    row = buf[:1, :k // 2]
+    assert row.stride(0) % 16
+    x = normal(m, k, seed=2)
+    d = gb.linear_w4(x, row, s[:1], zeros=z[:1], group=group)
+    check_linear_result(d, x, None, q[:1], s[:1], z[:1], None, None, "none", group)
+    assert torch.equal(d, gb.linear_w4(x, q[:1], s[:1], zeros=z[:1], group=group))
+    pair = gb.ffn_gated_w4(x, row, s[:1], row, s[:1], zeros1=z[:1], group=group)
+    assert torch.equal(pair, gb.ffn_gated_w4(x, q[:1], s[:1], q[:1], s[:1], zeros1=z[:1], group=group))
+    with pytest.raises(gb.GBError, match="16 bytes"):
+        gb.linear_w4(x, buf[:, :k // 2], s, group=group)
