@@ -7,9 +7,9 @@
     add_rms_norm_backward(dY, H, weight, rstd)   ->  (dX, dR, dweight)
     dropout(X, p, seed, offset, R)               ->  bf16(keep * X / (1 - p) + R)
 
-Argument marshalling only, like the package's module, here by the compiled ``_gbgemm_torch.so``
-(``csrc/binding.cpp``): these calls take microseconds on the GPU.  There is no fallback; a call raises if it
-is not built.  ``include/gbgemm.h`` has the definitions.
+Tensors are on the current device.  Argument marshalling only, like the package's module, here by the compiled
+``_gbgemm_torch.so`` (``csrc/binding.cpp``): these calls take microseconds on the GPU.  There is no fallback; a
+call raises if it is not built.  ``include/gbgemm.h`` has the definitions.
 """
 from __future__ import annotations
 
@@ -20,9 +20,16 @@ import os
 
 import torch
 
-from . import _PKG, ACT, GBError, _check, _lock, _on, _stream, lib
+from . import _PKG, ACT, GBError, _check, _lock, _on, _raw_stream, lib
 
 _module = None
+
+
+def _bind(m, L, device=torch._C._cuda_getDevice) -> None:
+    stream = _raw_stream or (lambda number: torch.cuda.current_stream(number).cuda_stream)
+    m.bind(GBError, device, stream, *[ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+        "gb_gemm_linear_w4", "gb_gemm_ffn_gated_w4", "gb_dropout", "gb_add_rms_norm", "gb_add_rms_norm_q8",
+        "gb_add_rms_norm_backward", "gb_add_rms_norm_backward_workspace_bytes", "gb_last_error")])
 
 
 def binding():
@@ -38,9 +45,7 @@ def binding():
             loader = importlib.machinery.ExtensionFileLoader("_gbgemm_torch", path)
             m = importlib.util.module_from_spec(importlib.util.spec_from_loader("_gbgemm_torch", loader))
             loader.exec_module(m)
-            m.bind(GBError, _stream, *[ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
-                "gb_gemm_linear_w4", "gb_gemm_ffn_gated_w4", "gb_dropout", "gb_add_rms_norm", "gb_add_rms_norm_q8",
-                "gb_add_rms_norm_backward", "gb_add_rms_norm_backward_workspace_bytes", "gb_last_error")])
+            _bind(m, L)
             _module = m
         return _module
 

@@ -27,7 +27,8 @@ decltype(&gb_add_rms_norm_backward) f_norm_bwd;
 decltype(&gb_add_rms_norm_backward_workspace_bytes) f_norm_bwd_ws;
 decltype(&gb_last_error) f_last_error;
 PyObject* g_error;   // the package's GBError
-PyObject* g_stream;  // and its _stream(): a stream's handle, None: the current one's, on which every call runs
+PyObject* g_device;  // gives the current device's number
+PyObject* g_stream;  // and of a device's number its current stream's handle: what every call runs on
 
 constexpr auto kBf16 = at::kBFloat16;
 constexpr auto kE4m3 = at::kFloat8_e4m3fn;
@@ -66,8 +67,31 @@ struct Arg {
     int64_t ld = 0;
 };
 
+// The device that the call runs on: the current one, asked for once in a call.
+thread_local int64_t t_device;
+
+int64_t device() {
+    if (t_device < 0) {
+        PyObject* o = PyObject_CallNoArgs(g_device);
+        if (!o) throw Raised{};
+        t_device = PyLong_AsLongLong(o);
+        Py_DECREF(o);
+        if (t_device < 0) {
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, "no current CUDA device");
+            throw Raised{};
+        }
+    }
+    return t_device;
+}
+
+void check_device(const at::Tensor& t, const char* name) {
+    if (t.get_device() != device())
+        raise(PyExc_ValueError, std::string(name) + ": on " + t.device().str() + ", the current device is cuda:" +
+                                    std::to_string(device()));
+}
+
 void check_type(const at::Tensor& t, const char* name, at::ScalarType type) {
-    if (t.scalar_type() == type && t.is_cuda()) return;
+    if (t.scalar_type() == type && t.is_cuda()) return check_device(t, name);
     raise(PyExc_TypeError, std::string(name) + ": expected a CUDA " + c10::toString(type) + " tensor, got " +
                                c10::toString(t.scalar_type()) + " on " + t.device().str());
 }
@@ -208,7 +232,9 @@ int64_t group_of(PyObject* o) {
 void* address(PyObject* o) { return reinterpret_cast<void*>(static_cast<uintptr_t>(word(o))); }
 
 void* current_stream() {
-    PyObject* handle = PyObject_CallOneArg(g_stream, Py_None);
+    PyObject* number = PyLong_FromLongLong(device());
+    PyObject* handle = number ? PyObject_CallOneArg(g_stream, number) : nullptr;
+    Py_XDECREF(number);
     if (!handle) throw Raised{};
     const uint64_t v = PyLong_AsUnsignedLongLongMask(handle);
     Py_DECREF(handle);
@@ -339,6 +365,7 @@ PyObject* add_rms_norm_backward(Args a, Py_ssize_t n) {
     } else {
         workspace = tensor(a[8], "workspace");
         if (!workspace.is_cuda()) raise(PyExc_TypeError, "workspace: expected a CUDA tensor");
+        check_device(workspace, "workspace");
         if (!workspace.is_contiguous() || workspace.nbytes() < need)
             raise(PyExc_ValueError, "workspace holds " + std::to_string(workspace.nbytes()) + " contiguous bytes, " +
                                         std::to_string(need) + " needed");
@@ -353,11 +380,11 @@ PyObject* add_rms_norm_backward(Args a, Py_ssize_t n) {
     return three(x, p > 0.0 ? THPVariable_Wrap(dR) : Py_XNewRef(x), THPVariable_Wrap(std::move(dweight)));
 }
 
-// GBError, _stream, then the addresses of the C functions in the order of the declarations above
+// GBError, the two functions, then the addresses of the C functions in the order of the declarations above
 PyObject* bind(Args a, Py_ssize_t n) {
-    expect<10>(n);
+    expect<11>(n);
     void* at[8];
-    for (int i = 0; i < 8; ++i) at[i] = address(a[i + 2]);
+    for (int i = 0; i < 8; ++i) at[i] = address(a[i + 3]);
     f_linear_w4 = reinterpret_cast<decltype(f_linear_w4)>(at[0]);
     f_ffn_gated_w4 = reinterpret_cast<decltype(f_ffn_gated_w4)>(at[1]);
     f_dropout = reinterpret_cast<decltype(f_dropout)>(at[2]);
@@ -367,13 +394,15 @@ PyObject* bind(Args a, Py_ssize_t n) {
     f_norm_bwd_ws = reinterpret_cast<decltype(f_norm_bwd_ws)>(at[6]);
     f_last_error = reinterpret_cast<decltype(f_last_error)>(at[7]);
     g_error = Py_NewRef(a[0]);
-    g_stream = Py_NewRef(a[1]);
+    g_device = Py_NewRef(a[1]);
+    g_stream = Py_NewRef(a[2]);
     return Py_NewRef(Py_None);
 }
 
 template <PyObject* (*F)(Args, Py_ssize_t)>
 PyObject* entry(PyObject*, Args a, Py_ssize_t n) {
     HANDLE_TH_ERRORS
+    t_device = -1;
     try {
         return F(a, n);
     } catch (const Raised&) {

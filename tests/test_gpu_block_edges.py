@@ -272,3 +272,20 @@ def test_w4_one_row_of_weights_with_any_stride(m):
     assert torch.equal(pair, gb.ffn_gated_w4(x, q[:1], s[:1], q[:1], s[:1], zeros1=z[:1], group=group))
     with pytest.raises(gb.GBError, match="16 bytes"):
         gb.linear_w4(x, buf[:, :k // 2], s, group=group)
+
+
+@pytest.fixture
+def another_device_is_current():
+    """The binding, told that the current device is one that no tensor is on."""
+    m = gb.block.binding()
+    gb.block._bind(m, gb.lib(), lambda: 1)
+    yield
+    gb.block._bind(m, gb.lib())
+
+
+def test_tensors_of_another_device_are_refused(another_device_is_current):
+    """A kernel would run on the current device's stream, with addresses of another device's memory."""
+    calls = every_call()
+    for name in ("linear_w4", "ffn_gated_w4", "dropout", "add_rms_norm", "add_rms_norm_q8", "add_rms_norm_backward"):
+        with pytest.raises(ValueError, match="on cuda:0, the current device is cuda:1"):
+            calls[name](None)
