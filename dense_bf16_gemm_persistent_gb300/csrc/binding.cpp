@@ -247,6 +247,16 @@ void expect(Py_ssize_t n) {
     if (n != N) raise(PyExc_TypeError, "expected " + std::to_string(N) + " arguments, got " + std::to_string(n));
 }
 
+// A C function, without Python's lock: a launch waits for room where many are queued, and other threads'
+// Python code runs meanwhile.
+template <class F, class... A>
+gb_status_t unlocked(F f, A... args) {
+    PyThreadState* state = PyEval_SaveThread();
+    const gb_status_t status = f(args...);
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 using Args = PyObject* const*;
 
 // X, Wq, scales, bias, R, act, zeros, group, x_scale, out
@@ -260,9 +270,9 @@ PyObject* linear_w4(Args a, Py_ssize_t n) {
     const void* bias = vector(a[3], "bias", kBf16, N);
     const Arg r = matrix(a[4], "R", kBf16, M, N);
     Out out(a[9], "out", kBf16, M, N, X);
-    check(f_linear_w4(x.x.p, x.x.ld, x.type, static_cast<float*>(x.scale.p), x.scale.ld, w.q.p, w.q.ld, w.s.p, w.s.ld,
-                      w.z.p, w.z.ld, static_cast<int>(group), bias, r.p, r.ld, static_cast<int>(number(a[5])), out.arg.p,
-                      out.arg.ld, M, N, K, current_stream()));
+    check(unlocked(f_linear_w4, x.x.p, x.x.ld, x.type, static_cast<float*>(x.scale.p), x.scale.ld, w.q.p, w.q.ld, w.s.p,
+                   w.s.ld, w.z.p, w.z.ld, static_cast<int>(group), bias, r.p, r.ld, static_cast<int>(number(a[5])),
+                   out.arg.p, out.arg.ld, M, N, K, current_stream()));
     return out.object();
 }
 
@@ -276,9 +286,9 @@ PyObject* ffn_gated_w4(Args a, Py_ssize_t n) {
     const Weights u = weights(a[1], a[2], a[5], {"W1q", "scales1", "zeros1"}, N, K, groups);
     const Weights v = weights(a[3], a[4], a[6], {"W3q", "scales3", "zeros3"}, N, K, groups);
     Out out(a[9], "out", kBf16, M, N, X);
-    check(f_ffn_gated_w4(x.x.p, x.x.ld, x.type, static_cast<float*>(x.scale.p), x.scale.ld, u.q.p, u.q.ld, u.s.p, u.s.ld,
-                         u.z.p, u.z.ld, v.q.p, v.q.ld, v.s.p, v.s.ld, v.z.p, v.z.ld, static_cast<int>(group), out.arg.p,
-                         out.arg.ld, M, N, K, current_stream()));
+    check(unlocked(f_ffn_gated_w4, x.x.p, x.x.ld, x.type, static_cast<float*>(x.scale.p), x.scale.ld, u.q.p, u.q.ld,
+                   u.s.p, u.s.ld, u.z.p, u.z.ld, v.q.p, v.q.ld, v.s.p, v.s.ld, v.z.p, v.z.ld, static_cast<int>(group),
+                   out.arg.p, out.arg.ld, M, N, K, current_stream()));
     return out.object();
 }
 
@@ -290,8 +300,8 @@ PyObject* dropout(Args a, Py_ssize_t n) {
     const Arg x = matrix(X, "X", kBf16, M, N), r = matrix(a[4], "R", kBf16, M, N);
     const Seed seed(a[2], a[3]);
     Out out(a[5], "out", kBf16, M, N, X);
-    check(f_dropout(x.p, x.ld, r.p, r.ld, real(a[1]), seed.seed, seed.offset, seed.state, out.arg.p, out.arg.ld, M, N,
-                    current_stream()));
+    check(unlocked(f_dropout, x.p, x.ld, r.p, r.ld, real(a[1]), seed.seed, seed.offset, seed.state, out.arg.p,
+                   out.arg.ld, M, N, current_stream()));
     return out.object();
 }
 
@@ -322,8 +332,9 @@ PyObject* add_rms_norm(Args a, Py_ssize_t n) {
     const bool same = a[8] == Py_None && !r.p && a[2] == Py_None && p == 0.0;  // H is X itself
     Out h(same ? a[0] : a[8], "h", kBf16, M, D, X);
     at::Tensor rstd = make({M}, at::kFloat, X);
-    check(f_norm(x.p, x.ld, r.p, r.ld, w, real(a[3]), p, seed.seed, seed.offset, seed.state, same ? nullptr : h.arg.p,
-                 h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(rstd.data_ptr()), M, D, current_stream()));
+    check(unlocked(f_norm, x.p, x.ld, r.p, r.ld, w, real(a[3]), p, seed.seed, seed.offset, seed.state,
+                   same ? nullptr : h.arg.p, h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(rstd.data_ptr()), M, D,
+                   current_stream()));
     return three(out.object(), h.object(), THPVariable_Wrap(std::move(rstd)));
 }
 
@@ -340,9 +351,9 @@ PyObject* add_rms_norm_q8(Args a, Py_ssize_t n) {
     const bool same = a[6] == Py_None && a[2] == Py_None;  // H is X itself
     Out h(same ? a[0] : a[6], "h", kBf16, M, D, X);
     at::Tensor scale = make({M, scales}, at::kFloat, X);
-    check(f_norm_q8(x.p, x.ld, r.p, r.ld, w, real(a[3]), static_cast<int>(group), same ? nullptr : h.arg.p, h.arg.ld,
-                    out.arg.p, out.arg.ld, static_cast<float*>(scale.data_ptr()), std::max<int64_t>(scales, 1), M, D,
-                    current_stream()));
+    check(unlocked(f_norm_q8, x.p, x.ld, r.p, r.ld, w, real(a[3]), static_cast<int>(group), same ? nullptr : h.arg.p,
+                   h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(scale.data_ptr()), std::max<int64_t>(scales, 1),
+                   M, D, current_stream()));
     return three(out.object(), THPVariable_Wrap(std::move(scale)), h.object());
 }
 
@@ -373,9 +384,9 @@ PyObject* add_rms_norm_backward(Args a, Py_ssize_t n) {
     at::Tensor dR = make({M, D}, kBf16, dY), dX = p > 0.0 ? make({M, D}, kBf16, dY) : dR;
     at::Tensor dweight = make({D}, at::kFloat, dY);
     const int64_t ld = std::max<int64_t>(D, 1);
-    check(f_norm_bwd(dy.p, dy.ld, h.p, h.ld, w, static_cast<const float*>(rstd), dh.p, dh.ld, p, seed.seed, seed.offset,
-                     seed.state, dR.data_ptr(), ld, dX.data_ptr(), ld, static_cast<float*>(dweight.data_ptr()),
-                     workspace.data_ptr(), workspace.nbytes(), M, D, current_stream()));
+    check(unlocked(f_norm_bwd, dy.p, dy.ld, h.p, h.ld, w, static_cast<const float*>(rstd), dh.p, dh.ld, p, seed.seed,
+                   seed.offset, seed.state, dR.data_ptr(), ld, dX.data_ptr(), ld, static_cast<float*>(dweight.data_ptr()),
+                   workspace.data_ptr(), workspace.nbytes(), M, D, current_stream()));
     PyObject* x = THPVariable_Wrap(dX);
     return three(x, p > 0.0 ? THPVariable_Wrap(dR) : Py_XNewRef(x), THPVariable_Wrap(std::move(dweight)));
 }

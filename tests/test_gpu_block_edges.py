@@ -289,3 +289,38 @@ def test_tensors_of_another_device_are_refused(another_device_is_current):
     for name in ("linear_w4", "ffn_gated_w4", "dropout", "add_rms_norm", "add_rms_norm_q8", "add_rms_norm_backward"):
         with pytest.raises(ValueError, match="on cuda:0, the current device is cuda:1"):
             calls[name](None)
+
+
+# ---------------------------------------------------------------------------------- threads
+
+def test_a_launch_that_waits_lets_other_threads_run():
+    """More launches than the GPU's queue holds, behind a second of work: the thread that makes them waits without
+    Python's lock."""
+    import threading
+    import time
+    x = normal(4, 64, seed=1)
+    out = torch.empty_like(x)
+    gb.dropout(x, 0.1, 1, out=out)
+    torch.cuda.synchronize()
+    stream = torch.cuda.current_stream()
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    torch.cuda._sleep(2_000_000_000)
+    end.record()
+
+    def launch():
+        with torch.cuda.stream(stream):
+            for _ in range(4000):
+                gb.dropout(x, 0.1, 1, out=out)
+    thread = threading.Thread(target=launch)
+    longest, last, start = 0.0, time.perf_counter(), time.perf_counter()
+    thread.start()
+    while thread.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        longest, last = max(longest, now - last), now
+    took = last - start
+    torch.cuda.synchronize()
+    busy = begin.elapsed_time(end) / 1000
+    assert busy > 0.5 and took > 0.5 * busy, (busy, took)  # (the thread did wait)
+    assert longest < 0.25 * busy, (busy, took, longest)
