@@ -115,16 +115,28 @@ def _binding_command(out: str) -> list:
             "-L" + lib, "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
 
 
+def _binding_stamp() -> str:
+    """What the binding is compiled for besides its source: a torch of another version, or elsewhere, needs another."""
+    import torch
+    return "\n".join([torch.__version__, *_binding_command(BINDING)])
+
+
 def build_binding(force: bool = False) -> str:
     """Build _gbgemm_torch.so, the operators' binding to torch (argument marshalling only)."""
-    if not force and not _stale(BINDING, ("binding.cpp",)):
-        return BINDING
+    stamp, kept = _binding_stamp(), os.path.join(LOG_DIR, "binding.stamp")
+    if not force and not _stale(BINDING, ("binding.cpp",)) and os.path.exists(kept):
+        with open(kept) as f:
+            if f.read() == stamp:
+                return BINDING
+    os.makedirs(LOG_DIR, exist_ok=True)
     tmp = BINDING + f".tmp{os.getpid()}"
     try:
         res = subprocess.run(_binding_command(tmp), capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"the torch binding did not compile ({res.returncode}):\n{res.stderr[-4000:]}")
         os.replace(tmp, BINDING)
+        with open(kept, "w") as f:
+            f.write(stamp)
     finally:
         if os.path.exists(tmp):
             os.remove(tmp)

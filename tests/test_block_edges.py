@@ -37,3 +37,29 @@ def test_a_call_without_work_says_so_in_its_plan(L):  # noqa: F811
                  lambda: norm(L, X=None, Y=None, w=None, M=0), lambda: norm_q8(L, X=None, Q=None, scale=None, D=0),
                  lambda: bwd(L, dY=None, H=None, w=None, rstd=None, dR=None, dw=None, D=0)):
         assert after(call) == "empty (no launch)"
+
+
+def test_binding_is_compiled_again_for_another_torch(tmp_path, monkeypatch):
+    """Its source is older than it, but what it was compiled for is not what is installed."""
+    from dense_bf16_gemm_persistent_gb300 import _build
+    made = []
+
+    class Done:
+        returncode, stderr = 0, ""
+
+    def compiler(command, **kwargs):
+        made.append(command)
+        open(command[command.index("-o") + 1], "w").close()
+        return Done
+    monkeypatch.setattr(_build, "BINDING", str(tmp_path / "binding.so"))
+    monkeypatch.setattr(_build, "LOG_DIR", str(tmp_path / "log"))
+    monkeypatch.setattr(_build.subprocess, "run", compiler)
+    for expected in (1, 1):  # (the second time there is nothing to do)
+        _build.build_binding()
+        assert len(made) == expected
+    monkeypatch.setattr("torch.__version__", "0.0")
+    _build.build_binding()
+    assert len(made) == 2
+    monkeypatch.setenv("CXX", "another-compiler")
+    _build.build_binding()
+    assert len(made) == 3 and made[-1][0] == "another-compiler"
