@@ -363,6 +363,18 @@ struct Cursor {
 // A CTA's warps form teams of k_warps; a team takes row tiles in turn and its warps share the
 // tile's units.  Each warp streams its units through a slot of its own in shared memory with
 // 16-byte cp.async, which runs ahead over the ends of tiles; no barrier but the warp's own.
+//
+// Which lanes may be apart at an instruction that a whole warp has to execute: none.  What decides
+// whether such an instruction is reached is the same in every lane: in stage_x the loop's end and
+// its break go by i & ~1, the same for a warp's two halves (its shuffles are under nothing else);
+// sum_x's loop and the loops over tiles and units go by the warp's and the team's number.  Lanes part
+// only between those (a token or a row past the last, the one lane of sixteen that fetches a scale, a
+// matrix with zeros beside one without, the outputs that a lane adds up), and every such stretch ends
+// in a __syncwarp before the next mma or barrier of the CTA's threads, or holds no wait and no
+// exit, so that the lanes meet behind it.  The cluster's barriers are of the form that does not ask
+// for converged warps, and every thread of every CTA comes to each of them: the loop over tiles runs
+// the same number of rounds in all CTAs of a cluster (`first` and `tile_step` go by the cluster), at
+// least one (there are no more clusters than groups of tiles).
 template <int G, int NT, bool GATED, int X>
 __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __grid_constant__ Params p) {
     constexpr bool kStepScale = X != kXRowScale;  // x has a scale for each step
@@ -511,10 +523,12 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
     if (steps == 0 && !kStepScale && tid < 8 * NT) xscale[tid] = 0.f;
     const bool finite = stage_x<G, NT, X>(p, xs, xscale, col_base, steps, token0, tokens);
     bool odd = false;
-    if constexpr (X != kXBf16) __syncthreads();  // (a vote on a constant is not a barrier to rely on)
+    __syncwarp();  // (a warp's two halves may have left the loop apart)
+    if constexpr (X != kXBf16) __syncthreads();
     else odd = __syncthreads_or(!finite);
     if (!kLess) {
         sum_x<G, NT>(xs, xsum, steps * kStepGroups, tokens);
+        __syncwarp();
         __syncthreads();
     }
 
