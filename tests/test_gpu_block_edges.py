@@ -324,3 +324,59 @@ def test_a_launch_that_waits_lets_other_threads_run():
     busy = begin.elapsed_time(end) / 1000
     assert busy > 0.5 and took > 0.5 * busy, (busy, took)  # (the thread did wait)
     assert longest < 0.25 * busy, (busy, took, longest)
+
+
+# ---------------------------------------------------------------------------------- a seed in device memory
+
+@pytest.mark.parametrize("m,d", [(5, 512), (40, 1027), (700, 1500), (60, 16384)])
+def test_norm_backward_with_the_seed_in_device_memory(m, d):
+    """The same bits as with the numbers, and what a replayed graph finds in the memory when it runs."""
+    dy, h, w, dh = normal(m, d, seed=1), normal(m, d, seed=2), normal(d, seed=3), normal(m, d, seed=4)
+    rstd = (h.float().square().mean(dim=1) + 1e-6).rsqrt()
+    seed, p = (1 << 40) + 12345, 0.3
+    want = [gb.add_rms_norm_backward(dy, h, w, rstd, dh, p=p, seed=seed, offset=o) for o in (0, 3, 1 << 33)]
+    state = torch.tensor([seed, 0], dtype=torch.int64, device=DEV)
+    ws = torch.empty(gb.add_rms_norm_backward_workspace_bytes(m, d), dtype=torch.uint8, device=DEV)
+    got = gb.add_rms_norm_backward(dy, h, w, rstd, dh, p=p, seed=state, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want[0]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = gb.add_rms_norm_backward(dy, h, w, rstd, dh, p=p, seed=state, workspace=ws)
+    for offset, expected in zip((3, 1 << 33), want[1:]):
+        state[1] = offset
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, expected))
+    keep = ref.keep_mask(m, d, p, seed, 3).to(DEV)
+    assert torch.equal(want[1][0] != 0, keep & (want[1][1] != 0))
+
+
+# ---------------------------------------------------------------------------------- a step at the norm's limits, in a graph
+
+@pytest.mark.parametrize("m,d", [(3, 1), (9, 64), (4, 16383), (300, 16384)])
+def test_norm_forward_and_backward_in_one_graph(m, d):
+    """The narrowest and the widest rows; every tensor made outside, as a captured step has them."""
+    x, r, w, dy, dh = (normal(*shape, seed=i) for i, shape in enumerate(((m, d), (m, d), (d,), (m, d), (m, d))))
+
+    def step():
+        y, h, rstd = gb.add_rms_norm(x, w, r, p=0.1, seed=7, offset=1)
+        return y, h, rstd, *gb.add_rms_norm_backward(dy, h, w, rstd, dh, p=0.1, seed=7, offset=1)
+    want = [t.clone() for t in step()]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for _ in range(2):
+        for t in got:
+            t.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    hw = ref.dropped(x, 0.1, 7, 1) + r.double()
+    rw = (hw.square().mean(dim=1) + 1e-6).rsqrt()
+    assert_within(want[2], rw, rw * 2.0 ** -17, "rstd")
+    dr, dw = ref.norm_gradient(dy, want[1], w, dh, 1e-6, want[2])
+    xhat, g = want[1].double() * want[2].double()[:, None], dy.double() * w.double()
+    size = want[2].double()[:, None] * (g.abs() + xhat.abs() * (g * xhat).abs().mean(dim=1, keepdim=True))
+    slack = 2.0 ** -17 * size + 2.0 ** -22 * dh.double().abs()
+    assert_within(want[4], dr, HALF_BF16 * dr.abs() + slack * (1 + HALF_BF16) + TINY, "dR")
+    assert_within(want[5], dw, (m / 8 + 72) * 2.0 ** -24 * (dy.double() * xhat).abs().sum(dim=0) + TINY, "dweight")
