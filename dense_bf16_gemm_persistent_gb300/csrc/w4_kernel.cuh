@@ -725,10 +725,10 @@ __global__ void __launch_bounds__(32 * warps_of(G, NT), 1) w4_kernel(const __gri
                                 float v = acc[r / 2][i][r % 2 * 2 + e];
                                 if (!kLess) v = fmaf(-z, __uint_as_float(sum[e]), v);
                                 float& to = total[r / 2][i][r % 2 * 2 + e];
-                                // (x's scale first: at most 15 * 128 of x's largest, over 2^12, is a finite
-                                // number, where the two scales' product need not be)
-                                if (kStepScale) v *= e ? xs1[i] : xs0[i];
-                                to = fmaf(scale, v, to);
+                                // (the sum meets one scale and then the other: the two scales' product
+                                // need not be finite where the result is)
+                                if (kStepScale) to = fmaf(v * scale, e ? xs1[i] : xs0[i], to);
+                                else to = fmaf(scale, v, to);
                             }
                         }
                     }

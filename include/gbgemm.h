@@ -235,8 +235,8 @@ GB_API gb_status_t gb_gemm_linear_dact(const void* dY, int64_t lddy, const void*
  *           (the two outputs of gb_add_rms_norm_q8)
  *   Wq      [N,K/2] bytes, row n at Wq + n*ldq (ldq in BYTES): the low nibble of byte j is
  *           q[n,2j], the high one q[n,2j+1]
- *   scales  [N,ceil(K/group)] bf16 (lds elements), below 2^100 in size (a group's integers are
- *           summed first, then times X's scale, then times this: no factor overflows before D does)
+ *   scales  [N,ceil(K/group)] bf16 (lds elements), below 2^100 in size (the integers' sum with
+ *           X is multiplied by this first and then by X's scale, so that no factor overflows before D)
  *   zeros   [N,ceil(K/group)] bytes (ldz bytes) of which the low four bits are z, or NULL:
  *           z = 8 everywhere
  *   group   32, 64 or 128 columns; the last group of a row may be shorter
