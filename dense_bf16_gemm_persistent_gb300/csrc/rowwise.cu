@@ -140,8 +140,9 @@ gb_status_t allow_smem(Kernel kernel, std::atomic<bool>* ready, int dev, size_t 
     return GB_OK;
 }
 
-// Blocks that fill the GPU with `per_sm` threads an SM, a multiple of 8 of them (see the kernels'
-// rows); no more than there are rows for.
+// Blocks of `per_sm` threads an SM, a multiple of 8 of them (see the kernels' rows); no more than there are
+// rows for.  (More than are resident at once in places: of the forward pass's 1024 threads at 4096 columns,
+// shared memory holds three blocks of 256, and the fourth of each SM comes after them.)
 int64_t blocks_for(int64_t m, const RowPlan& pl, int per_sm, int sms) {
     const int64_t full = static_cast<int64_t>(sms) * std::max(1, per_sm / (pl.threads * pl.rows)) / 8 * 8;
     return std::min(ceil_div(m, pl.rows), std::max<int64_t>(8, full));

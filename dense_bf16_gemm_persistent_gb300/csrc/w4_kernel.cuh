@@ -25,9 +25,9 @@
 // slowly (sum x would make NaN of an infinity).
 //
 // Measured on a GB300: one token x 131072 x 8192 (G = 128) 96 us, 5.8 TB/s of the bytes that the
-// product cannot do without, 0.85 of the copy bandwidth; 8 tokens 104 us (0.79); 16 tokens 163 us;
-// 32 tokens 293 to 300 us.  The bytes of a unit for each of an SM's sixteen warps take 1.47 us at the
-// memory's rate.  A token's pair 14336 x 4096 takes 16.6 us where its bytes take 8.9: launch, x's layout
+// product cannot do without, 0.85 of the copy bandwidth; 8 tokens 104 us (0.79); 16 tokens 166 us;
+// 32 tokens 304 us.  The bytes of a unit for each of an SM's sixteen warps take 1.47 us at the
+// memory's rate.  A token's pair 14336 x 4096 takes 16.4 us where its bytes take 8.9: launch, x's layout
 // and three rounds' joins are, by the plan's model, the rest.  Steps on the way, 8 tokens: subtracting z
 // from each weight 127.5 us, off the sums 120.6; tiles of 32 rows instead of 16, with the scales by row,
 // the split-phase join and the pushed sums, 108.  A pass of 32 tokens took 464 us when one of 16 took 157.

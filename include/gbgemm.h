@@ -227,7 +227,12 @@ GB_API gb_status_t gb_gemm_linear_dact(const void* dY, int64_t lddy, const void*
  *   D[m,n] = bf16( act( sum_k X[m,k] W[n,k] + bias[n] ) + R[m,n] )
  *
  * No weight is rounded: the integers' products with X are summed in fp32 within a group, as
- * sum q x - z sum x, and the sums are scaled in fp32.
+ * sum q x - z sum x, and the sums are scaled in fp32.  A zero point other than 8 may so leave
+ * 2^-24 of z s sum |x| where the weights are at it; 8 leaves nothing.
+ * X is multiplied as fp16.  e4m3 is exact.  bf16 is scaled by a power of two for each 128 columns
+ * of a row: what is below 2^-27 of the largest of them starts to lose bits, and what is below
+ * 2^-35 of it counts as zero (also where the large ones meet weights at their zero point, and
+ * fp32 would have kept the small ones' sum).  Infinities and NaN count as they are.
  *   X       [M,K], leading dimension ldx (elements); x_type is a gb_x_type_t:
  *           GB_X_BF16              bf16; x_scale is not read
  *           GB_X_E4M3_ROW_SCALE    e4m3, row m times x_scale[m*ldxs]
@@ -294,7 +299,8 @@ GB_API gb_status_t gb_dropout(const void* X, int64_t ldx, const void* R, int64_t
  *
  *   h = dropout(X) + R        rstd = 1 / sqrt(mean(h^2) + eps)        Y = bf16(h rstd weight)
  *
- * in fp32 from h before its rounding.  dropout(X) is gb_dropout's with p, seed, offset and
+ * in fp32 from h before its rounding (a row whose sum of squares passes fp32's range has rstd = 0).
+ * dropout(X) is gb_dropout's with p, seed, offset and
  * rng_state (p = 0: X itself).
  *   X, Y  [M,D];  weight [D] bf16;  D at most 16384
  *   R     [M,D] or NULL
