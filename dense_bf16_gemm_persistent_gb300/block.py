@@ -5,6 +5,8 @@
     add_rms_norm(X, weight, R, p, seed, offset)  ->  (Y, H, rstd): H = dropout(X) + R, Y = H / rms(H) * weight
     add_rms_norm_q8(X, weight, R)                ->  (Q, scale, H): the same in e4m3 with scales
     add_rms_norm_backward(dY, H, weight, rstd)   ->  (dX, dR, dweight)
+    add_layer_norm(X, weight, bias, R, p, seed)  ->  (Y, H, mean, rstd): Y = (H - mean) * rstd * weight + bias
+    add_layer_norm_backward(dY, H, weight, mean, rstd)  ->  (dX, dR, dweight, dbias)
     dropout(X, p, seed, offset, R)               ->  bf16(keep * X / (1 - p) + R)
 
 Tensors are on the current device.  Argument marshalling only, like the package's module, here by the compiled
@@ -29,7 +31,8 @@ def _bind(m, L, device=torch._C._cuda_getDevice) -> None:
     stream = _raw_stream or (lambda number: torch.cuda.current_stream(number).cuda_stream)
     m.bind(GBError, device, stream, *[ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
         "gb_gemm_linear_w4", "gb_gemm_ffn_gated_w4", "gb_dropout", "gb_add_rms_norm", "gb_add_rms_norm_q8",
-        "gb_add_rms_norm_backward", "gb_add_rms_norm_backward_workspace_bytes", "gb_last_error")])
+        "gb_add_rms_norm_backward", "gb_add_rms_norm_backward_workspace_bytes", "gb_add_layer_norm",
+        "gb_add_layer_norm_backward", "gb_add_layer_norm_backward_workspace_bytes", "gb_last_error")])
 
 
 def binding():
@@ -120,3 +123,34 @@ def add_rms_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tenso
     if stream is not None:
         return _on(stream, add_rms_norm_backward, dY, H, weight, rstd, dH, p, seed, offset, workspace)
     return (_module or binding()).add_rms_norm_backward(dY, H, weight, rstd, dH, p, seed, offset, workspace)
+
+
+def add_layer_norm(X: torch.Tensor, weight: torch.Tensor, bias: torch.Tensor | None = None,
+                   R: torch.Tensor | None = None, eps: float = 1e-5, p: float = 0.0, seed=0, offset: int = 0,
+                   out: torch.Tensor | None = None, h: torch.Tensor | None = None,
+                   stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(Y, H, mean, rstd): H = dropout(X) + R (p, seed, offset as in dropout()), the mean and
+    rstd = 1 / sqrt(variance + eps) of each row, Y = (H - mean) * rstd * weight + bias from H before its rounding.
+    Without R and dropout H is X itself."""
+    if stream is not None:
+        return _on(stream, add_layer_norm, X, weight, bias, R, eps, p, seed, offset, out, h)
+    return (_module or binding()).add_layer_norm(X, weight, bias, R, eps, p, seed, offset, out, h)
+
+
+def add_layer_norm_backward_workspace_bytes(M: int, D: int) -> int:
+    """Bytes of workspace add_layer_norm_backward() needs on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(lib().gb_add_layer_norm_backward_workspace_bytes(M, D, ctypes.byref(n)))
+    return int(n.value)
+
+
+def add_layer_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Tensor, mean: torch.Tensor,
+                            rstd: torch.Tensor, dH: torch.Tensor | None = None, p: float = 0.0, seed=0,
+                            offset: int = 0, workspace: torch.Tensor | None = None,
+                            stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(dX, dR, dweight, dbias) of add_layer_norm() from the gradient dY of Y and (optionally) dH of H, with H, mean
+    and rstd as it returned them and the same p, seed and offset.  Without dropout dX is dR; dweight and dbias
+    [D] are fp32."""
+    if stream is not None:
+        return _on(stream, add_layer_norm_backward, dY, H, weight, mean, rstd, dH, p, seed, offset, workspace)
+    return (_module or binding()).add_layer_norm_backward(dY, H, weight, mean, rstd, dH, p, seed, offset, workspace)

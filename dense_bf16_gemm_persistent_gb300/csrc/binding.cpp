@@ -25,6 +25,9 @@ decltype(&gb_add_rms_norm) f_norm;
 decltype(&gb_add_rms_norm_q8) f_norm_q8;
 decltype(&gb_add_rms_norm_backward) f_norm_bwd;
 decltype(&gb_add_rms_norm_backward_workspace_bytes) f_norm_bwd_ws;
+decltype(&gb_add_layer_norm) f_layer_norm;
+decltype(&gb_add_layer_norm_backward) f_layer_norm_bwd;
+decltype(&gb_add_layer_norm_backward_workspace_bytes) f_layer_norm_bwd_ws;
 decltype(&gb_last_error) f_last_error;
 PyObject* g_error;   // the package's GBError
 PyObject* g_device;  // gives the current device's number
@@ -167,6 +170,18 @@ struct Out {
     PyObject* object() { return given ? Py_NewRef(given) : THPVariable_Wrap(std::move(made)); }
 };
 
+// A call's workspace: the caller's tensor, or a new one.
+at::Tensor scratch(PyObject* o, size_t need, const at::Tensor& like) {
+    if (o == Py_None) return make({std::max<int64_t>(need, 1)}, at::kByte, like);
+    const at::Tensor& t = tensor(o, "workspace");
+    if (!t.is_cuda()) raise(PyExc_TypeError, "workspace: expected a CUDA tensor");
+    check_device(t, "workspace");
+    if (!t.is_contiguous() || t.nbytes() < need)
+        raise(PyExc_ValueError, "workspace holds " + std::to_string(t.nbytes()) + " contiguous bytes, " +
+                                    std::to_string(need) + " needed");
+    return t;
+}
+
 // seed and offset as numbers, or a CUDA int64 tensor {seed, offset} in the place of the seed.
 struct Seed {
     uint64_t seed = 0, offset = 0;
@@ -305,17 +320,18 @@ PyObject* dropout(Args a, Py_ssize_t n) {
     return out.object();
 }
 
-PyObject* three(PyObject* a, PyObject* b, PyObject* c) {
-    PyObject* t = a && b && c ? PyTuple_New(3) : nullptr;
+// A tuple of new references (of which one may be null: an error that is set already).
+template <class... O>
+PyObject* tuple(O... objects) {
+    PyObject* all[] = {objects...};
+    bool fine = true;
+    for (PyObject* o : all) fine &= o != nullptr;
+    PyObject* t = fine ? PyTuple_New(sizeof...(objects)) : nullptr;
     if (!t) {
-        Py_XDECREF(a);
-        Py_XDECREF(b);
-        Py_XDECREF(c);
+        for (PyObject* o : all) Py_XDECREF(o);
         throw Raised{};
     }
-    PyTuple_SET_ITEM(t, 0, a);
-    PyTuple_SET_ITEM(t, 1, b);
-    PyTuple_SET_ITEM(t, 2, c);
+    for (size_t i = 0; i < sizeof...(objects); ++i) PyTuple_SET_ITEM(t, i, all[i]);
     return t;
 }
 
@@ -335,7 +351,7 @@ PyObject* add_rms_norm(Args a, Py_ssize_t n) {
     check(unlocked(f_norm, x.p, x.ld, r.p, r.ld, w, real(a[3]), p, seed.seed, seed.offset, seed.state,
                    same ? nullptr : h.arg.p, h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(rstd.data_ptr()), M, D,
                    current_stream()));
-    return three(out.object(), h.object(), THPVariable_Wrap(std::move(rstd)));
+    return tuple(out.object(), h.object(), THPVariable_Wrap(std::move(rstd)));
 }
 
 // X, weight, R, eps, scale_group, out, h
@@ -354,7 +370,7 @@ PyObject* add_rms_norm_q8(Args a, Py_ssize_t n) {
     check(unlocked(f_norm_q8, x.p, x.ld, r.p, r.ld, w, real(a[3]), static_cast<int>(group), same ? nullptr : h.arg.p,
                    h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(scale.data_ptr()), std::max<int64_t>(scales, 1),
                    M, D, current_stream()));
-    return three(out.object(), THPVariable_Wrap(std::move(scale)), h.object());
+    return tuple(out.object(), THPVariable_Wrap(std::move(scale)), h.object());
 }
 
 // dY, H, weight, rstd, dH, p, seed, offset, workspace
@@ -370,17 +386,7 @@ PyObject* add_rms_norm_backward(Args a, Py_ssize_t n) {
     const Seed seed(a[6], a[7]);
     size_t need = 0;
     check(f_norm_bwd_ws(M, D, &need));
-    at::Tensor workspace;
-    if (a[8] == Py_None) {
-        workspace = make({std::max<int64_t>(need, 1)}, at::kByte, dY);
-    } else {
-        workspace = tensor(a[8], "workspace");
-        if (!workspace.is_cuda()) raise(PyExc_TypeError, "workspace: expected a CUDA tensor");
-        check_device(workspace, "workspace");
-        if (!workspace.is_contiguous() || workspace.nbytes() < need)
-            raise(PyExc_ValueError, "workspace holds " + std::to_string(workspace.nbytes()) + " contiguous bytes, " +
-                                        std::to_string(need) + " needed");
-    }
+    const at::Tensor workspace = scratch(a[8], need, dY);
     at::Tensor dR = make({M, D}, kBf16, dY), dX = p > 0.0 ? make({M, D}, kBf16, dY) : dR;
     at::Tensor dweight = make({D}, at::kFloat, dY);
     const int64_t ld = std::max<int64_t>(D, 1);
@@ -388,14 +394,62 @@ PyObject* add_rms_norm_backward(Args a, Py_ssize_t n) {
                    seed.offset, seed.state, dR.data_ptr(), ld, dX.data_ptr(), ld, static_cast<float*>(dweight.data_ptr()),
                    workspace.data_ptr(), workspace.nbytes(), M, D, current_stream()));
     PyObject* x = THPVariable_Wrap(dX);
-    return three(x, p > 0.0 ? THPVariable_Wrap(dR) : Py_XNewRef(x), THPVariable_Wrap(std::move(dweight)));
+    return tuple(x, p > 0.0 ? THPVariable_Wrap(dR) : Py_XNewRef(x), THPVariable_Wrap(std::move(dweight)));
+}
+
+// X, weight, bias, R, eps, p, seed, offset, out, h
+PyObject* add_layer_norm(Args a, Py_ssize_t n) {
+    expect<10>(n);
+    const at::Tensor& X = tensor(a[0], "X");
+    const auto [M, D] = sizes(X, "X");
+    const Arg x = matrix(X, "X", kBf16, M, D), r = matrix(a[3], "R", kBf16, M, D);
+    const void* w = vector(a[1], "weight", kBf16, D);
+    const void* b = vector(a[2], "bias", kBf16, D);
+    const double p = real(a[5]);
+    const Seed seed(a[6], a[7]);
+    Out out(a[8], "out", kBf16, M, D, X);
+    const bool same = a[9] == Py_None && a[3] == Py_None && p == 0.0;  // H is X itself
+    Out h(same ? a[0] : a[9], "h", kBf16, M, D, X);
+    at::Tensor mean = make({M}, at::kFloat, X), rstd = make({M}, at::kFloat, X);
+    check(unlocked(f_layer_norm, x.p, x.ld, r.p, r.ld, w, b, real(a[4]), p, seed.seed, seed.offset, seed.state,
+                   same ? nullptr : h.arg.p, h.arg.ld, out.arg.p, out.arg.ld, static_cast<float*>(mean.data_ptr()),
+                   static_cast<float*>(rstd.data_ptr()), M, D, current_stream()));
+    return tuple(out.object(), h.object(), THPVariable_Wrap(std::move(mean)), THPVariable_Wrap(std::move(rstd)));
+}
+
+// dY, H, weight, mean, rstd, dH, p, seed, offset, workspace
+PyObject* add_layer_norm_backward(Args a, Py_ssize_t n) {
+    expect<10>(n);
+    const at::Tensor& dY = tensor(a[0], "dY");
+    const auto [M, D] = sizes(dY, "dY");
+    const Arg dy = matrix(dY, "dY", kBf16, M, D), h = matrix(tensor(a[1], "H"), "H", kBf16, M, D);
+    const void* w = vector(a[2], "weight", kBf16, D);
+    const void* mean = vector(a[3], "mean", at::kFloat, M);
+    const void* rstd = vector(a[4], "rstd", at::kFloat, M);
+    const Arg dh = matrix(a[5], "dH", kBf16, M, D);
+    const double p = real(a[6]);
+    const Seed seed(a[7], a[8]);
+    size_t need = 0;
+    check(f_layer_norm_bwd_ws(M, D, &need));
+    const at::Tensor workspace = scratch(a[9], need, dY);
+    at::Tensor dR = make({M, D}, kBf16, dY), dX = p > 0.0 ? make({M, D}, kBf16, dY) : dR;
+    at::Tensor dweight = make({D}, at::kFloat, dY), dbias = make({D}, at::kFloat, dY);
+    const int64_t ld = std::max<int64_t>(D, 1);
+    check(unlocked(f_layer_norm_bwd, dy.p, dy.ld, h.p, h.ld, w, static_cast<const float*>(mean),
+                   static_cast<const float*>(rstd), dh.p, dh.ld, p, seed.seed, seed.offset, seed.state, dR.data_ptr(), ld,
+                   dX.data_ptr(), ld, static_cast<float*>(dweight.data_ptr()), static_cast<float*>(dbias.data_ptr()),
+                   workspace.data_ptr(), workspace.nbytes(), M, D, current_stream()));
+    PyObject* x = THPVariable_Wrap(dX);
+    return tuple(x, p > 0.0 ? THPVariable_Wrap(dR) : Py_XNewRef(x), THPVariable_Wrap(std::move(dweight)),
+                 THPVariable_Wrap(std::move(dbias)));
 }
 
 // GBError, the two functions, then the addresses of the C functions in the order of the declarations above
 PyObject* bind(Args a, Py_ssize_t n) {
-    expect<11>(n);
-    void* at[8];
-    for (int i = 0; i < 8; ++i) at[i] = address(a[i + 3]);
+    constexpr int count = 11;
+    expect<count + 3>(n);
+    void* at[count];
+    for (int i = 0; i < count; ++i) at[i] = address(a[i + 3]);
     f_linear_w4 = reinterpret_cast<decltype(f_linear_w4)>(at[0]);
     f_ffn_gated_w4 = reinterpret_cast<decltype(f_ffn_gated_w4)>(at[1]);
     f_dropout = reinterpret_cast<decltype(f_dropout)>(at[2]);
@@ -403,7 +457,10 @@ PyObject* bind(Args a, Py_ssize_t n) {
     f_norm_q8 = reinterpret_cast<decltype(f_norm_q8)>(at[4]);
     f_norm_bwd = reinterpret_cast<decltype(f_norm_bwd)>(at[5]);
     f_norm_bwd_ws = reinterpret_cast<decltype(f_norm_bwd_ws)>(at[6]);
-    f_last_error = reinterpret_cast<decltype(f_last_error)>(at[7]);
+    f_layer_norm = reinterpret_cast<decltype(f_layer_norm)>(at[7]);
+    f_layer_norm_bwd = reinterpret_cast<decltype(f_layer_norm_bwd)>(at[8]);
+    f_layer_norm_bwd_ws = reinterpret_cast<decltype(f_layer_norm_bwd_ws)>(at[9]);
+    f_last_error = reinterpret_cast<decltype(f_last_error)>(at[10]);
     g_error = Py_NewRef(a[0]);
     g_device = Py_NewRef(a[1]);
     g_stream = Py_NewRef(a[2]);
@@ -434,6 +491,8 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<add_rms_norm>("add_rms_norm"),
                          method<add_rms_norm_q8>("add_rms_norm_q8"),
                          method<add_rms_norm_backward>("add_rms_norm_backward"),
+                         method<add_layer_norm>("add_layer_norm"),
+                         method<add_layer_norm_backward>("add_layer_norm_backward"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gbgemm_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

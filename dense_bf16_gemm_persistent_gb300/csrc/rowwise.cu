@@ -1,11 +1,12 @@
 // C ABI of the row operators: argument checks, launch shapes and launches of the kernels in
-// rowwise.cuh.
+// rowwise.cuh and layernorm.cuh.
 #include <algorithm>
 #include <atomic>
 #include <cinttypes>
 #include <cmath>
 
 #include "host.h"
+#include "layernorm.cuh"
 #include "rowwise.cuh"
 
 namespace {
@@ -197,6 +198,49 @@ int bwd_blocks(int64_t m, const RowPlan& pl, int sms) {
 int64_t bwd_workspace(int64_t m, int64_t d, int sms) {
     const int64_t by_warps = bwd_blocks(m, plan_chunks(ceil_div(d, 8)), sms);
     return std::max<int64_t>(by_warps, bwd_blocks(m, plan_chunks(ceil_div(d + 7, 8)), sms)) * d * 4;
+}
+
+// ---------------------------------------------------------------- layer norm
+
+template <int V, int DROP>
+gb_status_t launch_layer_norm(const LayerNormParams& p, const RowPlan& pl, int dev, const DeviceInfo& info,
+                              cudaStream_t stream) {
+    static std::atomic<bool> ready[64];
+    gb_status_t st = allow_smem(layer_norm_kernel<V, DROP>, ready, dev, info.smem_optin - 1024);
+    if (st != GB_OK) return st;
+    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : DROP ? 768 : 1024, info.sms);
+    const size_t smem = static_cast<size_t>(layer_norm_stages(V) * 2 + 2) * V * 16 * pl.threads * pl.rows;
+    note_plan("kernel=add_layer_norm dropout=%lld threads=%lld rows=%lld chunks=%lld blocks=%lld wide=%lld", DROP,
+              pl.threads, pl.rows, V, blocks, pl.wide);
+    return Launch(static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream)(
+        "add_layer_norm launch", layer_norm_kernel<V, DROP>, p);
+}
+
+template <int DROP>
+gb_status_t run_layer_norm(const LayerNormParams& p, const RowPlan& pl, int dev, const DeviceInfo& info,
+                           cudaStream_t stream) {
+    return pl.chunks_per_thread <= 2 ? launch_layer_norm<2, DROP>(p, pl, dev, info, stream)
+                                     : launch_layer_norm<4, DROP>(p, pl, dev, info, stream);
+}
+
+template <int V, int DROP>
+gb_status_t launch_layer_bwd(const LayerNormBwdParams& p, const RowPlan& pl, int blocks, int dev, const DeviceInfo& info,
+                             cudaStream_t stream) {
+    static std::atomic<bool> ready[64];
+    gb_status_t st = allow_smem(layer_norm_bwd_kernel<V, DROP>, ready, dev, info.smem_optin - 1024);
+    if (st != GB_OK) return st;
+    // two stages of three matrices, and the weight; and the join of a block's rows
+    size_t smem = static_cast<size_t>(kBwdStages * 3 + 1) * V * 16 * pl.threads * pl.rows;
+    if (pl.rows > 1) smem = std::max(smem, static_cast<size_t>(p.d) * 8);
+    return Launch(blocks, dim3(pl.threads, pl.rows), smem, stream)("add_layer_norm_backward launch",
+                                                                   layer_norm_bwd_kernel<V, DROP>, p);
+}
+
+template <int DROP>
+gb_status_t run_layer_bwd(const LayerNormBwdParams& p, const RowPlan& pl, int blocks, int dev, const DeviceInfo& info,
+                          cudaStream_t stream) {
+    return pl.chunks_per_thread <= 2 ? launch_layer_bwd<2, DROP>(p, pl, blocks, dev, info, stream)
+                                     : launch_layer_bwd<4, DROP>(p, pl, blocks, dev, info, stream);
 }
 
 }  // namespace
@@ -419,6 +463,139 @@ gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const void* H
     return Launch(static_cast<unsigned>(ceil_div(D, kJoinColumns)), dim3(kJoinColumns, kJoinParts), 0, s)(
         "add_rms_norm_backward join launch", join_kernel, static_cast<const float*>(workspace), blocks, static_cast<int>(D),
         dweight);
+}
+
+gb_status_t gb_add_layer_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                              const void* bias, double eps, double p, uint64_t seed, uint64_t offset,
+                              const void* rng_state, void* H, int64_t ldh, void* Y, int64_t ldy, float* mean, float* rstd,
+                              int64_t M, int64_t D, void* stream) {
+    clear_error();
+    gb_status_t st;
+    if ((st = check_sizes(M, D)) != GB_OK) return st;
+    LayerNormParams prm{};
+    if ((st = make_drop(p, seed, offset, rng_state, &prm.drop)) != GB_OK) return st;
+    if (!(eps >= 0.0 && std::isfinite(eps))) return fail(GB_ERR_INVALID_ARG, "eps=%g is not a finite number >= 0", eps);
+    if (M == 0 || D == 0) {
+        note_empty();
+        return GB_OK;
+    }
+    const Mat mats[] = {{"X", X, ldx, 2}, {"Y", Y, ldy, 2}, {"R", R, ldr, 2}, {"H", H, ldh, 2}};
+    for (const Mat& m : mats)
+        if ((m.p || m.name[0] == 'X' || m.name[0] == 'Y') && (st = check_mat(m, D)) != GB_OK) return st;
+    if ((st = check_ptr("weight", weight, 2)) != GB_OK) return st;
+    if (bias && (st = check_ptr("bias", bias, 2)) != GB_OK) return st;
+    if (mean && (st = check_ptr("mean", mean, 4)) != GB_OK) return st;
+    if (rstd && (st = check_ptr("rstd", rstd, 4)) != GB_OK) return st;
+    if (D > kMaxNormColumns)
+        return fail(GB_ERR_UNSUPPORTED, "rows of %" PRId64 " columns: at most %d", D, kMaxNormColumns);
+    int dev = 0;
+    DeviceInfo info;
+    if ((st = device_info(&dev, &info)) != GB_OK) return st;
+    prm.x = static_cast<const uint16_t*>(X);
+    prm.r = static_cast<const uint16_t*>(R);
+    prm.weight = static_cast<const uint16_t*>(weight);
+    prm.bias = static_cast<const uint16_t*>(bias);
+    prm.h = static_cast<uint16_t*>(H);
+    prm.y = static_cast<uint16_t*>(Y);
+    prm.mean = mean;
+    prm.rstd = rstd;
+    prm.ldx = ldx;
+    prm.ldr = ldr;
+    prm.ldh = ldh;
+    prm.ldy = ldy;
+    prm.m = static_cast<int>(M);
+    prm.d = static_cast<int>(D);
+    prm.eps = static_cast<float>(eps);
+    const RowPlan pl = plan_rows(mats, M, D);
+    prm.wide = pl.wide;
+    prm.wide_weight = aligned_to(weight, 16);
+    prm.wide_bias = aligned_to(bias, 16);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    switch (drop_kind(p, rng_state)) {
+        case kNoDrop: return run_layer_norm<kNoDrop>(prm, pl, dev, info, s);
+        case kKeys: return run_layer_norm<kKeys>(prm, pl, dev, info, s);
+        default: return run_layer_norm<kState>(prm, pl, dev, info, s);
+    }
+}
+
+gb_status_t gb_add_layer_norm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes) {
+    const gb_status_t st = gb_add_rms_norm_backward_workspace_bytes(M, D, bytes);
+    if (st == GB_OK) *bytes *= 2;  // (the parts of two gradients)
+    return st;
+}
+
+gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* weight,
+                                       const float* mean, const float* rstd, const void* dH, int64_t lddh, double p,
+                                       uint64_t seed, uint64_t offset, const void* rng_state, void* dR, int64_t lddr,
+                                       void* dX, int64_t lddx, float* dweight, float* dbias, void* workspace,
+                                       size_t workspace_bytes, int64_t M, int64_t D, void* stream) {
+    clear_error();
+    gb_status_t st;
+    if ((st = check_sizes(M, D)) != GB_OK) return st;
+    LayerNormBwdParams prm{};
+    if ((st = make_drop(p, seed, offset, rng_state, &prm.drop)) != GB_OK) return st;
+    if (D == 0) {
+        note_empty();
+        return GB_OK;
+    }
+    const bool drop = p > 0.0;
+    if ((st = check_ptr("dweight", dweight, 4)) != GB_OK) return st;
+    if ((st = check_ptr("dbias", dbias, 4)) != GB_OK) return st;
+    const Mat mats[] = {{"dY", dY, lddy, 2}, {"H", H, ldh, 2}, {"dR", dR, lddr, 2}, {"dH", dH, lddh, 2},
+                        {"dX", drop ? dX : nullptr, lddx, 2}};
+    if (M > 0) {
+        for (int i = 0; i < 5; ++i)
+            if ((i < 3 || mats[i].p || (i == 4 && drop)) && (st = check_mat(mats[i], D)) != GB_OK) return st;
+        if ((st = check_ptr("weight", weight, 2)) != GB_OK) return st;
+        if ((st = check_ptr("mean", mean, 4)) != GB_OK) return st;
+        if ((st = check_ptr("rstd", rstd, 4)) != GB_OK) return st;
+    }
+    if (D > kMaxNormColumns)
+        return fail(GB_ERR_UNSUPPORTED, "rows of %" PRId64 " columns: at most %d", D, kMaxNormColumns);
+    int dev = 0;
+    DeviceInfo info;
+    if ((st = device_info(&dev, &info)) != GB_OK) return st;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int blocks = 0;
+    RowPlan pl;
+    if (M > 0) {
+        const size_t need = 2 * static_cast<size_t>(bwd_workspace(M, D, info.sms));
+        if (!workspace || workspace_bytes < need)
+            return fail(GB_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0),
+                        need);
+        if (!aligned_to(workspace, 4)) return fail(GB_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
+        prm.dy = static_cast<const uint16_t*>(dY);
+        prm.h = static_cast<const uint16_t*>(H);
+        prm.weight = static_cast<const uint16_t*>(weight);
+        prm.mean = mean;
+        prm.rstd = rstd;
+        prm.dh = static_cast<const uint16_t*>(dH);
+        prm.dr = static_cast<uint16_t*>(dR);
+        prm.dx = static_cast<uint16_t*>(dX);
+        prm.partial = static_cast<float*>(workspace);
+        prm.lddy = lddy;
+        prm.ldh = ldh;
+        prm.lddh = lddh;
+        prm.lddr = lddr;
+        prm.lddx = lddx;
+        prm.m = static_cast<int>(M);
+        prm.d = static_cast<int>(D);
+        pl = plan_rows(mats, M, D);
+        prm.wide = pl.wide;
+        prm.wide_weight = aligned_to(weight, 16);
+        blocks = bwd_blocks(M, pl, info.sms);
+        switch (drop_kind(p, rng_state)) {
+            case kNoDrop: st = run_layer_bwd<kNoDrop>(prm, pl, blocks, dev, info, s); break;
+            case kKeys: st = run_layer_bwd<kKeys>(prm, pl, blocks, dev, info, s); break;
+            default: st = run_layer_bwd<kState>(prm, pl, blocks, dev, info, s); break;
+        }
+        if (st != GB_OK) return st;
+    }
+    note_plan("kernel=add_layer_norm_backward blocks=%lld dropout=%lld threads=%lld rows=%lld chunks=%lld wide=%lld", blocks,
+              drop, pl.threads, pl.rows, pl.chunks_per_thread, pl.wide);
+    return Launch(static_cast<unsigned>(ceil_div(2 * D, kJoinColumns)), dim3(kJoinColumns, kJoinParts), 0, s)(
+        "add_layer_norm_backward join launch", join2_kernel, static_cast<const float*>(workspace), blocks,
+        static_cast<int>(D), dweight, dbias);
 }
 
 }  // extern "C"

@@ -352,6 +352,44 @@ GB_API gb_status_t gb_add_rms_norm_backward(const void* dY, int64_t lddy, const 
 GB_API gb_status_t gb_add_rms_norm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes);
 
 /*
+ * Layer norm of a row with the residual's addition before it:
+ *
+ *   h = dropout(X) + R     mean = mean(h)     rstd = 1 / sqrt(mean((h - mean)^2) + eps)
+ *   Y = bf16( (h - mean) rstd weight + bias )
+ *
+ * in fp32 from h before its rounding; the variance is summed from differences, so that a mean far from zero
+ * costs no bits (a row whose sum of squares passes fp32's range has rstd = 0).  X, Y, R, H, weight, dropout
+ * and the allowed overlaps are as gb_add_rms_norm's.
+ *   bias        [D] bf16 or NULL
+ *   mean, rstd  [M] fp32 or NULL: what the backward pass wants
+ */
+GB_API gb_status_t gb_add_layer_norm(const void* X, int64_t ldx, const void* R, int64_t ldr, const void* weight,
+                                     const void* bias, double eps, double p, uint64_t seed, uint64_t offset,
+                                     const void* rng_state, void* H, int64_t ldh, void* Y, int64_t ldy, float* mean,
+                                     float* rstd, int64_t M, int64_t D, void* stream);
+
+/*
+ * Backward pass of gb_add_layer_norm.  With xhat = (h - mean) rstd and g = dY weight:
+ *
+ *   dR = bf16( rstd (g - mean(g) - xhat mean(g xhat)) + dH )   the residual's gradient, and X's if p = 0
+ *   dX = bf16( keep dR / (1 - p) )                             X's gradient (dR before its rounding)
+ *   dweight[d] = sum_m dY[m,d] xhat[m,d]      dbias[d] = sum_m dY[m,d]        fp32
+ *
+ * H, mean and rstd as gb_add_layer_norm gave them; dweight and dbias are both written whole (zeros if M == 0).
+ * The other arguments, the order of sums and the allowed overlaps are as gb_add_rms_norm_backward's; the
+ * workspace is of at least gb_add_layer_norm_backward_workspace_bytes().
+ */
+GB_API gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh,
+                                              const void* weight, const float* mean, const float* rstd, const void* dH,
+                                              int64_t lddh, double p, uint64_t seed, uint64_t offset,
+                                              const void* rng_state, void* dR, int64_t lddr, void* dX, int64_t lddx,
+                                              float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                                              int64_t M, int64_t D, void* stream);
+
+/* Workspace bytes of gb_add_layer_norm_backward on the current device (0 if M or D is 0). */
+GB_API gb_status_t gb_add_layer_norm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes);
+
+/*
  * Workspace bytes the split-K call needs for this problem on the current
  * device under the current configuration (ffn: 0 = linear, 1 = FFN fusion;
  * splits as above).  Writes 0 when the plan does not split.  Needs a CUDA

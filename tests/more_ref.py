@@ -1,0 +1,65 @@
+"""Definitions in 64 bits of layer norm, low-rank adapters and the mixture of experts, with the errors that a
+correct implementation may have.
+
+eps / 2 of fp32 is 2^-24: a sum of n fp32 terms, added in chains and trees, is off by at most its longest chain times
+2^-24 of the sum of the terms' sizes.
+"""
+from __future__ import annotations
+
+import torch
+
+from tests import block_ref as ref
+from tests.block_ref import HALF_BF16, TINY
+
+U = 2.0 ** -24
+# the longest chain of a row's sum: 32 elements a thread, two trees of five steps, and a product or two a term
+ROW = 32 + 10 + 4
+
+
+def layer_norm(x, r, w, b, eps, p=0.0, seed=0, offset=0):
+    """{name: (value, tolerance)} of Y, H, mean and rstd."""
+    h = ref.dropped(x, p, seed, offset)
+    if r is not None:
+        h = h + r.double()
+    d = h.shape[1]
+    w = w.double()
+    off_h = (2 if p else 1) * 2 * U * (h.abs() + (r.double().abs() if r is not None else 0))
+    mean = h.mean(dim=1, keepdim=True)
+    e_mean = ROW * U * h.abs().mean(dim=1, keepdim=True) + off_h.mean(dim=1, keepdim=True)
+    dev = h - mean
+    var = dev.square().mean(dim=1, keepdim=True)
+    # each difference is off by e_mean, its own rounding and h's; the squares' sum by its chain
+    e_dev = e_mean + off_h + 2 * U * dev.abs()
+    e_var = (2 * dev.abs() * e_dev + e_dev.square()).mean(dim=1, keepdim=True) + 2 * ROW * U * var
+    rstd = (var + eps).rsqrt()
+    e_rstd = rstd * (0.5 * e_var / (var + eps) * (1 + 2 * e_var / (var + eps)) + 8 * U)
+    y = dev * rstd * w
+    e_y = (e_dev * rstd + dev.abs() * e_rstd + 4 * U * (dev * rstd).abs()) * w.abs() + 4 * U * y.abs()
+    if b is not None:
+        y = y + b.double()
+        e_y = e_y + U * (y.abs() + b.double().abs())
+    up = lambda v, e: (v, HALF_BF16 * v.abs() + e * (1 + HALF_BF16) + TINY)  # noqa: E731
+    return {"y": up(y, e_y), "h": up(h, off_h), "mean": (mean[:, 0], e_mean[:, 0] + U * mean[:, 0].abs() + TINY),
+            "rstd": (rstd[:, 0], e_rstd[:, 0])}
+
+
+def layer_norm_gradient(dy, h, w, mean, rstd, dh=None):
+    """(dR, dweight, dbias) of y = (h - mean) rstd w + b and of dh . h, from the formula, in 64 bits."""
+    dy, h, w, r = dy.double(), h.double(), w.double(), rstd.double()[:, None]
+    xhat, g = (h - mean.double()[:, None]) * r, dy * w
+    dr = r * (g - g.mean(dim=1, keepdim=True) - xhat * (g * xhat).mean(dim=1, keepdim=True))
+    if dh is not None:
+        dr = dr + dh.double()
+    return dr, (dy * xhat).sum(dim=0), dy.sum(dim=0)
+
+
+def layer_norm_gradient_tolerances(dy, h, w, mean, rstd, dh, dr):
+    """What dR before its rounding, dweight and dbias may be off."""
+    dy, h, w, r = dy.double(), h.double(), w.double(), rstd.double()[:, None]
+    xhat, g = (h - mean.double()[:, None]) * r, dy * w
+    size = g.abs() + g.abs().mean(dim=1, keepdim=True) + xhat.abs() * (g * xhat).abs().mean(dim=1, keepdim=True)
+    e = r * (ROW + 8) * U * size + 2 * U * dr.abs() + (U * dh.double().abs() if dh is not None else 0)
+    # a column's sum: at least eight blocks' rows one after another (a warp's where a block has eight), eight
+    # warps, and the join's chain and tree
+    rows = -(-dy.shape[0] // 8) + 8 + 48
+    return e, (rows + 3) * U * (dy * xhat).abs().sum(dim=0) + TINY, rows * U * dy.abs().sum(dim=0) + TINY

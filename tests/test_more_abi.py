@@ -1,0 +1,106 @@
+"""Layer norm, low-rank adapters and the mixture of experts on the CPU: what the C ABI and the Python entry points
+refuse before they touch a GPU, and the formulas of the gradients against differences."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from tests import more_ref
+
+GB_OK, GB_ERR_INVALID_ARG, GB_ERR_UNSUPPORTED = 0, 1, 2
+P16, P4, P2, P1 = 0x10000, 0x10004, 0x10002, 0x10001  # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    from dense_bf16_gemm_persistent_gb300 import _build
+    _build.build()
+    import dense_bf16_gemm_persistent_gb300 as gb
+    return gb.lib()
+
+
+# ---------------------------------------------------------------------------------- layer norm
+
+def norm(L, X=P16, ldx=32, R=None, ldr=0, w=P16, b=None, eps=1e-5, p=0.0, H=None, ldh=0, Y=P16, ldy=32, mean=None,
+         rstd=None, M=4, D=32, state=None):
+    return L.gb_add_layer_norm(X, ldx, R, ldr, w, b, eps, p, 1, 2, state, H, ldh, Y, ldy, mean, rstd, M, D, None)
+
+
+@pytest.mark.parametrize("kwargs,status,needle", [
+    (dict(X=None), GB_ERR_INVALID_ARG, "X is null"),
+    (dict(Y=None), GB_ERR_INVALID_ARG, "Y is null"),
+    (dict(w=None), GB_ERR_INVALID_ARG, "weight is null"),
+    (dict(M=-1), GB_ERR_INVALID_ARG, "negative"),
+    (dict(eps=-1.0), GB_ERR_INVALID_ARG, "eps"),
+    (dict(eps=float("nan")), GB_ERR_INVALID_ARG, "eps"),
+    (dict(p=2.0), GB_ERR_INVALID_ARG, "probability"),
+    (dict(ldx=31), GB_ERR_INVALID_ARG, "of X"),
+    (dict(R=P16, ldr=31), GB_ERR_INVALID_ARG, "of R"),
+    (dict(H=P16, ldh=31), GB_ERR_INVALID_ARG, "of H"),
+    (dict(b=P1), GB_ERR_UNSUPPORTED, "bias"),
+    (dict(mean=P2), GB_ERR_UNSUPPORTED, "mean"),
+    (dict(rstd=P2), GB_ERR_UNSUPPORTED, "rstd"),
+    (dict(state=P4), GB_ERR_UNSUPPORTED, "rng_state"),
+    (dict(D=16385, ldx=16385, ldy=16385), GB_ERR_UNSUPPORTED, "16384"),
+])
+def test_add_layer_norm_rejects(L, kwargs, status, needle):
+    assert norm(L, **kwargs) == status
+    assert needle in L.gb_last_error().decode()
+
+
+def bwd(L, dY=P16, H=P16, w=P16, mean=P16, rstd=P16, dH=None, p=0.0, dR=P16, dX=None, dw=P16, db=P16, D=32, M=4, ld=32):
+    return L.gb_add_layer_norm_backward(dY, ld, H, ld, w, mean, rstd, dH, ld, p, 1, 2, None, dR, ld, dX, ld, dw, db, P16,
+                                        1 << 30, M, D, None)
+
+
+@pytest.mark.parametrize("kwargs,status,needle", [
+    (dict(dY=None), GB_ERR_INVALID_ARG, "dY is null"),
+    (dict(H=None), GB_ERR_INVALID_ARG, "H is null"),
+    (dict(dR=None), GB_ERR_INVALID_ARG, "dR is null"),
+    (dict(p=0.5), GB_ERR_INVALID_ARG, "dX is null"),
+    (dict(dw=None), GB_ERR_INVALID_ARG, "dweight is null"),
+    (dict(db=None), GB_ERR_INVALID_ARG, "dbias is null"),
+    (dict(mean=None), GB_ERR_INVALID_ARG, "mean is null"),
+    (dict(rstd=P2), GB_ERR_UNSUPPORTED, "rstd"),
+    (dict(w=None), GB_ERR_INVALID_ARG, "weight is null"),
+    (dict(ld=16), GB_ERR_INVALID_ARG, "leading dimension"),
+    (dict(D=20000, ld=20000), GB_ERR_UNSUPPORTED, "16384"),
+])
+def test_add_layer_norm_backward_rejects(L, kwargs, status, needle):
+    assert bwd(L, **kwargs) == status
+    assert needle in L.gb_last_error().decode()
+
+
+def test_empty_layer_norms_are_noops_without_a_device(L):
+    assert norm(L, X=None, Y=None, w=None, M=0) == GB_OK and norm(L, X=None, Y=None, w=None, D=0) == GB_OK
+    assert bwd(L, dY=None, H=None, w=None, mean=None, rstd=None, dR=None, dw=None, db=None, D=0) == GB_OK
+    n = ctypes.c_size_t(7)
+    assert L.gb_add_layer_norm_backward_workspace_bytes(0, 5, ctypes.byref(n)) == GB_OK and n.value == 0
+    assert L.gb_add_layer_norm_backward_workspace_bytes(4, 5, None) == GB_ERR_INVALID_ARG
+
+
+def test_python_layer_norm_refuses_host_tensors():
+    import dense_bf16_gemm_persistent_gb300 as gb
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="X"):
+        gb.add_layer_norm(x, w)
+    with pytest.raises(TypeError, match="dY"):
+        gb.add_layer_norm_backward(x, x, w, torch.ones(2), torch.ones(2))
+
+
+def test_reference_layer_norm_gradient_is_the_forward_difference():
+    """The formula that the GPU's gradients are held to, against central differences in 64 bits."""
+    g = torch.Generator().manual_seed(5)
+    h, dy, dh = (torch.randn(3, 17, generator=g, dtype=torch.float64) for _ in range(3))
+    w, b = torch.rand(17, generator=g, dtype=torch.float64) + 0.5, torch.zeros(17, dtype=torch.float64)
+    rstd = (h.var(dim=1, unbiased=False) + 1e-5).rsqrt()
+    dr, dw, db = more_ref.layer_norm_gradient(dy, h, w, h.mean(dim=1), rstd, dh)
+
+    def loss(h_, w_, b_):
+        off = h_ - h_.mean(dim=1, keepdim=True)
+        return (dy * (off * (off.square().mean(dim=1, keepdim=True) + 1e-5).rsqrt() * w_ + b_)).sum() + (dh * h_).sum()
+    for grad, at, f in ((dr, h, lambda t: loss(t, w, b)), (dw, w, lambda t: loss(h, t, b)), (db, b, lambda t: loss(h, w, t))):
+        v = torch.from_numpy(np.random.default_rng(1).standard_normal(tuple(at.shape)))
+        # a central difference is off by step^2 times a third derivative (of order 10), and 1e-16 / step
+        assert abs((f(at + 1e-5 * v) - f(at - 1e-5 * v)) / 2e-5 - (grad * v).sum()) < 1e-7
