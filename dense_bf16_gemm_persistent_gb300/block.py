@@ -7,6 +7,7 @@
     add_rms_norm_backward(dY, H, weight, rstd)   ->  (dX, dR, dweight)
     add_layer_norm(X, weight, bias, R, p, seed)  ->  (Y, H, mean, rstd): Y = (H - mean) * rstd * weight + bias
     add_layer_norm_backward(dY, H, weight, mean, rstd)  ->  (dX, dR, dweight, dbias)
+    moe_ffn_gated(X, router, W1, W3, W2, top_k)  ->  (D, ids, weights): the top experts' gated layers, weighted
     dropout(X, p, seed, offset, R)               ->  bf16(keep * X / (1 - p) + R)
 
 Tensors are on the current device.  Argument marshalling only, like the package's module, here by the compiled
@@ -32,7 +33,8 @@ def _bind(m, L, device=torch._C._cuda_getDevice) -> None:
     m.bind(GBError, device, stream, *[ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
         "gb_gemm_linear_w4", "gb_gemm_ffn_gated_w4", "gb_dropout", "gb_add_rms_norm", "gb_add_rms_norm_q8",
         "gb_add_rms_norm_backward", "gb_add_rms_norm_backward_workspace_bytes", "gb_add_layer_norm",
-        "gb_add_layer_norm_backward", "gb_add_layer_norm_backward_workspace_bytes", "gb_last_error")])
+        "gb_add_layer_norm_backward", "gb_add_layer_norm_backward_workspace_bytes",
+        "gb_moe_ffn_gated", "gb_moe_ffn_gated_workspace_bytes", "gb_last_error")])
 
 
 def binding():
@@ -154,3 +156,23 @@ def add_layer_norm_backward(dY: torch.Tensor, H: torch.Tensor, weight: torch.Ten
     if stream is not None:
         return _on(stream, add_layer_norm_backward, dY, H, weight, mean, rstd, dH, p, seed, offset, workspace)
     return (_module or binding()).add_layer_norm_backward(dY, H, weight, mean, rstd, dH, p, seed, offset, workspace)
+
+
+def moe_ffn_gated_workspace_bytes(T: int, I: int, E: int, top_k: int) -> int:  # noqa: E741
+    """Bytes of workspace moe_ffn_gated() needs for T tokens, E experts and I inner columns."""
+    n = ctypes.c_size_t(0)
+    _check(lib().gb_moe_ffn_gated_workspace_bytes(T, I, E, top_k, ctypes.byref(n)))
+    return int(n.value)
+
+
+def moe_ffn_gated(X: torch.Tensor, router: torch.Tensor, W1: torch.Tensor, W3: torch.Tensor, W2: torch.Tensor,
+                  top_k: int, R: torch.Tensor | None = None, renormalize: bool = True, out: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """(D, ids, weights) of a mixture-of-experts layer for a few tokens: each row of X [T,D] goes to the top_k experts
+    of the largest logits X @ router.T (router [E,D]; equal ones: the lower expert first), and
+    D = bf16(R + sum_j weights[:,j] * (silu(X @ W1[e].T) * (X @ W3[e].T)) @ W2[e].T), e = ids[:,j], with W1 and W3
+    [E,I,D] and W2 [E,D,I].  weights [T,top_k] fp32 are the logits' softmax, over the chosen experts (renormalize) or
+    over all; ids [T,top_k] int32 are in falling order of the logits."""
+    if stream is not None:
+        return _on(stream, moe_ffn_gated, X, router, W1, W3, W2, top_k, R, renormalize, out, workspace)
+    return (_module or binding()).moe_ffn_gated(X, router, W1, W3, W2, top_k, R, renormalize, out, workspace)

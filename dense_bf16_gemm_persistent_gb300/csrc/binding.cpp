@@ -28,6 +28,8 @@ decltype(&gb_add_rms_norm_backward_workspace_bytes) f_norm_bwd_ws;
 decltype(&gb_add_layer_norm) f_layer_norm;
 decltype(&gb_add_layer_norm_backward) f_layer_norm_bwd;
 decltype(&gb_add_layer_norm_backward_workspace_bytes) f_layer_norm_bwd_ws;
+decltype(&gb_moe_ffn_gated) f_moe;
+decltype(&gb_moe_ffn_gated_workspace_bytes) f_moe_ws;
 decltype(&gb_last_error) f_last_error;
 PyObject* g_error;   // the package's GBError
 PyObject* g_device;  // gives the current device's number
@@ -115,6 +117,24 @@ Arg matrix(const at::Tensor& t, const char* name, at::ScalarType type, int64_t r
 Arg matrix(PyObject* o, const char* name, at::ScalarType type, int64_t rows, int64_t cols) {
     if (o == Py_None) return {};
     return matrix(tensor(o, name), name, type, rows, cols);
+}
+
+// A matrix for each of `count` experts: [count, rows, cols] with a contiguous last dimension.
+struct Stack {
+    void* p;
+    int64_t ld, apart;
+};
+
+Stack stack(PyObject* o, const char* name, int64_t count, int64_t rows, int64_t cols) {
+    const at::Tensor& t = tensor(o, name);
+    check_type(t, name, kBf16);
+    const auto s = t.sizes();
+    if (s.size() != 3 || s[0] != count || s[1] != rows || s[2] != cols)
+        raise(PyExc_ValueError, std::string(name) + ": expected shape (" + std::to_string(count) + ", " +
+                                    std::to_string(rows) + ", " + std::to_string(cols) + "), got " + shape_of(s));
+    const auto st = t.strides();
+    if (cols > 1 && st[2] != 1) raise(PyExc_ValueError, std::string(name) + ": expected a contiguous last dimension");
+    return {t.data_ptr(), rows > 1 ? st[1] : std::max<int64_t>({st[1], cols, 1}), st[0]};
 }
 
 void* vector(PyObject* o, const char* name, at::ScalarType type, int64_t n) {
@@ -444,9 +464,37 @@ PyObject* add_layer_norm_backward(Args a, Py_ssize_t n) {
                  THPVariable_Wrap(std::move(dbias)));
 }
 
+// X, router, W1, W3, W2, top_k, R, renormalize, out, workspace
+PyObject* moe_ffn_gated(Args a, Py_ssize_t n) {
+    expect<10>(n);
+    const at::Tensor& X = tensor(a[0], "X");
+    const auto [T, D] = sizes(X, "X");
+    const Arg x = matrix(X, "X", kBf16, T, D), r = matrix(a[6], "R", kBf16, T, D);
+    const at::Tensor& router = tensor(a[1], "router");
+    const int64_t E = sizes(router, "router").first;
+    const Arg g = matrix(router, "router", kBf16, E, D);
+    const at::Tensor& W1 = tensor(a[2], "W1");
+    if (W1.dim() != 3) raise(PyExc_ValueError, "W1: expected a 3-D tensor, got shape " + shape_of(W1.sizes()));
+    const int64_t I = W1.size(1);
+    const Stack w1 = stack(a[2], "W1", E, I, D), w3 = stack(a[3], "W3", E, I, D), w2 = stack(a[4], "W2", E, D, I);
+    const int top = static_cast<int>(std::clamp<int64_t>(number(a[5]), INT_MIN, INT_MAX));
+    const int renormalize = PyObject_IsTrue(a[7]);
+    if (renormalize < 0) throw Raised{};
+    size_t need = 0;
+    check(f_moe_ws(T, I, E, top, &need));
+    const at::Tensor workspace = scratch(a[9], need, X);
+    Out out(a[8], "out", kBf16, T, D, X);
+    at::Tensor ids = make({T, top}, at::kInt, X), weights = make({T, top}, at::kFloat, X);
+    check(unlocked(f_moe, x.p, x.ld, g.p, g.ld, w1.p, w1.ld, w1.apart, w3.p, w3.ld, w3.apart, w2.p, w2.ld, w2.apart, r.p,
+                   r.ld, top, renormalize, out.arg.p, out.arg.ld, static_cast<int32_t*>(ids.data_ptr()),
+                   static_cast<float*>(weights.data_ptr()), workspace.data_ptr(), workspace.nbytes(), T, D, I, E,
+                   current_stream()));
+    return tuple(out.object(), THPVariable_Wrap(std::move(ids)), THPVariable_Wrap(std::move(weights)));
+}
+
 // GBError, the two functions, then the addresses of the C functions in the order of the declarations above
 PyObject* bind(Args a, Py_ssize_t n) {
-    constexpr int count = 11;
+    constexpr int count = 13;
     expect<count + 3>(n);
     void* at[count];
     for (int i = 0; i < count; ++i) at[i] = address(a[i + 3]);
@@ -460,7 +508,9 @@ PyObject* bind(Args a, Py_ssize_t n) {
     f_layer_norm = reinterpret_cast<decltype(f_layer_norm)>(at[7]);
     f_layer_norm_bwd = reinterpret_cast<decltype(f_layer_norm_bwd)>(at[8]);
     f_layer_norm_bwd_ws = reinterpret_cast<decltype(f_layer_norm_bwd_ws)>(at[9]);
-    f_last_error = reinterpret_cast<decltype(f_last_error)>(at[10]);
+    f_moe = reinterpret_cast<decltype(f_moe)>(at[10]);
+    f_moe_ws = reinterpret_cast<decltype(f_moe_ws)>(at[11]);
+    f_last_error = reinterpret_cast<decltype(f_last_error)>(at[12]);
     g_error = Py_NewRef(a[0]);
     g_device = Py_NewRef(a[1]);
     g_stream = Py_NewRef(a[2]);
@@ -493,6 +543,7 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<add_rms_norm_backward>("add_rms_norm_backward"),
                          method<add_layer_norm>("add_layer_norm"),
                          method<add_layer_norm_backward>("add_layer_norm_backward"),
+                         method<moe_ffn_gated>("moe_ffn_gated"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gbgemm_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

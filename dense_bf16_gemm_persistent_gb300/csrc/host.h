@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -69,6 +70,17 @@ struct Launch {
         return e == cudaSuccess ? GB_OK : cuda_fail(e, what);
     }
 };
+
+// More than the default 48 KB of dynamic shared memory, once for each kernel and device.  (Two
+// threads may both set the attribute: to the same value.)
+template <class Kernel>
+gb_status_t allow_smem(Kernel kernel, std::atomic<bool>* ready, int dev, size_t most) {
+    if (ready[dev].load(std::memory_order_acquire)) return GB_OK;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
+    ready[dev].store(true, std::memory_order_release);
+    return GB_OK;
+}
 
 inline bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -130,17 +130,6 @@ RowPlan plan_rows(const Mat (&mats)[N], int64_t rows, int64_t cols) {
     return pl;
 }
 
-// More than the default 48 KB of dynamic shared memory, once for each kernel and device.  (Two
-// threads may both set the attribute: to the same value.)
-template <class Kernel>
-gb_status_t allow_smem(Kernel kernel, std::atomic<bool>* ready, int dev, size_t most) {
-    if (ready[dev].load(std::memory_order_acquire)) return GB_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute");
-    ready[dev].store(true, std::memory_order_release);
-    return GB_OK;
-}
-
 // Blocks of `per_sm` threads an SM, a multiple of 8 of them (see the kernels' rows); no more than there are
 // rows for.  (More than are resident at once in places: of the forward pass's 1024 threads at 4096 columns,
 // shared memory holds three blocks of 256, and the fourth of each SM comes after them.)

@@ -390,6 +390,40 @@ GB_API gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, cons
 GB_API gb_status_t gb_add_layer_norm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes);
 
 /*
+ * A whole mixture-of-experts layer for a few tokens:
+ *
+ *   l[t,e] = sum_d X[t,d] G[e,d]                     the top_k largest are token t's experts
+ *   w[t,j] = exp(l[t,e_j]) / sum exp(l[t,e])         over all experts, or (renormalize) over the chosen
+ *   D[t]   = bf16( R[t] + sum_j w[t,j] W2[e_j] . ( silu(W1[e_j] . X[t]) * (W3[e_j] . X[t]) ) )
+ *
+ * Equal logits: the lower expert first.  The logits are summed exactly enough (beyond 32 bits) that the choice
+ * does not depend on the order of a sum.  A NaN logit counts as the lowest and makes the token's weights NaN.
+ * Products are bf16 with fp32 sums; the inner activation, between the two products, is kept as two bf16 terms
+ * (16 bits); the weighted sum is fp32, and D is rounded once.  Results are the same on every run.
+ *   X       [T,D] (ldx);  G (router) [E,D] (ldrouter)
+ *   W1, W3  E matrices [I,D] (ld1, ld3), `expert1`, `expert3` elements apart
+ *   W2      E matrices [D,I] (ld2), `expert2` elements apart
+ *   R       [T,D] (ldr) or NULL;  D [T,D] (ldd): any 2-byte aligned address and leading dimension; D == R (same
+ *           pointer and leading dimension) is allowed, other overlaps are not
+ *   ids     [T,top_k] int32 and weights [T,top_k] fp32, contiguous: the choice, in falling order of the logits
+ *   workspace  device memory, 16-byte aligned, of at least gb_moe_ffn_gated_workspace_bytes(); need not be
+ *           cleared; calls that overlap on the GPU need one each
+ * X, G, W1, W3, W2: bf16, base address 16-byte aligned, and leading dimensions and distances of experts
+ * multiples of 8 elements; D and I any number.  At most 1024 experts and top_k = 16.  Up to 64 tokens read each
+ * chosen expert's matrices once (up to 32 that chose it: once in registers, beyond it again from L2); the call's
+ * time then grows as if there were a call for each 64.  T == 0 is a no-op.
+ * An infinity in W2 gives NaN.
+ */
+GB_API gb_status_t gb_moe_ffn_gated(const void* X, int64_t ldx, const void* router, int64_t ldrouter, const void* W1,
+                                    int64_t ld1, int64_t expert1, const void* W3, int64_t ld3, int64_t expert3,
+                                    const void* W2, int64_t ld2, int64_t expert2, const void* R, int64_t ldr, int top_k,
+                                    int renormalize, void* D, int64_t ldd, int32_t* ids, float* weights, void* workspace,
+                                    size_t workspace_bytes, int64_t T, int64_t D_cols, int64_t I, int64_t E, void* stream);
+
+/* Workspace bytes of gb_moe_ffn_gated. */
+GB_API gb_status_t gb_moe_ffn_gated_workspace_bytes(int64_t T, int64_t I, int64_t E, int top_k, size_t* bytes);
+
+/*
  * Workspace bytes the split-K call needs for this problem on the current
  * device under the current configuration (ffn: 0 = linear, 1 = FFN fusion;
  * splits as above).  Writes 0 when the plan does not split.  Needs a CUDA

@@ -63,3 +63,42 @@ def layer_norm_gradient_tolerances(dy, h, w, mean, rstd, dh, dr):
     # warps, and the join's chain and tree
     rows = -(-dy.shape[0] // 8) + 8 + 48
     return e, (rows + 3) * U * (dy * xhat).abs().sum(dim=0) + TINY, rows * U * dy.abs().sum(dim=0) + TINY
+
+
+def routing(x, router, top_k, renormalize):
+    """(ids, weights) in 64 bits: the largest logits, the lower expert first where they are equal; NaN last."""
+    logits = x.double() @ router.double().T
+    nan = torch.isnan(logits)
+    order = torch.sort(torch.where(nan, -torch.inf, logits), dim=1, descending=True, stable=True).indices[:, :top_k]
+    p = torch.softmax(torch.gather(logits, 1, order) if renormalize else logits, dim=1)
+    weights = p if renormalize else torch.gather(p, 1, order)
+    return order, torch.where(nan.any(dim=1, keepdim=True), torch.nan, weights)
+
+
+def moe(x, w1, w3, w2, r, ids, weights):
+    """(D, tolerance) for a choice: in 64 bits, expert by expert."""
+    t, d = x.shape
+    inner = w1.shape[1]
+    out = torch.zeros((t, d), dtype=torch.float64, device=x.device)
+    tol = torch.zeros_like(out)
+    xd = x.double()
+    # an fp32 sum of n products in an mma (2^-23 each: the adder may truncate), and the joins of the warps' parts
+    first, second = (d + 24) * 2.0 ** -23, (inner + 24) * 2.0 ** -23
+    for e in ids.unique().tolist():
+        at = (ids == e)
+        rows = at.any(dim=1).nonzero()[:, 0]
+        w = (weights.double() * at).sum(dim=1)[rows][:, None]
+        a, b = xd[rows] @ w1[e].double().T, xd[rows] @ w3[e].double().T
+        off_a = first * (xd[rows].abs() @ w1[e].double().abs().T)
+        off_b = first * (xd[rows].abs() @ w3[e].double().abs().T)
+        gate = ref.act(a, "silu")
+        act = gate * b
+        # the activation's slope is at most 1.13, it is computed to 2^-20 of its argument; two bf16 terms keep 2^-16
+        off = (1.13 * off_a + 2.0 ** -20 * a.abs()) * (b.abs() + off_b) + gate.abs() * off_b + 2.0 ** -16 * act.abs()
+        w2d = w2[e].double()
+        out[rows] += w * (act @ w2d.T)
+        tol[rows] += w.abs() * (off @ w2d.abs().T + second * (act.abs() @ w2d.abs().T)) * (1 + 2.0 ** -10)
+    tol = tol + (2.0 ** -20) * out.abs()
+    if r is not None:
+        out = out + r.double()
+    return out, tol + (HALF_BF16 + 2.0 ** -20) * out.abs() + HALF_BF16 * tol + TINY

@@ -104,3 +104,64 @@ def test_reference_layer_norm_gradient_is_the_forward_difference():
         v = torch.from_numpy(np.random.default_rng(1).standard_normal(tuple(at.shape)))
         # a central difference is off by step^2 times a third derivative (of order 10), and 1e-16 / step
         assert abs((f(at + 1e-5 * v) - f(at - 1e-5 * v)) / 2e-5 - (grad * v).sum()) < 1e-7
+
+
+# ---------------------------------------------------------------------------------- mixture of experts
+
+def moe(L, X=P16, ldx=64, router=P16, ldrouter=64, W1=P16, ld1=64, e1=2048, W3=P16, ld3=64, e3=2048, W2=P16, ld2=32, e2=2048,
+        R=None, ldr=0, top=2, D=P16, ldd=64, ids=P16, weights=P16, ws=P16, wsb=1 << 30, T=3, d=64, inner=32, experts=4):
+    return L.gb_moe_ffn_gated(X, ldx, router, ldrouter, W1, ld1, e1, W3, ld3, e3, W2, ld2, e2, R, ldr, top, 1, D, ldd, ids,
+                              weights, ws, wsb, T, d, inner, experts, None)
+
+
+@pytest.mark.parametrize("kwargs,status,needle", [
+    (dict(X=None), GB_ERR_INVALID_ARG, "X is null"),
+    (dict(router=None), GB_ERR_INVALID_ARG, "router is null"),
+    (dict(W1=None), GB_ERR_INVALID_ARG, "W1 is null"),
+    (dict(W3=None), GB_ERR_INVALID_ARG, "W3 is null"),
+    (dict(W2=None), GB_ERR_INVALID_ARG, "W2 is null"),
+    (dict(D=None), GB_ERR_INVALID_ARG, "D is null"),
+    (dict(ids=None), GB_ERR_INVALID_ARG, "ids is null"),
+    (dict(weights=None), GB_ERR_INVALID_ARG, "weights is null"),
+    (dict(ws=None), GB_ERR_INVALID_ARG, "workspace"),
+    (dict(wsb=100), GB_ERR_INVALID_ARG, "workspace"),
+    (dict(ws=P4), GB_ERR_INVALID_ARG, "16-byte"),
+    (dict(T=-1), GB_ERR_INVALID_ARG, "negative"),
+    (dict(T=1 << 31), GB_ERR_UNSUPPORTED, "2^31"),
+    (dict(inner=0), GB_ERR_INVALID_ARG, "experts of"),
+    (dict(top=0), GB_ERR_INVALID_ARG, "top_k"),
+    (dict(top=5), GB_ERR_INVALID_ARG, "top_k"),
+    (dict(experts=1025), GB_ERR_UNSUPPORTED, "1024"),
+    (dict(experts=64, top=17), GB_ERR_UNSUPPORTED, "top_k"),
+    (dict(ldx=63), GB_ERR_INVALID_ARG, "of X"),
+    (dict(ldx=68), GB_ERR_UNSUPPORTED, "X"),
+    (dict(W1=P4), GB_ERR_UNSUPPORTED, "W1"),
+    (dict(ld2=31), GB_ERR_INVALID_ARG, "of W2"),
+    (dict(e1=2040), GB_ERR_INVALID_ARG, "W1"),
+    (dict(e3=2052), GB_ERR_UNSUPPORTED, "W3"),
+    (dict(e2=0), GB_ERR_INVALID_ARG, "W2"),
+    (dict(ldd=63), GB_ERR_INVALID_ARG, "of D"),
+    (dict(R=P16, ldr=63), GB_ERR_INVALID_ARG, "of R"),
+    (dict(D=P1), GB_ERR_UNSUPPORTED, "2-byte"),
+    (dict(weights=P2), GB_ERR_UNSUPPORTED, "4-byte"),
+])
+def test_moe_ffn_gated_rejects(L, kwargs, status, needle):
+    assert moe(L, **kwargs) == status
+    assert needle in L.gb_last_error().decode()
+
+
+def test_empty_moe_is_a_noop_and_its_workspace_is_counted(L):
+    assert moe(L, X=None, D=None, T=0) == GB_OK
+    n = ctypes.c_size_t(7)
+    # two terms of two bytes for each pair of a token and an expert, rows of whole 16 bytes; a pass has 64 tokens
+    for t, tokens in ((0, 0), (3, 3), (64, 64), (1000, 64)):
+        assert L.gb_moe_ffn_gated_workspace_bytes(t, 33, 8, 2, ctypes.byref(n)) == GB_OK and n.value == tokens * 2 * 40 * 4
+    assert L.gb_moe_ffn_gated_workspace_bytes(3, 33, 8, 9, ctypes.byref(n)) == GB_ERR_INVALID_ARG
+    assert L.gb_moe_ffn_gated_workspace_bytes(3, 33, 8, 2, None) == GB_ERR_INVALID_ARG
+
+
+def test_python_moe_refuses_host_tensors():
+    import dense_bf16_gemm_persistent_gb300 as gb
+    x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(4, 64, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="X"):
+        gb.moe_ffn_gated(x, x, w, w, w, 2)
