@@ -10,7 +10,8 @@ fallback of any kind, and every call raises if the library is missing.
 
 and, from block.py, the operators around them: linear_w4, ffn_gated_w4 (4-bit weights, a few
 tokens), add_rms_norm (and its 8-bit and backward forms), add_layer_norm (and its backward form), dropout,
-moe_ffn_gated (a whole mixture-of-experts layer for a few tokens).
+lora (low-rank adapters of many requests beside a projection), moe_ffn_gated (a whole mixture-of-experts
+layer for a few tokens).
 
 Tensors are torch CUDA bf16 tensors, 2-D with a contiguous last dimension
 (bias: contiguous 1-D).  Work is enqueued on ``torch.cuda.current_stream()``
@@ -105,6 +106,9 @@ def lib() -> ctypes.CDLL:
         L.gb_moe_ffn_gated.argtypes = [p, i64, p, i64, p, i64, i64, p, i64, i64, p, i64, i64, p, i64, i, i, p, i64, p, p, p,
                                        ctypes.c_size_t, i64, i64, i64, i64, p]
         L.gb_moe_ffn_gated_workspace_bytes.argtypes = [i64, i64, i64, i, ctypes.POINTER(ctypes.c_size_t)]
+        L.gb_lora.argtypes = [p, i64, p, i64, i64, p, i64, i64, p, p, p, i64, i, p, i64, p, ctypes.c_size_t, i64, i64, i64, i64,
+                              i64, p]
+        L.gb_lora_workspace_bytes.argtypes = [i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]
         L.gb_version.argtypes = []
         L.gb_version.restype = ctypes.c_char_p
         for name in ("gb_gemm_linear", "gb_gemm_ffn_gated", "gb_gemm_linear_preact", "gb_gemm_linear_dact",
@@ -118,7 +122,7 @@ def lib() -> ctypes.CDLL:
                      "gb_dropout", "gb_add_rms_norm", "gb_add_rms_norm_q8", "gb_add_rms_norm_backward",
                      "gb_add_rms_norm_backward_workspace_bytes", "gb_add_layer_norm", "gb_add_layer_norm_backward",
                      "gb_add_layer_norm_backward_workspace_bytes", "gb_moe_ffn_gated",
-                     "gb_moe_ffn_gated_workspace_bytes"):
+                     "gb_moe_ffn_gated_workspace_bytes", "gb_lora", "gb_lora_workspace_bytes"):
             getattr(L, name).restype = st
         _lib = L
         return L
@@ -378,4 +382,4 @@ def version() -> str:
 from . import block  # noqa: E402
 from .block import (add_layer_norm, add_layer_norm_backward, add_layer_norm_backward_workspace_bytes,  # noqa: E402
                     add_rms_norm, add_rms_norm_backward, add_rms_norm_backward_workspace_bytes, add_rms_norm_q8, dropout,
-                    ffn_gated_w4, linear_w4, moe_ffn_gated, moe_ffn_gated_workspace_bytes)
+                    ffn_gated_w4, linear_w4, lora, lora_workspace_bytes, moe_ffn_gated, moe_ffn_gated_workspace_bytes)

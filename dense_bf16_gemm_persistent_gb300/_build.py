@@ -11,9 +11,9 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libgbgemm.so")
 BINDING = os.path.join(PKG, "_gbgemm_torch.so")
 LOG_DIR = os.path.join(PKG, "_build")
-SOURCES = ["gbgemm.cu", "moe.cu", "rowwise.cu", "w4.cu"]
-HEADERS = ["gemm_kernel.cuh", "host.h", "layernorm.cuh", "moe_kernel.cuh", "ptx.cuh", "probe.cuh", "rowwise.cuh",
-           "skinny.cuh", "w4_kernel.cuh"]
+SOURCES = ["gbgemm.cu", "lora.cu", "moe.cu", "rowwise.cu", "w4.cu"]
+HEADERS = ["gemm_kernel.cuh", "host.h", "layernorm.cuh", "lora_kernel.cuh", "moe_kernel.cuh", "ptx.cuh", "probe.cuh",
+           "rowwise.cuh", "skinny.cuh", "w4_kernel.cuh"]
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden", "-Xptxas", "-v",
               "--diag-suppress", "177"]

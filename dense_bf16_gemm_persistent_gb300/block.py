@@ -1,4 +1,4 @@
-"""The operators around the products: 4-bit layers for a few tokens, the norm, dropout.
+"""The operators around the products: 4-bit layers for a few tokens, norms, dropout, adapters, experts.
 
     linear_w4(X, Wq, scales, bias, R, act)       ->  bf16(act(X @ W.T + bias) + R), W = (q - z) * s
     ffn_gated_w4(X, W1q, s1, W3q, s3)            ->  bf16(silu(X @ W1.T) * (X @ W3.T))
@@ -7,6 +7,7 @@
     add_rms_norm_backward(dY, H, weight, rstd)   ->  (dX, dR, dweight)
     add_layer_norm(X, weight, bias, R, p, seed)  ->  (Y, H, mean, rstd): Y = (H - mean) * rstd * weight + bias
     add_layer_norm_backward(dY, H, weight, mean, rstd)  ->  (dX, dR, dweight, dbias)
+    lora(X, A, B, ids, scale, R, act)            ->  bf16(act(R + scale * (X @ A[id].T) @ B[id].T)), id = ids[row]
     moe_ffn_gated(X, router, W1, W3, W2, top_k)  ->  (D, ids, weights): the top experts' gated layers, weighted
     dropout(X, p, seed, offset, R)               ->  bf16(keep * X / (1 - p) + R)
 
@@ -34,7 +35,7 @@ def _bind(m, L, device=torch._C._cuda_getDevice) -> None:
         "gb_gemm_linear_w4", "gb_gemm_ffn_gated_w4", "gb_dropout", "gb_add_rms_norm", "gb_add_rms_norm_q8",
         "gb_add_rms_norm_backward", "gb_add_rms_norm_backward_workspace_bytes", "gb_add_layer_norm",
         "gb_add_layer_norm_backward", "gb_add_layer_norm_backward_workspace_bytes",
-        "gb_moe_ffn_gated", "gb_moe_ffn_gated_workspace_bytes", "gb_last_error")])
+        "gb_moe_ffn_gated", "gb_moe_ffn_gated_workspace_bytes", "gb_lora", "gb_lora_workspace_bytes", "gb_last_error")])
 
 
 def binding():
@@ -176,3 +177,24 @@ def moe_ffn_gated(X: torch.Tensor, router: torch.Tensor, W1: torch.Tensor, W3: t
     if stream is not None:
         return _on(stream, moe_ffn_gated, X, router, W1, W3, W2, top_k, R, renormalize, out, workspace)
     return (_module or binding()).moe_ffn_gated(X, router, W1, W3, W2, top_k, R, renormalize, out, workspace)
+
+
+def lora_workspace_bytes(M: int, N: int, K: int, r: int) -> int:
+    """Bytes of workspace lora() needs on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(lib().gb_lora_workspace_bytes(M, N, K, r, ctypes.byref(n)))
+    return int(n.value)
+
+
+def lora(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, scale: torch.Tensor | None = None,
+         R: torch.Tensor | None = None, act: str = "none", out: torch.Tensor | None = None,
+         workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """D = bf16(act(R + scale[id] * (X @ A[id].T) @ B[id].T)), id = ids[row]: low-rank adapters of many requests at once
+    (X [M,K], A [adapters,r,K], B [adapters,N,r], ids [M] int32, scale [adapters] fp32 or None, R [M,N] or None).  A
+    row whose id is outside 0 .. adapters - 1 has none: act(R).  Beside a projection: linear(X, W, bias,
+    R=lora(X, A, B, ids, scale)), or before its activation lora(..., R=linear(X, W, bias), act=...)."""
+    if stream is not None:
+        return _on(stream, lora, X, A, B, ids, scale, R, act, out, workspace)
+    if act not in ACT:
+        raise ValueError(f"act must be one of {sorted(ACT)}")
+    return (_module or binding()).lora(X, A, B, ids, scale, R, ACT[act], out, workspace)

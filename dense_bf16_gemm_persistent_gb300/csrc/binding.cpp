@@ -30,6 +30,8 @@ decltype(&gb_add_layer_norm_backward) f_layer_norm_bwd;
 decltype(&gb_add_layer_norm_backward_workspace_bytes) f_layer_norm_bwd_ws;
 decltype(&gb_moe_ffn_gated) f_moe;
 decltype(&gb_moe_ffn_gated_workspace_bytes) f_moe_ws;
+decltype(&gb_lora) f_lora;
+decltype(&gb_lora_workspace_bytes) f_lora_ws;
 decltype(&gb_last_error) f_last_error;
 PyObject* g_error;   // the package's GBError
 PyObject* g_device;  // gives the current device's number
@@ -119,7 +121,7 @@ Arg matrix(PyObject* o, const char* name, at::ScalarType type, int64_t rows, int
     return matrix(tensor(o, name), name, type, rows, cols);
 }
 
-// A matrix for each of `count` experts: [count, rows, cols] with a contiguous last dimension.
+// A matrix for each of `count` experts or adapters: [count, rows, cols] with a contiguous last dimension.
 struct Stack {
     void* p;
     int64_t ld, apart;
@@ -492,9 +494,33 @@ PyObject* moe_ffn_gated(Args a, Py_ssize_t n) {
     return tuple(out.object(), THPVariable_Wrap(std::move(ids)), THPVariable_Wrap(std::move(weights)));
 }
 
+// X, A, B, ids, scale, R, act, out, workspace
+PyObject* lora(Args a, Py_ssize_t n) {
+    expect<9>(n);
+    const at::Tensor& X = tensor(a[0], "X");
+    const auto [M, K] = sizes(X, "X");
+    const at::Tensor &A = tensor(a[1], "A"), &B = tensor(a[2], "B");
+    if (A.dim() != 3) raise(PyExc_ValueError, "A: expected a 3-D tensor, got shape " + shape_of(A.sizes()));
+    if (B.dim() != 3) raise(PyExc_ValueError, "B: expected a 3-D tensor, got shape " + shape_of(B.sizes()));
+    const int64_t adapters = A.size(0), rank = A.size(1), N = B.size(1);
+    const Arg x = matrix(X, "X", kBf16, M, K), r = matrix(a[5], "R", kBf16, M, N);
+    const Stack down = stack(a[1], "A", adapters, rank, K), up = stack(a[2], "B", adapters, N, rank);
+    tensor(a[3], "ids");
+    const void* ids = vector(a[3], "ids", at::kInt, M);
+    const void* scale = vector(a[4], "scale", at::kFloat, adapters);
+    size_t need = 0;
+    check(f_lora_ws(M, N, K, rank, &need));
+    const at::Tensor workspace = scratch(a[8], need, X);
+    Out out(a[7], "out", kBf16, M, N, X);
+    check(unlocked(f_lora, x.p, x.ld, down.p, down.ld, down.apart, up.p, up.ld, up.apart, static_cast<const int32_t*>(ids),
+                   static_cast<const float*>(scale), r.p, r.ld, static_cast<int>(number(a[6])), out.arg.p, out.arg.ld,
+                   workspace.data_ptr(), workspace.nbytes(), M, N, K, rank, adapters, current_stream()));
+    return out.object();
+}
+
 // GBError, the two functions, then the addresses of the C functions in the order of the declarations above
 PyObject* bind(Args a, Py_ssize_t n) {
-    constexpr int count = 13;
+    constexpr int count = 15;
     expect<count + 3>(n);
     void* at[count];
     for (int i = 0; i < count; ++i) at[i] = address(a[i + 3]);
@@ -510,7 +536,9 @@ PyObject* bind(Args a, Py_ssize_t n) {
     f_layer_norm_bwd_ws = reinterpret_cast<decltype(f_layer_norm_bwd_ws)>(at[9]);
     f_moe = reinterpret_cast<decltype(f_moe)>(at[10]);
     f_moe_ws = reinterpret_cast<decltype(f_moe_ws)>(at[11]);
-    f_last_error = reinterpret_cast<decltype(f_last_error)>(at[12]);
+    f_lora = reinterpret_cast<decltype(f_lora)>(at[12]);
+    f_lora_ws = reinterpret_cast<decltype(f_lora_ws)>(at[13]);
+    f_last_error = reinterpret_cast<decltype(f_last_error)>(at[14]);
     g_error = Py_NewRef(a[0]);
     g_device = Py_NewRef(a[1]);
     g_stream = Py_NewRef(a[2]);
@@ -544,6 +572,7 @@ PyMethodDef methods[] = {method<bind>("bind"),
                          method<add_layer_norm>("add_layer_norm"),
                          method<add_layer_norm_backward>("add_layer_norm_backward"),
                          method<moe_ffn_gated>("moe_ffn_gated"),
+                         method<lora>("lora"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_gbgemm_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

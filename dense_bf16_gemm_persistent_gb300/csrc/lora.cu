@@ -1,0 +1,166 @@
+// C ABI of the low-rank adapters: argument checks, launch shapes and launches of the kernels in
+// lora_kernel.cuh.
+#include <algorithm>
+#include <atomic>
+#include <cinttypes>
+
+#include "host.h"
+#include "lora_kernel.cuh"
+
+namespace {
+
+using namespace gb::host;
+using namespace gb::lora;
+
+gb_status_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters) {
+    if (M < 0 || N < 0 || K < 0 || r < 0 || adapters < 0)
+        return fail(GB_ERR_INVALID_ARG, "negative size M=%" PRId64 " N=%" PRId64 " K=%" PRId64 " r=%" PRId64 " adapters=%" PRId64,
+                    M, N, K, r, adapters);
+    // (the kernels count columns in 32 bits, some steps ahead)
+    if (M > kMaxDim || N > kMaxDim - 4096 || K > kMaxDim - 4096 || adapters > kMaxDim)
+        return fail(GB_ERR_UNSUPPORTED, "sizes must be below 2^31 - 4096 (M=%" PRId64 " N=%" PRId64 " K=%" PRId64
+                                        " adapters=%" PRId64 ")", M, N, K, adapters);
+    if (r > kMaxRank) return fail(GB_ERR_UNSUPPORTED, "rank %" PRId64 ": at most %d", r, kMaxRank);
+    return GB_OK;
+}
+
+struct Plan {
+    int down_tile, splits, split_steps, up_tile;
+    int64_t down_blocks, up_blocks, chunks;
+};
+
+// Tiles are as large as leaves a block to each SM's two places: rows of one adapter in a tile share its matrices'
+// loads.  The columns are split for the same, down to a step for each of a block's warps.
+Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
+    Plan pl;
+    const int64_t want = 2 * sms, steps = std::max<int64_t>(1, ceil_div(K, kStep));
+    const int64_t most = std::min<int64_t>(32, ceil_div(steps, kDownWarps));
+    pl.down_tile = kMaxTile;
+    while (pl.down_tile > 1 && ceil_div(M, pl.down_tile) * most < want) pl.down_tile /= 2;
+    const int64_t tiles = ceil_div(M, pl.down_tile);
+    const int64_t splits = std::min(most, ceil_div(want, tiles));
+    pl.split_steps = static_cast<int>(ceil_div(steps, splits));
+    pl.splits = static_cast<int>(ceil_div(steps, pl.split_steps));
+    pl.down_blocks = tiles * pl.splits;
+    pl.chunks = ceil_div(N, kUpWarps * kUpColumns);
+    pl.up_tile = kMaxTile;
+    while (pl.up_tile > 1 && ceil_div(M, pl.up_tile) * pl.chunks < want) pl.up_tile /= 2;
+    pl.up_blocks = ceil_div(M, pl.up_tile) * pl.chunks;
+    return pl;
+}
+
+int64_t low_columns(int64_t r) { return ceil_div(r, 16) * 16; }
+
+int64_t workspace_of(const Plan& pl, int64_t M, int64_t r) { return pl.splits * M * low_columns(r) * 4; }
+
+}  // namespace
+
+extern "C" {
+
+gb_status_t gb_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r, size_t* bytes) {
+    clear_error();
+    if (!bytes) return fail(GB_ERR_INVALID_ARG, "bytes is null");
+    *bytes = 0;
+    gb_status_t st = check_sizes(M, N, K, r, 0);
+    if (st != GB_OK || M == 0 || N == 0 || K == 0 || r == 0) return st;
+    int dev = 0;
+    DeviceInfo info;
+    if ((st = device_info(&dev, &info)) != GB_OK) return st;
+    *bytes = static_cast<size_t>(workspace_of(make_plan(M, N, K, info.sms), M, r));
+    return GB_OK;
+}
+
+gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t apart_a, const void* B, int64_t ldb,
+                    int64_t apart_b, const int32_t* ids, const float* scale, const void* R, int64_t ldr, int act, void* D,
+                    int64_t ldd, void* workspace, size_t workspace_bytes, int64_t M, int64_t N, int64_t K, int64_t r,
+                    int64_t adapters, void* stream) {
+    clear_error();
+    gb_status_t st = check_sizes(M, N, K, r, adapters);
+    if (st != GB_OK) return st;
+    if (act < GB_ACT_NONE || act > GB_ACT_RELU) return fail(GB_ERR_INVALID_ARG, "unknown activation %d", act);
+    if (M == 0 || N == 0) {
+        note_empty();
+        return GB_OK;
+    }
+    if (!D) return fail(GB_ERR_INVALID_ARG, "D is null");
+    if (ldd < N) return fail(GB_ERR_INVALID_ARG, "leading dimension %" PRId64 " of D is below its row length %" PRId64, ldd, N);
+    if (R && ldr < N) return fail(GB_ERR_INVALID_ARG, "leading dimension %" PRId64 " of R is below its row length %" PRId64, ldr, N);
+    if (!aligned_to(D, 2) || !aligned_to(R, 2)) return fail(GB_ERR_UNSUPPORTED, "D and R must be 2-byte aligned");
+    if (!ids) return fail(GB_ERR_INVALID_ARG, "ids is null");
+    if (!aligned_to(ids, 4) || !aligned_to(scale, 4)) return fail(GB_ERR_UNSUPPORTED, "ids and scale must be 4-byte aligned");
+    const bool any = K > 0 && r > 0 && adapters > 0;  // (else D = act(R))
+    if (any) {
+        struct {
+            const char* name;
+            const void* p;
+            int64_t ld, rows, cols, apart, count;
+        } mats[] = {{"X", X, ldx, M, K, 0, 1}, {"A", A, lda, r, K, apart_a, adapters}, {"B", B, ldb, N, r, apart_b, adapters}};
+        for (const auto& m : mats) {
+            if (!m.p) return fail(GB_ERR_INVALID_ARG, "%s is null", m.name);
+            if (m.ld < m.cols)
+                return fail(GB_ERR_INVALID_ARG, "leading dimension %" PRId64 " of %s is below its row length %" PRId64, m.ld,
+                            m.name, m.cols);
+            if (!aligned_to(m.p, 16) || (m.rows > 1 && m.ld % 8))  // (one row has no next one)
+                return fail(GB_ERR_UNSUPPORTED, "%s: base address and rows must be 16-byte aligned (leading dimension %" PRId64
+                                                ")", m.name, m.ld);
+            if (m.count > 1 && (m.apart % 8 || m.apart < (m.rows - 1) * m.ld + m.cols))
+                return fail(m.apart % 8 ? GB_ERR_UNSUPPORTED : GB_ERR_INVALID_ARG,
+                            "%s: adapters %" PRId64 " elements apart (a multiple of 8, and at least a matrix)", m.name, m.apart);
+        }
+    }
+    int dev = 0;
+    DeviceInfo info;
+    if ((st = device_info(&dev, &info)) != GB_OK) return st;
+    const Plan pl = make_plan(M, N, K, info.sms);
+    if (pl.down_blocks > kMaxDim || pl.up_blocks > kMaxDim)
+        return fail(GB_ERR_UNSUPPORTED, "%" PRId64 " rows of %" PRId64 " columns are more than a launch's blocks", M, N);
+    const size_t need = any ? static_cast<size_t>(workspace_of(pl, M, r)) : 0;
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(GB_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0), need);
+    if (need && !aligned_to(workspace, 4)) return fail(GB_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
+
+    Params prm{};
+    prm.x = static_cast<const uint16_t*>(X);
+    prm.a = static_cast<const uint16_t*>(A);
+    prm.b = static_cast<const uint16_t*>(B);
+    prm.ids = ids;
+    prm.scale = scale;
+    prm.r = static_cast<const uint16_t*>(R);
+    prm.d = static_cast<uint16_t*>(D);
+    prm.low = static_cast<float*>(workspace);
+    prm.ldx = ldx;
+    prm.lda = lda;
+    prm.ldb = ldb;
+    prm.ldr = ldr;
+    prm.ldd = ldd;
+    prm.apart_a = apart_a;
+    prm.apart_b = apart_b;
+    prm.m = static_cast<int>(M);
+    prm.n = static_cast<int>(N);
+    prm.k = static_cast<int>(K);
+    prm.rank = static_cast<int>(r);
+    prm.adapters = any ? static_cast<int>(adapters) : 0;
+    prm.ldlow = any ? static_cast<int>(low_columns(r)) : 0;
+    prm.act = act;
+    prm.splits = pl.splits;
+    prm.split_steps = pl.split_steps;
+    prm.chunks = static_cast<int>(pl.chunks);
+    prm.wide_r = aligned_to(R, 16) && (M == 1 || ldr % 8 == 0);
+    prm.wide_d = aligned_to(D, 16) && (M == 1 || ldd % 8 == 0);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    static std::atomic<bool> ready[64];
+    if ((st = allow_smem(up_kernel, ready, dev, 2 * kMaxTile * low_words(kMaxRank) * 4)) != GB_OK) return st;
+    if (any) {
+        prm.tile = pl.down_tile;
+        st = Launch(static_cast<unsigned>(pl.down_blocks), kDownThreads, 0, s)(
+            "lora down launch", r <= 16 ? down_kernel<1> : down_kernel<2>, prm);
+        if (st != GB_OK) return st;
+    }
+    prm.tile = pl.up_tile;
+    const size_t smem = static_cast<size_t>(2) * pl.up_tile * low_words(prm.ldlow) * 4;
+    note_plan("kernel=lora down_tile=%lld splits=%lld down_blocks=%lld up_tile=%lld up_blocks=%lld wide=%lld", pl.down_tile,
+              pl.splits, any ? pl.down_blocks : 0, pl.up_tile, pl.up_blocks, prm.wide_d);
+    return Launch(static_cast<unsigned>(pl.up_blocks), kUpThreads, smem, s)("lora up launch", up_kernel, prm);
+}
+
+}  // extern "C"

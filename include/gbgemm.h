@@ -424,6 +424,34 @@ GB_API gb_status_t gb_moe_ffn_gated(const void* X, int64_t ldx, const void* rout
 GB_API gb_status_t gb_moe_ffn_gated_workspace_bytes(int64_t T, int64_t I, int64_t E, int top_k, size_t* bytes);
 
 /*
+ * Low-rank adapters of many requests at once, added to what a shared projection gave:
+ *
+ *   D[m] = bf16( act( R[m] + scale[a] B[a] . (A[a] . X[m]) ) )        a = ids[m]
+ *
+ * A row whose id is outside 0 .. adapters - 1 (-1, say) has no adapter: D[m] = act(R[m]), and none of A, B or
+ * scale reaches it.  With act = none, D can be the R of gb_gemm_linear or gb_gemm_linear_w4 (the adapters first,
+ * the projection on top); with an activation, R is the projection's sum before it.
+ *   X      [M,K] (ldx);  A: `adapters` matrices [r,K] (lda), `apart_a` elements apart;  B: [N,r] (ldb), `apart_b`
+ *   ids    [M] int32, in any order;  scale [adapters] fp32 or NULL (1)
+ *   R      [M,N] (ldr) or NULL (0);  D [M,N] (ldd): any 2-byte aligned address and leading dimension (16-byte
+ *          aligned rows move in 16-byte words); D == R (same pointer and leading dimension) is allowed, other
+ *          overlaps are not
+ *   workspace  device memory, 4-byte aligned, of at least gb_lora_workspace_bytes(); need not be cleared;
+ *          calls that overlap on the GPU need one each
+ * X, A, B: bf16, base address 16-byte aligned, leading dimensions and distances of adapters multiples of 8
+ * elements; M, N, K any number, r at most 256.  Products are bf16 with fp32 sums; A . X, scaled, is multiplied
+ * by B as two bf16 terms (16 bits), and the result is rounded once.  An infinity in B gives NaN.  M == 0 or N == 0 is a
+ * no-op.  Results are the same on every run, and a row's do not depend on the other rows' ids.
+ */
+GB_API gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t apart_a, const void* B, int64_t ldb,
+                           int64_t apart_b, const int32_t* ids, const float* scale, const void* R, int64_t ldr, int act,
+                           void* D, int64_t ldd, void* workspace, size_t workspace_bytes, int64_t M, int64_t N, int64_t K,
+                           int64_t r, int64_t adapters, void* stream);
+
+/* Workspace bytes of gb_lora on the current device. */
+GB_API gb_status_t gb_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r, size_t* bytes);
+
+/*
  * Workspace bytes the split-K call needs for this problem on the current
  * device under the current configuration (ffn: 0 = linear, 1 = FFN fusion;
  * splits as above).  Writes 0 when the plan does not split.  Needs a CUDA

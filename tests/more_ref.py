@@ -102,3 +102,28 @@ def moe(x, w1, w3, w2, r, ids, weights):
     if r is not None:
         out = out + r.double()
     return out, tol + (HALF_BF16 + 2.0 ** -20) * out.abs() + HALF_BF16 * tol + TINY
+
+
+def lora(x, a, b, ids, scale, r, act="none"):
+    """(D, tolerance): row by row's adapter, in 64 bits."""
+    m, k = x.shape
+    count, n, rank = b.shape
+    v = r.double() if r is not None else torch.zeros((m, n), dtype=torch.float64, device=x.device)
+    off = U * v.abs()
+    for i in ids.unique().tolist():
+        if not 0 <= i < count:
+            continue
+        rows = (ids == i).nonzero()[:, 0]
+        s = float(scale[i]) if scale is not None else 1.0
+        xd, ad, bd = x[rows].double(), a[i].double(), b[i].double()
+        low = xd @ ad.T * s
+        # an fp32 sum of k products in an mma (2^-23 each: the adder may truncate) and the joins of its parts; the
+        # product by the scale; two bf16 terms; then 2 rank products, and R
+        e = (k + 48) * 2.0 ** -23 * (xd.abs() @ ad.abs().T) * abs(s) + (2.0 ** -16 + 2 * U) * low.abs()
+        v[rows] += low @ bd.T
+        off[rows] += e @ bd.abs().T + (2 * rank + 4) * 2.0 ** -23 * (low.abs() @ bd.abs().T)
+    off = off + U * v.abs()
+    want = ref.act(v, act)
+    # the activations' slopes are at most 1.13; they are computed to 2^-20 of their argument
+    tol = 1.13 * off + (2.0 ** -20 * v.abs() if act in ("gelu_tanh", "silu") else 0)
+    return want, tol + HALF_BF16 * want.abs() + HALF_BF16 * tol + TINY

@@ -165,3 +165,56 @@ def test_python_moe_refuses_host_tensors():
     x, w = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(4, 64, 64, dtype=torch.bfloat16)
     with pytest.raises(TypeError, match="X"):
         gb.moe_ffn_gated(x, x, w, w, w, 2)
+
+
+# ---------------------------------------------------------------------------------- low-rank adapters
+
+def lora(L, X=P16, ldx=64, A=P16, lda=64, aa=512, B=P16, ldb=8, ab=256, ids=P16, scale=None, R=None, ldr=0, act=0, D=P16,
+         ldd=32, ws=P16, wsb=1 << 30, M=3, N=32, K=64, r=8, adapters=4):
+    return L.gb_lora(X, ldx, A, lda, aa, B, ldb, ab, ids, scale, R, ldr, act, D, ldd, ws, wsb, M, N, K, r, adapters, None)
+
+
+@pytest.mark.parametrize("kwargs,status,needle", [
+    (dict(X=None), GB_ERR_INVALID_ARG, "X is null"),
+    (dict(A=None), GB_ERR_INVALID_ARG, "A is null"),
+    (dict(B=None), GB_ERR_INVALID_ARG, "B is null"),
+    (dict(D=None), GB_ERR_INVALID_ARG, "D is null"),
+    (dict(ids=None), GB_ERR_INVALID_ARG, "ids is null"),
+    (dict(M=-1), GB_ERR_INVALID_ARG, "negative"),
+    (dict(N=1 << 31), GB_ERR_UNSUPPORTED, "2^31"),
+    (dict(r=257, ldb=264), GB_ERR_UNSUPPORTED, "rank"),
+    (dict(act=4), GB_ERR_INVALID_ARG, "activation"),
+    (dict(ldx=63), GB_ERR_INVALID_ARG, "of X"),
+    (dict(ldx=65), GB_ERR_UNSUPPORTED, "X"),
+    (dict(lda=60), GB_ERR_INVALID_ARG, "of A"),
+    (dict(B=P4), GB_ERR_UNSUPPORTED, "B"),
+    (dict(ldb=12), GB_ERR_UNSUPPORTED, "B"),
+    (dict(aa=504), GB_ERR_INVALID_ARG, "A"),
+    (dict(ab=260), GB_ERR_UNSUPPORTED, "B"),
+    (dict(ldd=31), GB_ERR_INVALID_ARG, "of D"),
+    (dict(R=P16, ldr=31), GB_ERR_INVALID_ARG, "of R"),
+    (dict(R=P1, ldr=32), GB_ERR_UNSUPPORTED, "2-byte"),
+    (dict(ids=P2), GB_ERR_UNSUPPORTED, "4-byte"),
+    (dict(scale=P2), GB_ERR_UNSUPPORTED, "4-byte"),
+])
+def test_lora_rejects(L, kwargs, status, needle):
+    assert lora(L, **kwargs) == status
+    assert needle in L.gb_last_error().decode()
+
+
+def test_empty_lora_is_a_noop(L):
+    assert lora(L, X=None, A=None, B=None, D=None, ids=None, M=0) == GB_OK
+    assert lora(L, X=None, A=None, B=None, D=None, ids=None, N=0) == GB_OK
+    n = ctypes.c_size_t(7)
+    assert L.gb_lora_workspace_bytes(0, 8, 8, 8, ctypes.byref(n)) == GB_OK and n.value == 0
+    assert L.gb_lora_workspace_bytes(8, 8, 8, 300, ctypes.byref(n)) == GB_ERR_UNSUPPORTED
+    assert L.gb_lora_workspace_bytes(8, 8, 8, 8, None) == GB_ERR_INVALID_ARG
+
+
+def test_python_lora_refuses_host_tensors():
+    import dense_bf16_gemm_persistent_gb300 as gb
+    x, a = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(4, 8, 64, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="X"):
+        gb.lora(x, a, a.transpose(1, 2).contiguous(), torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="act"):
+        gb.lora(x, a, a, torch.zeros(2, dtype=torch.int32), act="tanh")
