@@ -180,7 +180,7 @@ def moe_ffn_gated(X: torch.Tensor, router: torch.Tensor, W1: torch.Tensor, W3: t
 
 
 def lora_workspace_bytes(M: int, N: int, K: int, r: int) -> int:
-    """Bytes of workspace lora() needs on the current device."""
+    """Bytes of workspace lora() needs for M rows of K and N columns and a rank of r."""
     n = ctypes.c_size_t(0)
     _check(lib().gb_lora_workspace_bytes(M, N, K, r, ctypes.byref(n)))
     return int(n.value)

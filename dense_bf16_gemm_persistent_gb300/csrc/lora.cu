@@ -25,33 +25,38 @@ gb_status_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adap
 }
 
 struct Plan {
-    int down_tile, splits, split_steps, up_tile;
-    int64_t down_blocks, up_blocks, chunks;
+    int down_tile, cluster, up_tile, parts;
+    int64_t down_blocks, up_blocks;
 };
 
 // Tiles are as large as leaves a block to each SM's two places: rows of one adapter in a tile share its matrices'
-// loads.  The columns are split for the same, down to a step for each of a block's warps.
+// loads.  X's columns are shared out to a cluster for the same, down to a step for each of its warps; D's to
+// blocks, down to 32 columns for each of their warps.
 Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
     Plan pl;
-    const int64_t want = 2 * sms, steps = std::max<int64_t>(1, ceil_div(K, kStep));
-    const int64_t most = std::min<int64_t>(32, ceil_div(steps, kDownWarps));
+    const int64_t slots = 2 * sms, steps = ceil_div(K, kStep);
+    int most = 1;
+    while (most < 8 && most * kWarps < steps) most *= 2;
     pl.down_tile = kMaxTile;
-    while (pl.down_tile > 1 && ceil_div(M, pl.down_tile) * most < want) pl.down_tile /= 2;
-    const int64_t tiles = ceil_div(M, pl.down_tile);
-    const int64_t splits = std::min(most, ceil_div(want, tiles));
-    pl.split_steps = static_cast<int>(ceil_div(steps, splits));
-    pl.splits = static_cast<int>(ceil_div(steps, pl.split_steps));
-    pl.down_blocks = tiles * pl.splits;
-    pl.chunks = ceil_div(N, kUpWarps * kUpColumns);
+    while (pl.down_tile > 1 && ceil_div(M, pl.down_tile) * most < slots) pl.down_tile /= 2;
+    const int64_t down_tiles = ceil_div(M, pl.down_tile);
+    pl.cluster = 1;
+    while (pl.cluster < most && down_tiles * pl.cluster < slots) pl.cluster *= 2;
+    pl.down_blocks = down_tiles * pl.cluster;
+    const int64_t most_parts = ceil_div(N, kWarps * kColumns);
     pl.up_tile = kMaxTile;
-    while (pl.up_tile > 1 && ceil_div(M, pl.up_tile) * pl.chunks < want) pl.up_tile /= 2;
-    pl.up_blocks = ceil_div(M, pl.up_tile) * pl.chunks;
+    while (pl.up_tile > 1 && ceil_div(M, pl.up_tile) * most_parts < slots) pl.up_tile /= 2;
+    const int64_t up_tiles = ceil_div(M, pl.up_tile);
+    pl.parts = static_cast<int>(std::min(most_parts, std::max<int64_t>(1, slots / up_tiles)));
+    pl.up_blocks = up_tiles * pl.parts;
     return pl;
 }
 
-int64_t low_columns(int64_t r) { return ceil_div(r, 16) * 16; }
+int64_t low_columns(int64_t r) { return r <= 16 ? 16 : ceil_div(r, 32) * 32; }
 
-int64_t workspace_of(const Plan& pl, int64_t M, int64_t r) { return pl.splits * M * low_columns(r) * 4; }
+int64_t workspace_of(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
+
+size_t down_smem(int teams, int tiles) { return static_cast<size_t>(kWarps + 2 * teams) * tiles * 4 * 128 * 4; }
 
 }  // namespace
 
@@ -61,13 +66,9 @@ gb_status_t gb_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r, 
     clear_error();
     if (!bytes) return fail(GB_ERR_INVALID_ARG, "bytes is null");
     *bytes = 0;
-    gb_status_t st = check_sizes(M, N, K, r, 0);
-    if (st != GB_OK || M == 0 || N == 0 || K == 0 || r == 0) return st;
-    int dev = 0;
-    DeviceInfo info;
-    if ((st = device_info(&dev, &info)) != GB_OK) return st;
-    *bytes = static_cast<size_t>(workspace_of(make_plan(M, N, K, info.sms), M, r));
-    return GB_OK;
+    const gb_status_t st = check_sizes(M, N, K, r, 0);
+    if (st == GB_OK && M > 0 && N > 0 && K > 0 && r > 0) *bytes = static_cast<size_t>(workspace_of(M, r));
+    return st;
 }
 
 gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t apart_a, const void* B, int64_t ldb,
@@ -114,10 +115,10 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     const Plan pl = make_plan(M, N, K, info.sms);
     if (pl.down_blocks > kMaxDim || pl.up_blocks > kMaxDim)
         return fail(GB_ERR_UNSUPPORTED, "%" PRId64 " rows of %" PRId64 " columns are more than a launch's blocks", M, N);
-    const size_t need = any ? static_cast<size_t>(workspace_of(pl, M, r)) : 0;
+    const size_t need = any ? static_cast<size_t>(workspace_of(M, r)) : 0;
     if (need && (!workspace || workspace_bytes < need))
         return fail(GB_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0), need);
-    if (need && !aligned_to(workspace, 4)) return fail(GB_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
+    if (need && !aligned_to(workspace, 16)) return fail(GB_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
 
     Params prm{};
     prm.x = static_cast<const uint16_t*>(X);
@@ -127,7 +128,7 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     prm.scale = scale;
     prm.r = static_cast<const uint16_t*>(R);
     prm.d = static_cast<uint16_t*>(D);
-    prm.low = static_cast<float*>(workspace);
+    prm.low = static_cast<uint16_t*>(workspace);
     prm.ldx = ldx;
     prm.lda = lda;
     prm.ldb = ldb;
@@ -142,25 +143,30 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     prm.adapters = any ? static_cast<int>(adapters) : 0;
     prm.ldlow = any ? static_cast<int>(low_columns(r)) : 0;
     prm.act = act;
-    prm.splits = pl.splits;
-    prm.split_steps = pl.split_steps;
-    prm.chunks = static_cast<int>(pl.chunks);
+    prm.cluster = pl.cluster;
+    prm.parts = pl.parts;
     prm.wide_r = aligned_to(R, 16) && (M == 1 || ldr % 8 == 0);
     prm.wide_d = aligned_to(D, 16) && (M == 1 || ldd % 8 == 0);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    static std::atomic<bool> ready[64];
-    if ((st = allow_smem(up_kernel, ready, dev, 2 * kMaxTile * low_words(kMaxRank) * 4)) != GB_OK) return st;
     if (any) {
+        const int tiles = r <= 16 ? 1 : 2;
+        prm.teams = 1;
+        while (prm.teams < kWarps && prm.teams * 16 * tiles < r) prm.teams *= 2;
         prm.tile = pl.down_tile;
-        st = Launch(static_cast<unsigned>(pl.down_blocks), kDownThreads, 0, s)(
-            "lora down launch", r <= 16 ? down_kernel<1> : down_kernel<2>, prm);
+        static std::atomic<bool> ready[64];
+        if ((st = allow_smem(down_kernel<2>, ready, dev, down_smem(kWarps, 2))) != GB_OK) return st;
+        st = Launch(static_cast<unsigned>(pl.down_blocks), kThreads, down_smem(prm.teams, tiles), s, pl.cluster)(
+            "lora down launch", tiles == 1 ? down_kernel<1> : down_kernel<2>, prm);
         if (st != GB_OK) return st;
     }
     prm.tile = pl.up_tile;
+    note_plan("kernel=lora down_tile=%lld cluster=%lld down_blocks=%lld up_tile=%lld up_blocks=%lld wide=%lld", pl.down_tile,
+              pl.cluster, any ? pl.down_blocks : 0, pl.up_tile, pl.up_blocks, prm.wide_d);
     const size_t smem = static_cast<size_t>(2) * pl.up_tile * low_words(prm.ldlow) * 4;
-    note_plan("kernel=lora down_tile=%lld splits=%lld down_blocks=%lld up_tile=%lld up_blocks=%lld wide=%lld", pl.down_tile,
-              pl.splits, any ? pl.down_blocks : 0, pl.up_tile, pl.up_blocks, prm.wide_d);
-    return Launch(static_cast<unsigned>(pl.up_blocks), kUpThreads, smem, s)("lora up launch", up_kernel, prm);
+    static std::atomic<bool> ready[64];
+    if ((st = allow_smem(up_kernel<32>, ready, dev, 2 * kMaxTile * low_words(kMaxRank) * 4)) != GB_OK) return st;
+    return Launch(static_cast<unsigned>(pl.up_blocks), kThreads, smem, s)(
+        "lora up launch", prm.ldlow <= 16 ? up_kernel<16> : up_kernel<32>, prm);
 }
 
 }  // extern "C"

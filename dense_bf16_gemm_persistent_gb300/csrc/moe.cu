@@ -130,23 +130,26 @@ gb_status_t gb_moe_ffn_gated(const void* X, int64_t ldx, const void* router, int
     prm.renormalize = renormalize != 0;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-    int route = 1;  // CTAs of a token's router: an expert to each of their warps
-    while (route < 8 && route * kWarps < E) route *= 2;
+    // a token's router: warps for 512 columns of each expert, as far as eight CTAs go
+    int route = 1, parts = 1;
+    while (route < 8 && route * kWarps < E * ceil_div(D, 512)) route *= 2;
+    while (2 * parts * E <= route * kWarps && parts < ceil_div(D, 256)) parts *= 2;
     const int64_t tiles = ceil_div(D, kRows), slots = 2 * info.sms;
     int share = 1;  // CTAs of a tile of D: as many as run at once
     while (share < 8 && tiles * share * 2 <= slots) share *= 2;
+    prm.share = share;
     for (int64_t at = 0; at < T; at += kPassTokens) {
         prm.tokens = static_cast<int>(std::min<int64_t>(T - at, kPassTokens));
         const int64_t chosen = std::min<int64_t>(E, static_cast<int64_t>(prm.tokens) * top_k);
         const int64_t units = chosen * ceil_div(I, kRows), blocks = std::min(units, slots);
         if ((st = Launch(static_cast<unsigned>(prm.tokens * route), kThreads, 0, s, route)("moe router launch", router_kernel,
-                                                                                          prm, route)) != GB_OK)
+                                                                                          prm, route, parts)) != GB_OK)
             return st;
         if ((st = Launch(static_cast<unsigned>(blocks), kThreads, 0, s)("moe gated product launch", up_kernel, prm)) != GB_OK)
             return st;
         const size_t smem = static_cast<size_t>(kWarps) * prm.tokens * kRows * 4;
         if ((st = Launch(static_cast<unsigned>(tiles * share), kThreads, smem, s, share)("moe second product launch",
-                                                                                        down_kernel, prm, share)) != GB_OK)
+                                                                                        down_kernel, prm)) != GB_OK)
             return st;
         note_plan("kernel=moe_ffn_gated tokens=%lld router=%lld up_blocks=%lld tiles=%lld cluster=%lld passes=%lld", prm.tokens,
                   route, blocks, tiles, share, ceil_div(T, kPassTokens));

@@ -20,6 +20,7 @@ constexpr int kPassTokens = 64;  // of a pass: a bit each in an expert's mask
 constexpr int kPairs = kPassTokens * kMaxTop;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRows = 16;        // weight rows of a tile
+constexpr int kAhead = 16;       // steps of the second products that are on their way to L2 before their launch
 
 struct Params {
     const uint16_t* x;
@@ -34,7 +35,19 @@ struct Params {
     int64_t ldw[3], expert[3];  // elements between rows, and between experts
     int tokens, d, inner, experts, top;
     int renormalize;
+    int share;               // CTAs of a tile of D in the last launch
 };
+
+// Which of the second products' steps a warp has: all chosen experts' steps one after the other, shared out evenly.
+struct Share {
+    int64_t at, end;
+};
+
+__device__ __forceinline__ Share share_of(int actives, int steps, int share, int rank, int warp) {
+    const int64_t all = static_cast<int64_t>(actives) * steps;
+    const int shares = share * kWarps, mine = rank * kWarps + warp;
+    return {all * mine / shares, all * (mine + 1) / shares};
+}
 
 // ---------------------------------------------------------------- router
 
@@ -47,10 +60,10 @@ __device__ __forceinline__ void add_exact(float& s, float& err, float p) {
     s = t;
 }
 
-__device__ __forceinline__ double exact_dot(const uint16_t* a, const uint16_t* b, int n, int lane) {
+__device__ __forceinline__ double exact_dot(const uint16_t* a, const uint16_t* b, int first, int last, int n, int lane) {
     float s = 0.f, err = 0.f;
-#pragma unroll 4
-    for (int col = 8 * lane; col < n; col += 256) {
+#pragma unroll 8
+    for (int col = first + 8 * lane; col < last; col += 256) {
         const uint4 u = load_edge(a, col, n), v = load_edge(b, col, n);
         const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -66,67 +79,84 @@ __device__ __forceinline__ double exact_dot(const uint16_t* a, const uint16_t* b
     return v;
 }
 
-// Cluster blockIdx.x / size is token's; its CTAs share the experts, and the first one chooses.  A logit that
-// is NaN is chosen last, and makes the token's weights NaN.
-__global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ Params p, int cluster) {
+// A logit as a whole number of the same order (comparisons in 64-bit floating point are slow): 0 for a NaN.
+__device__ __forceinline__ uint64_t order_of(double v) {
+    const uint64_t u = static_cast<uint64_t>(__double_as_longlong(v + 0.0));  // (-0 is 0)
+    return v != v ? 0 : u >> 63 ? ~u : u | 0x8000000000000000ull;
+}
+__device__ __forceinline__ double value_of(uint64_t key) {
+    return __longlong_as_double(static_cast<long long>(key >> 63 ? key & 0x7fffffffffffffffull : ~key));
+}
+
+// A cluster to a token: its warps share the experts and, where there are more warps than experts, `parts` of the
+// columns; the cluster's first CTA chooses.  A logit that is NaN is chosen last, and makes the token's weights NaN.
+// 40 CTAs of one warp to an expert, and choices by 64-bit floating point comparisons, took 14 us for a token where
+// this takes its launch, a read from memory and the choice.
+__global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ Params p, int cluster, int parts) {
     allow_next_kernel();
     wait_for_earlier_kernels();
-    __shared__ double logits[kMaxExperts];
+    __shared__ double logits[kMaxExperts];  // [expert][part]; then the logits' order
     const int token = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint16_t* x = p.x + token * p.ldx;
     const uint32_t first = mapa_shared(smem_addr(logits), 0);
+    const int span = (p.d + 256 * parts - 1) / (256 * parts) * 256;
     cluster_sync();  // (the first CTA runs: its shared memory may be written)
-    for (int e = rank * kWarps + warp; e < p.experts; e += cluster * kWarps) {
-        const double v = exact_dot(x, p.router + e * p.ldrouter, p.d, lane);
-        if (lane == 0) asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(first + 8 * e), "d"(v) : "memory");
+    for (int i = rank * kWarps + warp; i < p.experts * parts; i += cluster * kWarps) {
+        const int e = i / parts, from = i % parts * span;
+        const double v = exact_dot(x, p.router + e * p.ldrouter, from, min(from + span, p.d), p.d, lane);
+        if (lane == 0) asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(first + 8 * i), "d"(v) : "memory");
     }
     cluster_sync();
     if (rank != 0 || warp != 0) return;
 
-    uint32_t taken = 0;  // bit i: expert lane + 32 i
+    uint64_t* keys = reinterpret_cast<uint64_t*>(logits);
     bool nan = false;
-    for (int e = lane; e < p.experts; e += 32) {
-        const double v = logits[e];
-        nan |= v != v;
+    for (int base = 0; base < p.experts; base += 32) {
+        const int e = base + lane;
+        uint64_t key = 0;
+        if (e < p.experts) {
+            double v = logits[e * parts];
+            for (int i = 1; i < parts; ++i) v += logits[e * parts + i];
+            key = order_of(v);
+            nan |= key == 0;
+        }
+        __syncwarp();  // (parts > 1: at most 64 experts, whose sums another lane may still read)
+        if (e < p.experts) keys[e] = key;
+        __syncwarp();
     }
     nan = __any_sync(0xffffffffu, nan);
-    const double lowest = -__longlong_as_double(0x7ff0000000000000ll);
+    uint32_t taken = 0;  // bit i: expert lane + 32 i
     double top = 0.0;
     float mine = 0.f, sum = 0.f;  // lane j has the j-th choice
     int my_id = 0;
     for (int j = 0; j < p.top; ++j) {
-        double best = lowest;
+        uint64_t best = 0;
         int at = kMaxExperts;
         for (int e = lane, i = 0; e < p.experts; e += 32, ++i) {
             if (taken >> i & 1) continue;
-            double v = logits[e];
-            if (v != v) v = lowest;
-            if (v > best || (v == best && e < at)) {
-                best = v;
+            const uint64_t key = keys[e];
+            if (key > best || at == kMaxExperts) {
+                best = key;
                 at = e;
             }
         }
-#pragma unroll
-        for (int i = 16; i > 0; i >>= 1) {
-            const double v = __shfl_xor_sync(0xffffffffu, best, i);
-            const int e = __shfl_xor_sync(0xffffffffu, at, i);
-            if (v > best || (v == best && e < at)) {
-                best = v;
-                at = e;
-            }
-        }
+        const uint32_t high = static_cast<uint32_t>(best >> 32), low = static_cast<uint32_t>(best);
+        const uint32_t top_high = __reduce_max_sync(0xffffffffu, high);
+        const uint32_t top_low = __reduce_max_sync(0xffffffffu, high == top_high ? low : 0u);
+        at = __reduce_min_sync(0xffffffffu, high == top_high && low == top_low ? at : kMaxExperts);
         if ((at & 31) == lane) taken |= 1u << (at >> 5);
-        if (j == 0) top = best;
+        const double v = value_of(static_cast<uint64_t>(top_high) << 32 | top_low);
+        if (j == 0) top = v;
         if (lane == j) {
-            mine = expf(static_cast<float>(best - top));
+            mine = expf(static_cast<float>(v - top));
             my_id = at;
         }
     }
     if (p.renormalize) {
         sum = lane < p.top ? mine : 0.f;
     } else {
-        for (int e = lane; e < p.experts; e += 32) sum += expf(static_cast<float>(logits[e] - top));
+        for (int e = lane; e < p.experts; e += 32) sum += expf(static_cast<float>(value_of(keys[e]) - top));
     }
 #pragma unroll
     for (int i = 16; i > 0; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
@@ -287,6 +317,23 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
             else up_unit<4>(p, l, joined, e, row0, pair0, n);
         }
     }
+    // The second products' first steps to L2, so that the memory is not idle while this launch ends and the next
+    // one begins: a thread to a row of a warp's share, kAhead steps of it.
+    const int steps = (p.inner + kStep - 1) / kStep, blocks = (p.d + kRows - 1) / kRows * p.share;
+    for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
+        const int warp = threadIdx.x / kRows, row = block / p.share * kRows + threadIdx.x % kRows;
+        if (warp >= kWarps || row >= p.d) continue;
+        const Share mine = share_of(l.actives, steps, p.share, block % p.share, warp);
+        const int a = static_cast<int>(mine.at / steps), first = static_cast<int>(mine.at - static_cast<int64_t>(a) * steps);
+        if (mine.at >= mine.end) continue;
+        const int n = static_cast<int>(min(mine.end - mine.at, static_cast<int64_t>(kAhead)));
+        const int bytes = min(n * kStep, p.inner - first * kStep) / 8 * 16;
+        if (bytes > 0)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.w[2] + l.active[a] * p.expert[2] + row * p.ldw[2] +
+                                                                            first * kStep),
+                         "r"(bytes)
+                         : "memory");
+    }
 }
 
 // ---------------------------------------------------------------- the second products and the weighted sum
@@ -355,7 +402,7 @@ __device__ __forceinline__ void down_part(const Params& p, const Lists& l, const
 // A cluster to 16 columns of D: its warps share all the steps of all the chosen experts evenly, one after the
 // other, and their sums are joined in the same order on every run.
 // Dynamic shared memory: the warps' sums [warp][token][16].
-__global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p) {
     allow_next_kernel();
     wait_for_earlier_kernels();
     __shared__ Lists l;
@@ -364,12 +411,9 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     const int outputs = p.tokens * kRows;
     for (int i = threadIdx.x; i < kWarps * outputs; i += kThreads) sums[i] = 0.f;
     make_lists(l, p, pair_weight);
-    const int rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * kRows;
-    const int warp = threadIdx.x >> 5;
-    const int steps = (p.inner + kStep - 1) / kStep, shares = cluster * kWarps, share = rank * kWarps + warp;
-    const int64_t all = static_cast<int64_t>(l.actives) * steps;
-    int64_t at = all * share / shares;
-    const int64_t end = all * (share + 1) / shares;
+    const int cluster = p.share, rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * kRows;
+    const int warp = threadIdx.x >> 5, steps = (p.inner + kStep - 1) / kStep;
+    auto [at, end] = share_of(l.actives, steps, cluster, rank, warp);
     float* y = sums + warp * outputs;
     while (at < end) {
         const int a = static_cast<int>(at / steps), first = static_cast<int>(at - static_cast<int64_t>(a) * steps);

@@ -436,7 +436,7 @@ GB_API gb_status_t gb_moe_ffn_gated_workspace_bytes(int64_t T, int64_t I, int64_
  *   R      [M,N] (ldr) or NULL (0);  D [M,N] (ldd): any 2-byte aligned address and leading dimension (16-byte
  *          aligned rows move in 16-byte words); D == R (same pointer and leading dimension) is allowed, other
  *          overlaps are not
- *   workspace  device memory, 4-byte aligned, of at least gb_lora_workspace_bytes(); need not be cleared;
+ *   workspace  device memory, 16-byte aligned, of at least gb_lora_workspace_bytes(); need not be cleared;
  *          calls that overlap on the GPU need one each
  * X, A, B: bf16, base address 16-byte aligned, leading dimensions and distances of adapters multiples of 8
  * elements; M, N, K any number, r at most 256.  Products are bf16 with fp32 sums; A . X, scaled, is multiplied
@@ -448,7 +448,7 @@ GB_API gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t ld
                            void* D, int64_t ldd, void* workspace, size_t workspace_bytes, int64_t M, int64_t N, int64_t K,
                            int64_t r, int64_t adapters, void* stream);
 
-/* Workspace bytes of gb_lora on the current device. */
+/* Workspace bytes of gb_lora. */
 GB_API gb_status_t gb_lora_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t r, size_t* bytes);
 
 /*
