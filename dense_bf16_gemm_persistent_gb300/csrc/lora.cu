@@ -29,34 +29,48 @@ struct Plan {
     int64_t down_blocks, up_blocks;
 };
 
-// Tiles are as large as leaves a block to each SM's two places: rows of one adapter in a tile share its matrices'
-// loads.  X's columns are shared out to a cluster for the same, down to a step for each of its warps; D's to
-// blocks, down to 32 columns for each of their warps.
-Plan make_plan(int64_t M, int64_t N, int64_t K, int sms) {
-    Plan pl;
-    const int64_t slots = 2 * sms, steps = ceil_div(K, kStep);
-    int most = 1;
-    while (most < 8 && most * kWarps < steps) most *= 2;
-    pl.down_tile = kMaxTile;
-    while (pl.down_tile > 1 && ceil_div(M, pl.down_tile) * most < slots) pl.down_tile /= 2;
-    const int64_t down_tiles = ceil_div(M, pl.down_tile);
-    pl.cluster = 1;
-    while (pl.cluster < most && down_tiles * pl.cluster < slots) pl.cluster *= 2;
-    pl.down_blocks = down_tiles * pl.cluster;
-    const int64_t most_parts = ceil_div(N, kWarps * kColumns);
-    pl.up_tile = kMaxTile;
-    while (pl.up_tile > 1 && ceil_div(M, pl.up_tile) * most_parts < slots) pl.up_tile /= 2;
-    const int64_t up_tiles = ceil_div(M, pl.up_tile);
-    pl.parts = static_cast<int>(std::min(most_parts, std::max<int64_t>(1, slots / up_tiles)));
-    pl.up_blocks = up_tiles * pl.parts;
-    return pl;
-}
-
 int64_t low_columns(int64_t r) { return r <= 16 ? 16 : ceil_div(r, 32) * 32; }
 
 int64_t workspace_of(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
 
-size_t down_smem(int teams, int tiles) { return static_cast<size_t>(kWarps + 2 * teams) * tiles * 4 * 128 * 4; }
+// The product down to the rank: X's columns are shared out to a cluster, down to a step for each of its warps, and the
+// rows so that all blocks run at once (two an SM), with as many rows as a turn takes at most.  The product up to D:
+// tiles of 64 rows, fewer where these and all columns' warps are not enough for the SMs; a block of columns a warp, or
+// two where that is twice as many blocks as run at once.  (Small tiles cost more than few blocks of them: 1000 rows of
+// 4099 columns in 16 tiles of 64 took 15 us, in 63 of 16 rows, which two adapters meet in more often, 24.  8192 x 4096
+// with two blocks of columns a warp 34 us, with as many as all run at once 36, since those are not done together.)  Less
+// than 64 rows are requests of a token or a few, with adapters of their own as a rule: a tile each, and the blocks that
+// run at once (48 rows of 14336 columns, rank 64: 20 us; in tiles of 8 rows 24).
+Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t ld, int sms, bool shift) {
+    Plan pl;
+    const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), rows = turn_rows(r <= 16 ? 1 : 2);
+    pl.cluster = 1;
+    while (pl.cluster < 8 && pl.cluster * kWarps < steps) pl.cluster *= 2;
+    while (pl.cluster > 1 && ceil_div(M, slots / pl.cluster) > rows) pl.cluster /= 2;
+    pl.down_tile = static_cast<int>(std::min(rows, ceil_div(M, slots / pl.cluster)));
+    pl.down_blocks = ceil_div(M, pl.down_tile) * pl.cluster;
+    const int64_t turns = ceil_div(N, kWarps * kColumns), pairs = ceil_div(turns, 2);
+    const int64_t places = (shift || low_columns(r) > 32 ? 2 : 3) * sms;
+    pl.up_tile = kMaxTile;
+    while (pl.up_tile > 1 && ceil_div(M, pl.up_tile) * turns * 5 < places * 4) pl.up_tile /= 2;
+    while (pl.up_tile > 1 && pl.up_tile * ld > kMaxDim) pl.up_tile /= 2;  // (the kernel's distances within a tile)
+    if (M < kMaxTile) pl.up_tile = 1;
+    const int64_t up_tiles = ceil_div(M, pl.up_tile);
+    pl.parts = static_cast<int>(up_tiles * pairs >= 2 * places ? pairs : turns);
+    if (M < kMaxTile) pl.parts = static_cast<int>(ceil_div(turns, ceil_div(turns, std::max<int64_t>(1, places / M))));
+    pl.up_blocks = up_tiles * pl.parts;
+    return pl;
+}
+
+size_t down_smem(int teams) { return static_cast<size_t>(kWarps + 2 * teams) * kSums * 4; }
+
+using UpKernel = void (*)(Params);
+
+template <bool SHIFT>
+UpKernel up_kernel_for(int ldlow) {
+    return ldlow <= 16 ? up_kernel<16, 1, SHIFT> : ldlow == 32 ? up_kernel<32, 1, SHIFT> : ldlow == 64 ? up_kernel<32, 2, SHIFT>
+                                                                                          : up_kernel<32, 0, SHIFT>;
+}
 
 }  // namespace
 
@@ -112,7 +126,9 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     int dev = 0;
     DeviceInfo info;
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
-    const Plan pl = make_plan(M, N, K, info.sms);
+    const bool wide_r = aligned_to(R, 16) && (M == 1 || ldr % 8 == 0), wide_d = aligned_to(D, 16) && (M == 1 || ldd % 8 == 0);
+    const bool shift = !(wide_d && (wide_r || !R));  // rows start anywhere
+    const Plan pl = make_plan(M, N, K, r, std::max(ldd, R ? ldr : 0), info.sms, shift);
     if (pl.down_blocks > kMaxDim || pl.up_blocks > kMaxDim)
         return fail(GB_ERR_UNSUPPORTED, "%" PRId64 " rows of %" PRId64 " columns are more than a launch's blocks", M, N);
     const size_t need = any ? static_cast<size_t>(workspace_of(M, r)) : 0;
@@ -145,28 +161,29 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     prm.act = act;
     prm.cluster = pl.cluster;
     prm.parts = pl.parts;
-    prm.wide_r = aligned_to(R, 16) && (M == 1 || ldr % 8 == 0);
-    prm.wide_d = aligned_to(D, 16) && (M == 1 || ldd % 8 == 0);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (any) {
         const int tiles = r <= 16 ? 1 : 2;
         prm.teams = 1;
         while (prm.teams < kWarps && prm.teams * 16 * tiles < r) prm.teams *= 2;
         prm.tile = pl.down_tile;
-        static std::atomic<bool> ready[64];
-        if ((st = allow_smem(down_kernel<2>, ready, dev, down_smem(kWarps, 2))) != GB_OK) return st;
-        st = Launch(static_cast<unsigned>(pl.down_blocks), kThreads, down_smem(prm.teams, tiles), s, pl.cluster)(
-            "lora down launch", tiles == 1 ? down_kernel<1> : down_kernel<2>, prm);
+        static std::atomic<bool> ready[2][64];
+        const auto kernel = tiles == 1 ? down_kernel<1> : down_kernel<2>;
+        if ((st = allow_smem(kernel, ready[tiles - 1], dev, down_smem(tiles == 1 ? 1 : kWarps))) != GB_OK) return st;
+        st = Launch(static_cast<unsigned>(pl.down_blocks), kThreads, down_smem(prm.teams), s, pl.cluster)(
+            "lora down launch", kernel, prm);
         if (st != GB_OK) return st;
     }
     prm.tile = pl.up_tile;
-    note_plan("kernel=lora down_tile=%lld cluster=%lld down_blocks=%lld up_tile=%lld up_blocks=%lld wide=%lld", pl.down_tile,
-              pl.cluster, any ? pl.down_blocks : 0, pl.up_tile, pl.up_blocks, prm.wide_d);
-    const size_t smem = static_cast<size_t>(2) * pl.up_tile * low_words(prm.ldlow) * 4;
-    static std::atomic<bool> ready[64];
-    if ((st = allow_smem(up_kernel<32>, ready, dev, 2 * kMaxTile * low_words(kMaxRank) * 4)) != GB_OK) return st;
-    return Launch(static_cast<unsigned>(pl.up_blocks), kThreads, smem, s)(
-        "lora up launch", prm.ldlow <= 16 ? up_kernel<16> : up_kernel<32>, prm);
+    note_plan("kernel=lora down_tile=%lld cluster=%lld down_blocks=%lld up_tile=%lld up_blocks=%lld shifted=%lld", pl.down_tile,
+              pl.cluster, any ? pl.down_blocks : 0, pl.up_tile, pl.up_blocks, shift);
+    const UpKernel kernel = shift ? up_kernel_for<true>(prm.ldlow) : up_kernel_for<false>(prm.ldlow);
+    if (prm.ldlow > 64) {  // (less is within what any kernel may have)
+        static std::atomic<bool> ready[2][64];
+        if ((st = allow_smem(kernel, ready[shift], dev, kMaxTile * low_words(kMaxRank) * 4)) != GB_OK) return st;
+    }
+    const size_t smem = static_cast<size_t>(pl.up_tile) * low_words(prm.ldlow) * 4;
+    return Launch(static_cast<unsigned>(pl.up_blocks), kThreads, smem, s)("lora up launch", kernel, prm);
 }
 
 }  // extern "C"

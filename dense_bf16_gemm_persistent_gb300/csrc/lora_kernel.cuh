@@ -8,6 +8,8 @@
 // X, R and D once, and the adapters' matrices.
 #pragma once
 
+#include <type_traits>
+
 #include "skinny.cuh"
 
 namespace gb {
@@ -28,7 +30,7 @@ struct Params {
     const float* scale;      // or null: 1
     const uint16_t* r;       // or null
     uint16_t* d;
-    uint16_t* low;           // [m][2][ldlow]: scale X A^T as the sum of two bf16
+    uint16_t* low;           // [m][2 ldlow]: scale X A^T as the sum of two bf16 terms, placed as term_at() says
     int64_t ldx, lda, ldb, ldr, ldd;
     int64_t apart_a, apart_b;  // elements between adapters
     int m, n, k, rank, adapters;
@@ -38,21 +40,31 @@ struct Params {
     int tile;                // rows of a tile (of the launch at hand)
     int parts;               // CTAs of a tile that share the columns of D
     int teams;               // of a CTA's warps: 16 or 32 ranks each
-    int wide_r, wide_d;      // rows start on 16 bytes
 };
+
+// Where the terms of rank j of a row of S are, of RS ranks a step of the product up to D (16, or 32 beyond 16 ranks):
+// a lane's quarter of a step lies together, first terms and second terms.
+template <int RS>
+__device__ __forceinline__ int term_at(int j, int term) {
+    return j / RS * 2 * RS + j % RS / (RS / 4) * (RS / 2) + term * (RS / 4) + j % (RS / 4);
+}
 
 // ---------------------------------------------------------------- a tile's rows by adapter
 
+// Units of up to UNIT rows of one adapter.
 struct Order {
-    int id[kMaxTile];          // as given; then in order
+    int id[kMaxTile];          // in order
     int row[kMaxTile];         // in order: rows of one adapter together, those without one last
-    int start[kMaxTile + 1];   // the groups' first places
-    int groups;
+    int start[kMaxTile + 1];   // the units' first places
+    int units;
+    __device__ __forceinline__ int adapter(int unit) const { return id[start[unit]]; }  // -1: none
 };
 
-// By all threads of a block; a row without an adapter has id -1 afterwards.
+// By all threads of a block.
+template <int UNIT>
 __device__ __forceinline__ void make_order(Order& o, const Params& p, int64_t row0, int rows) {
     __shared__ int given[kMaxTile];
+    __shared__ bool begins[kMaxTile];  // (in order) a unit
     const int t = threadIdx.x;
     int key = p.adapters, first = p.adapters;  // (without one: after all others)
     if (t < rows) {
@@ -61,39 +73,41 @@ __device__ __forceinline__ void make_order(Order& o, const Params& p, int64_t ro
         if (id0 >= 0 && id0 < p.adapters) first = id0;
         given[t] = key;
     }
-    if (__syncthreads_and(key == first || t >= rows)) {  // (a prompt's rows: one group)
+    if (__syncthreads_and(key == first || t >= rows)) {  // (a prompt's rows: one adapter)
+        const int units = (rows + UNIT - 1) / UNIT;
         if (t < rows) {
             o.row[t] = t;
             o.id[t] = key < p.adapters ? key : -1;
         }
-        if (t == 0) {
-            o.start[0] = 0;
-            o.start[1] = rows;
-            o.groups = 1;
-        }
+        if (t <= units) o.start[t] = min(t * UNIT, rows);
+        if (t == 0) o.units = units;
         __syncthreads();
         return;
     }
     if (t < rows) {
-        int at = 0;
+        int less = 0, same = 0;
 #pragma unroll 8
-        for (int i = 0; i < rows; ++i) at += given[i] < key || (given[i] == key && i < t);
-        o.row[at] = t;
-        o.id[at] = key < p.adapters ? key : -1;
+        for (int i = 0; i < rows; ++i) {
+            less += given[i] < key;
+            same += given[i] == key && i < t;
+        }
+        o.row[less + same] = t;
+        o.id[less + same] = key < p.adapters ? key : -1;
+        begins[less + same] = same % UNIT == 0;
     }
     __syncthreads();
     if (t < 32) {
-        int groups = 0;
+        int units = 0;
         for (int base = 0; base < rows; base += 32) {
             const int i = base + t;
-            const bool begins = i < rows && (i == 0 || o.id[i] != o.id[i - 1]);
-            const uint32_t on = __ballot_sync(0xffffffffu, begins);
-            if (begins) o.start[groups + __popc(on & ((1u << t) - 1))] = i;
-            groups += __popc(on);
+            const bool one = i < rows && begins[i];
+            const uint32_t on = __ballot_sync(0xffffffffu, one);
+            if (one) o.start[units + __popc(on & ((1u << t) - 1))] = i;
+            units += __popc(on);
         }
         if (t == 0) {
-            o.start[groups] = rows;
-            o.groups = groups;
+            o.start[units] = rows;
+            o.units = units;
         }
     }
     __syncthreads();
@@ -101,71 +115,100 @@ __device__ __forceinline__ void make_order(Order& o, const Params& p, int64_t ro
 
 // ---------------------------------------------------------------- down to the rank
 
-// 16 MT ranks of one adapter with up to 8 NT rows of X, over the steps first, first + by, ... before last.
-template <int MT, int NT>
-__device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p, const Order& o, int64_t row0, int adapter,
-                                          int rank0, int place, int rows, int first, int by, int last) {
-    constexpr int kUnroll = 2 * MT + NT <= 4 ? 4 : 2;
+// 16 MT ranks with NT units of rows, over the steps first, first + by, ...  ADAPTERS: how many the units have at most
+// (they are in order; NT: each has its own), whose fragments the units of one share.
+//
+// Loads go straight to the fragments.  Each row's 64 bytes come from one warp, 512 contiguous bytes from the block's
+// eight, and two blocks an SM have 70 to 80 KB on their way: 64 rows of 4096 columns a block and a cluster of two
+// stream at 7.4 TB/s (8192 rows of 67 MB).  A ring of steps in shared memory, filled by cp.async, streamed at 4.8.
+template <int MT, int NT, int ADAPTERS>
+__device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p, const Order& o, int64_t row0, int rank0,
+                                          int unit0, int units, int first, int by) {
+    constexpr int kOf = 2 * MT * ADAPTERS + NT, kUnroll = kOf <= 4 ? 4 : kOf <= 8 ? 2 : 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    // (ranks beyond the last are the last's, rows the first's: their sums are not used)
-    const uint16_t* a[2 * MT];
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) a[i] = p.a + adapter * p.apart_a + min(rank0 + g + 8 * i, p.rank - 1) * p.lda;
+    // (ranks beyond the last are the last's, rows the unit's first's, units the last's: their sums are not used)
+    const uint16_t* a[ADAPTERS][2 * MT];
     const uint16_t* x[NT];
+    int cut = NT;  // of two adapters: the second's first unit
 #pragma unroll
-    for (int t = 0; t < NT; ++t) x[t] = p.x + (row0 + o.row[place + (8 * t + g < rows ? 8 * t + g : 0)]) * p.ldx;
+    for (int t = 0; t < NT; ++t) {
+        const int unit = unit0 + min(t, units - 1), place = o.start[unit] + g;
+        x[t] = p.x + (row0 + o.row[place < o.start[unit + 1] ? place : place - g]) * p.ldx + 8 * q;
+        if (ADAPTERS == 2 && o.adapter(unit) != o.adapter(unit0)) cut = min(cut, t);
+    }
+#pragma unroll
+    for (int t = 0; t < ADAPTERS; ++t) {
+        const int unit = unit0 + min(ADAPTERS == 2 && t ? cut : t, units - 1);
+#pragma unroll
+        for (int i = 0; i < 2 * MT; ++i)
+            a[t][i] = p.a + o.adapter(unit) * p.apart_a + min(rank0 + g + 8 * i, p.rank - 1) * p.lda + 8 * q;
+    }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[m][t][i] = 0.f;
-    const int whole = min(last, p.k / kStep);
-    int s = first;
-    for (; s + (kUnroll - 1) * by < whole; s += kUnroll * by) {
-        uint4 u[kUnroll][2 * MT], v[kUnroll][NT];
+    auto add = [&](const uint4 (&u)[ADAPTERS][2 * MT], const uint4 (&v)[NT]) {
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-            const int col = (s + j * by) * kStep + 8 * q;
+        for (int t = 0; t < NT; ++t) {
+            if constexpr (ADAPTERS == 2) {
+                const bool later = t >= cut;
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) u[j][i] = *reinterpret_cast<const uint4*>(a[i] + col);
+                for (int m = 0; m < MT; ++m) {
+                    if (later) mma_step(c[m][t], u[1][2 * m], u[1][2 * m + 1], v[t]);
+                    else mma_step(c[m][t], u[0][2 * m], u[0][2 * m + 1], v[t]);
+                }
+            } else {
+                constexpr bool kOwn = ADAPTERS == NT;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) v[j][t] = *reinterpret_cast<const uint4*>(x[t] + col);
+                for (int m = 0; m < MT; ++m) mma_step(c[m][t], u[kOwn ? t : 0][2 * m], u[kOwn ? t : 0][2 * m + 1], v[t]);
+            }
+        }
+    };
+    const int whole = p.k / kStep;
+    for (int s = first; s < whole; s += kUnroll * by) {
+        uint4 u[kUnroll][ADAPTERS][2 * MT], v[kUnroll][NT];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) {  // (all loads at once; beyond the last step, it again)
+            const int col = min(s + j * by, whole - 1) * kStep;
+#pragma unroll
+            for (int t = 0; t < ADAPTERS; ++t)
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) u[j][t][i] = *reinterpret_cast<const uint4*>(a[t][i] + col);
+#pragma unroll
+            for (int t = 0; t < NT; ++t)   // (up to 16 ranks X is read by one warp only)
+                v[j][t] = MT == 1 ? load_once(x[t] + col) : *reinterpret_cast<const uint4*>(x[t] + col);
         }
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j)
-#pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) mma_step(c[m][t], u[j][2 * m], u[j][2 * m + 1], v[j][t]);
+            if (s + j * by < whole) add(u[j], v[j]);
     }
-    for (; s < last; s += by) {
-        const int col = s * kStep + 8 * q;
-        uint4 u[2 * MT];
+    if (whole * kStep < p.k && first == 0) {
+        const int col = whole * kStep, left = p.k - 8 * q;
+        uint4 u[ADAPTERS][2 * MT], v[NT];
 #pragma unroll
-        for (int i = 0; i < 2 * MT; ++i) u[i] = load_edge(a[i], col, p.k);
+        for (int t = 0; t < ADAPTERS; ++t)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const uint4 v = load_edge(x[t], col, p.k);
+            for (int i = 0; i < 2 * MT; ++i) u[t][i] = load_edge(a[t][i], col, left);
 #pragma unroll
-            for (int m = 0; m < MT; ++m) mma_step(c[m][t], u[2 * m], u[2 * m + 1], v);
-        }
+        for (int t = 0; t < NT; ++t) v[t] = load_edge(x[t], col, left);
+        add(u, v);
     }
 }
 
-// A group's rows place .. place + rows - 1 (up to 8 NT).  The cluster's CTAs share the columns, and in each CTA a
-// team of warps 16 MT ranks and, again, the columns; the sums are joined over the warps, then over the CTAs, in
-// the same order on every run.  `joined`: the warps' sums; `mine`: the CTA's, one of two places in turn, so
-// that a turn has one barrier of the cluster.
-template <int MT, int NT>
-__device__ __forceinline__ void down_part(const Params& p, const Order& o, float* joined, float* mine, int64_t row0, int rank,
-                                          int adapter, int place, int rows) {
+// A turn: `units` units of rows (up to NT).  The cluster's CTAs share the columns, and in each CTA a team of warps
+// 16 MT ranks and, again, the columns; the sums are joined over the warps, then over the CTAs, in the same order on
+// every run.  `joined`: the warps' sums; `mine`: the CTA's, one of two places in turn, so that a turn has one barrier
+// of the cluster.
+template <int MT, int NT, int ADAPTERS>
+__device__ __forceinline__ void down_turn(const Params& p, const Order& o, float* joined, float* mine, int64_t row0, int rank,
+                                          int unit0, int units) {
     constexpr int kOf = MT * NT * 128;  // sums of a warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sharing = kWarps / p.teams, team = warp / sharing, part = warp % sharing;
-    const int by = p.cluster * sharing, last = (p.k + kStep - 1) / kStep;
     float c[MT][NT][4];
-    down_sums<MT, NT>(c, p, o, row0, adapter, team * 16 * MT, place, rows, rank * sharing + part, by, last);
+    down_sums<MT, NT, ADAPTERS>(c, p, o, row0, team * 16 * MT, unit0, units, rank * sharing + part, p.cluster * sharing);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -180,78 +223,94 @@ __device__ __forceinline__ void down_part(const Params& p, const Order& o, float
         mine[at] = v;
     }
     cluster_sync();
-    const float scale = p.scale ? p.scale[adapter] : 1.f;
     for (int at = rank * kThreads + threadIdx.x; at < p.teams * kOf; at += p.cluster * kThreads) {
+        const int its = at / kOf, in = at % kOf;
+        const int from = in & 31, i = in >> 5 & 3, t = (in >> 7) % NT, m = (in >> 7) / NT;
+        const int j = (its * MT + m) * 16 + (from >> 2) + 8 * (i >> 1);
+        if (t >= units || j >= p.ldlow) continue;
+        const int place = o.start[unit0 + t] + 2 * (from & 3) + (i & 1);
+        if (place >= o.start[unit0 + t + 1]) continue;
         float v = 0.f;
         for (int k = 0; k < p.cluster; ++k) {
             float other;
             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(other) : "r"(mapa_shared(smem_addr(mine + at), k)) : "memory");
             v += other;
         }
-        const int its = at / kOf, in = at % kOf;
-        const int from = in & 31, i = in >> 5 & 3, t = (in >> 7) % NT, m = (in >> 7) / NT;
-        const int j = (its * MT + m) * 16 + (from >> 2) + 8 * (i >> 1), row = 8 * t + 2 * (from & 3) + (i & 1);
-        if (j < p.ldlow && row < rows) {
-            uint16_t* to = p.low + (row0 + o.row[place + row]) * 2 * p.ldlow + j;
-            split(j < p.rank ? v * scale : 0.f, to[0], to[p.ldlow]);
-        }
+        uint16_t* to = p.low + (row0 + o.row[place]) * 2 * p.ldlow;
+        constexpr int kStepRanks = MT == 1 ? 16 : 32;
+        split(j < p.rank ? v * (p.scale ? p.scale[o.id[place]] : 1.f) : 0.f, to[term_at<kStepRanks>(j, 0)],
+              to[term_at<kStepRanks>(j, 1)]);
     }
 }
 
-// Dynamic shared memory: the warps' sums, and two of the CTA's.
+// Units a turn takes (rows of one adapter, or of two; of more, half of them at most), and rows a tile has so that the
+// rows of two adapters make no more units than that: where one request ends in a tile, that tile would else take
+// another turn, and the launch waits for it (8192 rows of 12 requests: 27 us instead of 20).
+__host__ __device__ constexpr int turn_units(int mt) { return mt == 1 ? 8 : 4; }
+__host__ __device__ constexpr int turn_rows(int mt) { return 8 * (turn_units(mt) - 1); }
+constexpr int kSums = 8 * 128;  // of a warp in a turn, at most
+
+// Dynamic shared memory: the warps' sums, and two places for the CTA's.
 template <int MT>
 __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p) {
     allow_next_kernel();
     wait_for_earlier_kernels();
     __shared__ Order o;
-    extern __shared__ float sums[];
+    extern __shared__ __align__(16) float sums[];
     const int rank = blockIdx.x % p.cluster;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.cluster) * p.tile;
-    make_order(o, p, row0, static_cast<int>(min(static_cast<int64_t>(p.tile), p.m - row0)));
-    constexpr int kMost = MT * 4 * 128;
-    int turn = 0;
-    for (int i = 0; i < o.groups; ++i) {
-        const int adapter = o.id[o.start[i]];
-        if (adapter < 0) break;  // (the last group)
-        for (int place = o.start[i]; place < o.start[i + 1]; place += 32, turn ^= 1) {
-            const int rows = min(o.start[i + 1] - place, 32);
-            float* mine = sums + (kWarps + turn * p.teams) * kMost;
-            if (rows <= 8) down_part<MT, 1>(p, o, sums, mine, row0, rank, adapter, place, rows);
-            else if (rows <= 16) down_part<MT, 2>(p, o, sums, mine, row0, rank, adapter, place, rows);
-            else down_part<MT, 4>(p, o, sums, mine, row0, rank, adapter, place, rows);
+    make_order<8>(o, p, row0, static_cast<int>(min(static_cast<int64_t>(p.tile), p.m - row0)));
+    constexpr int kMost = turn_units(MT);
+    int units = 0;  // with an adapter
+    while (units < o.units && o.adapter(units) >= 0) ++units;
+    for (int unit = 0, turn = 0; unit < units; turn ^= 1) {
+        int n = 0, two = 0;  // units of one adapter, and of two
+        for (int i = unit, changes = 0; i < min(units, unit + kMost); ++i) {
+            changes += i > unit && o.adapter(i) != o.adapter(i - 1);
+            n += changes == 0;
+            two += changes <= 1;
         }
+        float* mine = sums + (kWarps + turn * p.teams) * kSums;
+        const int left = min(units - unit, kMost);
+        if (n < left && two == left) {  // (all that a turn can have)
+            n = two;
+            if (n <= 2) down_turn<MT, 2, 2>(p, o, sums, mine, row0, rank, unit, n);
+            else down_turn<MT, kMost, 2>(p, o, sums, mine, row0, rank, unit, n);
+        } else if (n < min(left, kMost / 2)) {
+            n = min(left, kMost / 2);
+            if (n <= 2) down_turn<MT, 2, 2>(p, o, sums, mine, row0, rank, unit, n);
+            else if constexpr (MT == 1) down_turn<MT, kMost / 2, kMost / 2>(p, o, sums, mine, row0, rank, unit, n);
+        } else if (n == 1) {
+            down_turn<MT, 1, 1>(p, o, sums, mine, row0, rank, unit, n);
+        } else if (n == 2) {
+            down_turn<MT, 2, 1>(p, o, sums, mine, row0, rank, unit, n);
+        } else if (MT == 2 || n <= 4) {
+            down_turn<MT, 4, 1>(p, o, sums, mine, row0, rank, unit, n);
+        } else if constexpr (MT == 1) {
+            down_turn<MT, 8, 1>(p, o, sums, mine, row0, rank, unit, n);
+        }
+        unit += n;
     }
     cluster_sync();  // (the others may still read this CTA's sums)
 }
 
 // ---------------------------------------------------------------- up to D
 
-// Words of a row of one of S's terms in shared memory, so that the rows of a fragment's loads are in different banks:
-// an odd multiple of 8 for 8-byte loads (eight rows of 8 words), of 16 for 16-byte ones.
-__host__ __device__ constexpr int low_words(int ldlow) {
-    const int unit = ldlow <= 16 ? 8 : 16, words = ldlow / 2;
-    return words / unit % 2 ? words : words + unit;
-}
+// Words of a row of S in shared memory: the rows of a fragment's 16-byte loads are in different banks.
+__host__ __device__ constexpr int low_words(int ldlow) { return ldlow <= 16 ? 16 : ldlow + 4; }
 
-// S's fragment words and B's: RS / 4 elements of a row at `col` (zeros from `cols` on).
+// A lane's words of a step of a row of B: RS / 4 elements.
 template <int RS>
 struct __align__(RS / 2) Words {
     uint32_t w[RS / 8];
 };
 
-template <int RS>
+// Those at `col` (zeros from `cols` on).  WHOLE: there are always so many (a load that may branch waits for the one
+// before).
+template <int RS, bool WHOLE>
 __device__ __forceinline__ Words<RS> load_words(const uint16_t* row, int col, int cols) {
+    if (WHOLE || col + RS / 4 <= cols) return *reinterpret_cast<const Words<RS>*>(row + col);
     Words<RS> v;
-    if (col + RS / 4 <= cols) {
-        if constexpr (RS == 16) {
-            const uint2 u = *reinterpret_cast<const uint2*>(row + col);
-            v.w[0] = u.x, v.w[1] = u.y;
-        } else {
-            const uint4 u = *reinterpret_cast<const uint4*>(row + col);
-            v.w[0] = u.x, v.w[1] = u.y, v.w[2] = u.z, v.w[3] = u.w;
-        }
-        return v;
-    }
 #pragma unroll
     for (int i = 0; i < RS / 8; ++i) {
         v.w[i] = col + 2 * i < cols ? row[col + 2 * i] : 0u;
@@ -260,116 +319,248 @@ __device__ __forceinline__ Words<RS> load_words(const uint16_t* row, int col, in
     return v;
 }
 
-__device__ __forceinline__ uint4 load_row8(const uint16_t* row, int col, int cols, bool wide) {
-    if (wide && col + 8 <= cols) return *reinterpret_cast<const uint4*>(row + col);
-    uint32_t e[8];
+// Eight elements of two neighbouring 16-byte words, from the element `by` (0 .. 8) on.
+__device__ __forceinline__ uint4 window(const uint4& a, const uint4& b, int by) {
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (by & 4) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = col + i < cols ? row[col + i] : 0u;
-    return make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (by & 2) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (by & 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return by & 8 ? b : make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ void store_row8(uint16_t* row, int col, int cols, bool wide, const float (&v)[8]) {
-    if (wide && col + 8 <= cols) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = bf16_bits(v[2 * i]) | static_cast<uint32_t>(bf16_bits(v[2 * i + 1])) << 16;
-        *reinterpret_cast<uint4*>(row + col) = make_uint4(w[0], w[1], w[2], w[3]);
-        return;
-    }
+// Elements between the 16-byte boundary below p and p.
+__device__ __forceinline__ int shift_of(const uint16_t* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7; }
+
+// A lane's columns where a block is cut off: the first `columns` of eight.  (Few blocks: their code is kept small.)
+__device__ __noinline__ uint4 load_cut(const uint16_t* at, int columns) {
+    uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        if (col + i < cols) row[col + i] = bf16_bits(v[i]);
+        if (i < columns) w[i >> 1] |= static_cast<uint32_t>(at[i]) << (i & 1) * 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
+__device__ __noinline__ void store_cut(uint16_t* at, uint4 v, int columns) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < columns) at[i] = static_cast<uint16_t>(w[i >> 1] >> (i & 1) * 16);
+}
+
+// A lane's eight columns of 32 in a row (8q .. 8q + 7, at `at`), on their way.  SHIFT: rows start anywhere; the two
+// 16-byte words are loaded that hold them.
+template <bool SHIFT>
+struct Row8 {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const uint16_t* at) {
+        const uint16_t* from = SHIFT ? at - shift_of(at) : at;
+        a = SHIFT ? *reinterpret_cast<const uint4*>(from) : load_once(from);
+        if (SHIFT) b = *reinterpret_cast<const uint4*>(shift_of(at) ? from + 8 : from);
+    }
+    __device__ __forceinline__ uint4 get(const uint16_t* at, bool edge) const {
+        return SHIFT && !edge ? window(a, b, shift_of(at)) : a;
+    }
+};
+
+// A lane's eight columns of 32 in a row (8q .. 8q + 7, at `at`) written.  With rows that start anywhere a lane writes the 16-byte word that ends in its
+// columns, with its neighbour's; the four lanes' first and last words are parts, in pieces of 8, 4 and 2 bytes.
+// By all lanes of a warp; `on`: the lane's row is written.
+template <bool SHIFT>
+__device__ __forceinline__ void store_row8(uint16_t* at, const uint4& v, int q, bool on) {
+    if (!SHIFT) {
+        if (on) *reinterpret_cast<uint4*>(at) = v;
+        return;
+    }
+    const uint4 before = make_uint4(__shfl_up_sync(0xffffffffu, v.x, 1), __shfl_up_sync(0xffffffffu, v.y, 1),
+                                    __shfl_up_sync(0xffffffffu, v.z, 1), __shfl_up_sync(0xffffffffu, v.w, 1));
+    if (!on) return;
+    const int s = shift_of(at);
+    const uint4 word = window(before, v, 8 - s);
+    uint16_t* to = at - s;
+    if (q > 0 || s == 0) {
+        *reinterpret_cast<uint4*>(to) = word;
+    } else {
+        const int even = s + (s & 1);  // (elements s .. 7)
+        if (s & 1) to[s] = static_cast<uint16_t>((s == 1 ? word.x : s == 3 ? word.y : s == 5 ? word.z : word.w) >> 16);
+        if (even & 2) *reinterpret_cast<uint32_t*>(to + even) = even == 2 ? word.y : word.w;
+        if (even <= 4) *reinterpret_cast<uint2*>(to + 4) = make_uint2(word.z, word.w);
+    }
+    if (q == 3 && s) {
+        const uint4 rest = window(v, v, 8 - s);  // (elements 0 .. s - 1)
+        uint16_t* end = to + 8;
+        if (s & 4) *reinterpret_cast<uint2*>(end) = make_uint2(rest.x, rest.y);
+        if (s & 2) *reinterpret_cast<uint32_t*>(end + (s & 4)) = s & 4 ? rest.z : rest.x;
+        if (s & 1) end[s & 6] = static_cast<uint16_t>(s == 1 ? rest.x : s == 3 ? rest.y : s == 5 ? rest.z : rest.w);
+    }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+
+// A row of a unit, as the loop over columns wants it: what lies between the tile's first row and this one, in elements
+// (the host keeps a tile's rows within 32 bits), and its place of S.
+struct __align__(16) RowAt {
+    uint32_t r, d, low;
+    int on;  // else beyond the unit's last row, which stands in its place
+};
 
 // A CTA: a tile of rows, and a part of D's columns in blocks of 32, a warp each.  The mma's columns are taken in an
 // order in which a lane's sums are 8 neighbouring columns of a row: of a block's four mma tiles, column i of tile j
-// is number 8 (i / 2) + 2 j + i % 2.  Rows are taken 32 at a time (two mma tiles), their R on its way together.
-// Dynamic shared memory: S's first terms [row in order][low_words], then its second ones.
-template <int RS>
-__global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__ Params p) {
+// is number 8 (i / 2) + 2 j + i % 2.  Of a block a warp takes two units (16 rows) of one adapter at a time: their R,
+// and B, are asked for at once, and B's fragments serve both.  All that a row needs comes from shared memory in one
+// load, since the blocks are short.
+// RS: ranks of a step (of a lane's loads of 8 or 16 bytes); STEPS: steps of B in registers (0: the rank has more than
+// two, and B is read step by step, after the first unit from L1).
+// Dynamic shared memory: S [row in order][low_words].
+//
+// 8192 x 4096 of rank 16 (134 MB) takes 36 us, 3.7 TB/s.  While all SMs are full it moves 5 TB/s; the rest is the start
+// (1.5 us until a block knows its rows' order and has S), and blocks that are not done together.  Left out for a
+// measurement, the mma, S's loads and B's took 8 % together, R's 40 %, D's 25 %.  Four units at a time in twice the
+// registers took as long, and so did R and B fetched four turns ahead to a ring in shared memory.
+template <int RS, int STEPS, bool SHIFT>
+__global__ void __launch_bounds__(kThreads, STEPS == 1 && !SHIFT ? 3 : 2) up_kernel(const __grid_constant__ Params p) {
+    constexpr int kBatch = 2;
     allow_next_kernel();
     wait_for_earlier_kernels();
     __shared__ Order o;
+    __shared__ RowAt rows_at[kMaxTile * 16];
     extern __shared__ __align__(16) uint32_t low[];
     const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.parts) * p.tile;
     const int rows = static_cast<int>(min(static_cast<int64_t>(p.tile), p.m - row0));
-    make_order(o, p, row0, rows);
-    const int words = low_words(p.ldlow), second = p.tile * words, chunks = p.ldlow / 8;
-    for (int i = threadIdx.x; i < rows * 2 * chunks; i += kThreads) {
-        const int place = i / (2 * chunks), j = i - place * 2 * chunks, term = j >= chunks;
-        if (o.id[place] < 0) continue;
-        *reinterpret_cast<uint4*>(low + term * second + place * words + 4 * (j - term * chunks)) =
-            *reinterpret_cast<const uint4*>(p.low + ((row0 + o.row[place]) * 2 + term) * p.ldlow + 8 * (j - term * chunks));
+    make_order<16>(o, p, row0, rows);
+    const int words = low_words(p.ldlow), chunks = p.ldlow / 4, units = o.units;
+    for (int i = threadIdx.x; i < units * 16; i += kThreads) {
+        const int end = o.start[i / 16 + 1], place = o.start[i / 16] + i % 16, at = min(place, end - 1);
+        rows_at[i] = {o.row[at] * static_cast<uint32_t>(p.ldr), o.row[at] * static_cast<uint32_t>(p.ldd),
+                      static_cast<uint32_t>(at * words), place < end};
+    }
+    for (int i = threadIdx.x; i < rows * chunks; i += kThreads) {
+        const int place = i / chunks, j = i - place * chunks;
+        if (o.id[place] >= 0)
+            *reinterpret_cast<uint4*>(low + place * words + 4 * j) =
+                *reinterpret_cast<const uint4*>(p.low + (row0 + o.row[place]) * 2 * p.ldlow + 8 * j);
     }
     __syncthreads();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+    const bool whole = p.rank == p.ldlow;
     const int64_t step = static_cast<int64_t>(p.parts) * kWarps * kColumns;
+    const uint16_t* r_tile = p.r + row0 * p.ldr;
+    uint16_t* d_tile = p.d + row0 * p.ldd;
     for (int64_t at64 = (static_cast<int64_t>(blockIdx.x % p.parts) * kWarps + warp) * kColumns; at64 < p.n; at64 += step) {
         const int col0 = static_cast<int>(at64), col = col0 + 8 * q;
-        for (int i = 0; i < o.groups; ++i) {
-            const int adapter = o.id[o.start[i]], end = o.start[i + 1];
-            const uint16_t* b[4];
+        // Element by element: a block that is cut off, and, since rows that start anywhere are read in whole 16-byte
+        // words, where those may begin before the matrix or end after it.
+        const bool edge = col0 + kColumns > p.n ||
+                          (SHIFT && ((col0 == 0 && row0 == 0) || (col0 + kColumns + 8 > p.n && row0 + rows == p.m)));
+        int64_t b_at[4];  // (columns beyond the last are the last's)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)  // (columns beyond the last are the last's)
-                b[j] = p.b + max(adapter, 0) * p.apart_b + min(col0 + 8 * (g >> 1) + 2 * j + (g & 1), p.n - 1) * p.ldb;
-            for (int place = o.start[i]; place < end; place += 32) {
-                const bool both = place + 16 < end;
-                uint4 r[4];
+        for (int j = 0; j < 4; ++j) b_at[j] = min(col0 + 8 * (g >> 1) + 2 * j + (g & 1), p.n - 1) * p.ldb + RS / 4 * q;
+        for (int unit = 0, n; unit < units; unit += n) {
+            const int adapter = o.adapter(unit);
+            n = unit + 1 < units && o.adapter(unit + 1) == adapter ? 2 : 1;
+            const RowAt* at = rows_at + 16 * unit + g;
+            Row8<SHIFT> r[kBatch][2];
+            auto load_r = [&](auto units_here) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h)
-                    if (p.r && place + g + 8 * h < end)
-                        r[h] = load_row8(p.r + (row0 + o.row[place + g + 8 * h]) * p.ldr, col, p.n, p.wide_r);
-                float c[2][4][4];
+                for (int i = 0; i < decltype(units_here)::value; ++i)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                    for (int h = 0; h < 2; ++h) r[i][h].load(r_tile + at[16 * i + 8 * h].r + col);
+            };
+            if (p.r && !edge) {
+                if (n == 2) load_r(std::integral_constant<int, 2>());
+                else load_r(std::integral_constant<int, 1>());
+            } else if (p.r) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                for (int i = 0; i < 4; ++i)
+                    if (i < 2 * n) r[i / 2][i % 2].a = load_cut(r_tile + at[8 * i].r + col, p.n - col);
+            }
+            const uint16_t* b = p.b + max(adapter, 0) * p.apart_b;
+            auto load_b = [&](Words<RS>(&to)[4], int k0) {
+                if (whole) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) c[t][j][k] = 0.f;
+                    for (int j = 0; j < 4; ++j) to[j] = load_words<RS, true>(b + b_at[j], k0, p.rank);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) to[j] = load_words<RS, false>(b + b_at[j], k0, p.rank - RS / 4 * q);
+                }
+            };
+            Words<RS> held[STEPS > 0 ? STEPS : 1][4];
+            if (adapter >= 0) {
+#pragma unroll
+                for (int i = 0; i < STEPS; ++i) load_b(held[i], i * RS);
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                if (i >= n) continue;
+                const RowAt row[2] = {at[16 * i], at[16 * i + 8]};
+                float c[4][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 u = p.r ? r[i][h].get(r_tile + row[h].r + col, edge) : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        c[j][2 * h] = __uint_as_float(w[j] << 16);
+                        c[j][2 * h + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                    }
+                }
                 if (adapter >= 0) {
-                    const uint32_t* s[4];
+                    auto add = [&](const Words<RS>(&u)[4], int k0) {
+                        Words<RS> s[2][2];  // [row][term]
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) s[h] = low + min(place + g + 8 * h, end - 1) * words + RS / 8 * q;
+                        for (int h = 0; h < 2; ++h) {
+                            const Words<RS>* from = reinterpret_cast<const Words<RS>*>(low + row[h].low + k0 + RS / 4 * q);
+                            s[h][0] = from[0], s[h][1] = from[1];
+                        }
+#pragma unroll
+                        for (int term = 0; term < 2; ++term)
+#pragma unroll
+                            for (int w = 0; w < RS / 8; w += 2)
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    mma(c[j], s[0][term].w[w], s[1][term].w[w], s[0][term].w[w + 1], s[1][term].w[w + 1],
+                                        u[j].w[w], u[j].w[w + 1]);
+                    };
+                    if (STEPS > 0) {
+#pragma unroll
+                        for (int k = 0; k < STEPS; ++k) add(held[k], k * RS);
+                    } else {
 #pragma unroll 2
-                    for (int k0 = 0; k0 < p.ldlow; k0 += RS) {
-                        Words<RS> u[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) u[j] = load_words<RS>(b[j], k0 + RS / 4 * q, p.rank);
-#pragma unroll
-                        for (int t = 0; t < 2; ++t) {
-                            if (t && !both) continue;
-#pragma unroll
-                            for (int term = 0; term < 2; ++term) {
-                                const Words<RS> x = *reinterpret_cast<const Words<RS>*>(s[2 * t] + term * second + k0 / 2);
-                                const Words<RS> y = *reinterpret_cast<const Words<RS>*>(s[2 * t + 1] + term * second + k0 / 2);
-#pragma unroll
-                                for (int w = 0; w < RS / 8; w += 2)
-#pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        mma(c[t][j], x.w[w], y.w[w], x.w[w + 1], y.w[w + 1], u[j].w[w], u[j].w[w + 1]);
-                            }
+                        for (int k0 = 0; k0 < p.ldlow; k0 += RS) {
+                            Words<RS> u[4];
+                            load_b(u, k0);
+                            add(u, k0);
                         }
                     }
                 }
+                if (p.act) {
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    if (place + g + 8 * h >= end) continue;
-                    float v[8];
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] = c[h >> 1][k >> 1][2 * (h & 1) + (k & 1)];
-                    if (p.r) {
-                        const uint32_t w[4] = {r[h].x, r[h].y, r[h].z, r[h].w};
+                        for (int k = 0; k < 4; ++k) c[j][k] = activate(c[j][k], p.act);
+                }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v[2 * k] += __uint_as_float(w[k] << 16);
-                            v[2 * k + 1] += __uint_as_float(w[k] & 0xffff0000u);
-                        }
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = pack2(c[j][2 * h], c[j][2 * h + 1]);
+                    uint16_t* to = d_tile + row[h].d + col;
+                    if (!edge) {
+                        store_row8<SHIFT>(to, make_uint4(w[0], w[1], w[2], w[3]), q, row[h].on);
+                    } else if (row[h].on) {
+                        store_cut(to, make_uint4(w[0], w[1], w[2], w[3]), p.n - col);
                     }
-                    if (p.act)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) v[k] = activate(v[k], p.act);
-                    store_row8(p.d + (row0 + o.row[place + g + 8 * h]) * p.ldd, col, p.n, p.wide_d, v);
                 }
             }
         }

@@ -62,16 +62,27 @@ __device__ __forceinline__ void add_exact(float& s, float& err, float p) {
 
 __device__ __forceinline__ double exact_dot(const uint16_t* a, const uint16_t* b, int first, int last, int n, int lane) {
     float s = 0.f, err = 0.f;
-#pragma unroll 8
-    for (int col = first + 8 * lane; col < last; col += 256) {
-        const uint4 u = load_edge(a, col, n), v = load_edge(b, col, n);
+    auto add = [&](const uint4& u, const uint4& v) {
         const uint32_t uw[4] = {u.x, u.y, u.z, u.w}, vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             add_exact(s, err, __fmul_rn(__uint_as_float(uw[i] << 16), __uint_as_float(vw[i] << 16)));
             add_exact(s, err, __fmul_rn(__uint_as_float(uw[i] & 0xffff0000u), __uint_as_float(vw[i] & 0xffff0000u)));
         }
+    };
+    constexpr int kBatch = 4;
+    int col = first + 8 * lane;
+    for (; col + 256 * (kBatch - 1) + 8 <= last; col += 256 * kBatch) {
+        uint4 u[kBatch], v[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            u[i] = *reinterpret_cast<const uint4*>(a + col + 256 * i);
+            v[i] = load_once(b + col + 256 * i);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) add(u[i], v[i]);
     }
+    for (; col < last; col += 256) add(load_edge(a, col, n), load_edge(b, col, n));
     // (of an infinite sum the error is none)
     double v = static_cast<double>(s) + (fabsf(s) <= 3.4028235e38f ? static_cast<double>(err) : 0.0);
 #pragma unroll
@@ -246,27 +257,28 @@ __device__ __forceinline__ void up_unit(const Params& p, const Lists& l, float* 
             for (int i = 0; i < 4; ++i) c[m][t][i] = 0.f;
 
     const int steps = p.d / kStep;
-    int s = warp;
-    for (; s + (kUnroll - 1) * kWarps < steps; s += kUnroll * kWarps) {
+    for (int s = warp; s < steps; s += kUnroll * kWarps) {
         uint4 a[kUnroll][4], b[kUnroll][NT];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int col = (s + u * kWarps) * kStep + 8 * q;
+        for (int u = 0; u < kUnroll; ++u) {  // (all loads at once; beyond the last step, it again)
+            const int col = min(s + u * kWarps, steps - 1) * kStep + 8 * q;
 #pragma unroll
             for (int i = 0; i < 4; ++i) a[u][i] = load_once(w[i] + col);
 #pragma unroll
             for (int t = 0; t < NT; ++t) b[u][t] = *reinterpret_cast<const uint4*>(x[t] + col);
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < kUnroll; ++u) {
+            if (s + u * kWarps >= steps) continue;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 mma_step(c[0][t], a[u][0], a[u][1], b[u][t]);
                 mma_step(c[1][t], a[u][2], a[u][3], b[u][t]);
             }
+        }
     }
-    for (; s * kStep < p.d; s += kWarps) {
-        const int col = s * kStep + 8 * q;
+    if (steps * kStep < p.d && warp == 0) {
+        const int col = steps * kStep + 8 * q;
         uint4 a[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = load_edge(w[i], col, p.d);
@@ -357,12 +369,11 @@ __device__ __forceinline__ void down_part(const Params& p, const Lists& l, const
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[t][i] = 0.f;
     const int whole = min(last, p.inner / kStep);
-    int s = first;
-    for (; s + kUnroll <= whole; s += kUnroll) {
+    for (int s = first; s < whole; s += kUnroll) {
         uint4 a[kUnroll][2], b[kUnroll][NT][2];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int col = (s + u) * kStep + 8 * q;
+        for (int u = 0; u < kUnroll; ++u) {  // (all loads at once; beyond the last step, it again)
+            const int col = min(s + u, whole - 1) * kStep + 8 * q;
 #pragma unroll
             for (int i = 0; i < 2; ++i) a[u][i] = load_once(w[i] + col);
 #pragma unroll
@@ -371,14 +382,16 @@ __device__ __forceinline__ void down_part(const Params& p, const Lists& l, const
                 for (int i = 0; i < 2; ++i) b[u][t][i] = *reinterpret_cast<const uint4*>(p.act[i] + x[t] + col);
         }
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
+        for (int u = 0; u < kUnroll; ++u) {
+            if (s + u >= whole) continue;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) mma_step(c[t], a[u][0], a[u][1], b[u][t][i]);
+        }
     }
-    for (; s < last; ++s) {
-        const int col = s * kStep + 8 * q;
+    if (whole < last) {
+        const int col = whole * kStep + 8 * q;
         uint4 a[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) a[i] = load_edge(w[i], col, p.inner);

@@ -69,12 +69,15 @@ __device__ __forceinline__ void split(float v, uint16_t& hi, uint16_t& lo) {
 __device__ __forceinline__ float bf16_value(uint16_t u) { return __uint_as_float(static_cast<uint32_t>(u) << 16); }
 __device__ __forceinline__ uint16_t bf16_bits(float v) { return __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-__device__ __forceinline__ float silu(float v) { return v / (1.f + __expf(-v)); }
+// The activations with the hardware's 2^x and 1/x (2^-22 of their value each; exact divisions took three times as long
+// as all else in the adapters' epilogue).  silu(-infinity) is NaN, as -infinity / infinity is.
+__device__ __forceinline__ float silu(float v) { return v * rcp_approx(1.f + ex2_approx(-1.44269504f * v)); }
 
 __device__ __forceinline__ float activate(float v, int act) {
     if (act == 1) {
+        // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u)), u = sqrt(2 / pi) (v + 0.044715 v^3)
         const float u = 0.7978845608028654f * (v + 0.044715f * v * v * v);
-        return v / (1.f + __expf(-2.f * u));  // 0.5 (1 + tanh u) = 1 / (1 + exp(-2u))
+        return v * rcp_approx(1.f + ex2_approx(-2.88539008f * u));
     }
     if (act == 2) return silu(v);
     if (act == 3) return v > 0.f ? v : (v != v ? v : 0.f);
