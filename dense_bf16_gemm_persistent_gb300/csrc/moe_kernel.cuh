@@ -20,7 +20,6 @@ constexpr int kPassTokens = 64;  // of a pass: a bit each in an expert's mask
 constexpr int kPairs = kPassTokens * kMaxTop;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kRows = 16;        // weight rows of a tile
-constexpr int kAhead = 16;       // steps of the second products that are on their way to L2 before their launch
 
 struct Params {
     const uint16_t* x;
@@ -37,17 +36,6 @@ struct Params {
     int renormalize;
     int share;               // CTAs of a tile of D in the last launch
 };
-
-// Which of the second products' steps a warp has: all chosen experts' steps one after the other, shared out evenly.
-struct Share {
-    int64_t at, end;
-};
-
-__device__ __forceinline__ Share share_of(int actives, int steps, int share, int rank, int warp) {
-    const int64_t all = static_cast<int64_t>(actives) * steps;
-    const int shares = share * kWarps, mine = rank * kWarps + warp;
-    return {all * mine / shares, all * (mine + 1) / shares};
-}
 
 // ---------------------------------------------------------------- router
 
@@ -70,7 +58,7 @@ __device__ __forceinline__ double exact_dot(const uint16_t* a, const uint16_t* b
             add_exact(s, err, __fmul_rn(__uint_as_float(uw[i] & 0xffff0000u), __uint_as_float(vw[i] & 0xffff0000u)));
         }
     };
-    constexpr int kBatch = 4;
+    constexpr int kBatch = 8;
     int col = first + 8 * lane;
     for (; col + 256 * (kBatch - 1) + 8 <= last; col += 256 * kBatch) {
         uint4 u[kBatch], v[kBatch];
@@ -329,23 +317,6 @@ __global__ void __launch_bounds__(kThreads, 2) up_kernel(const __grid_constant__
             else up_unit<4>(p, l, joined, e, row0, pair0, n);
         }
     }
-    // The second products' first steps to L2, so that the memory is not idle while this launch ends and the next
-    // one begins: a thread to a row of a warp's share, kAhead steps of it.
-    const int steps = (p.inner + kStep - 1) / kStep, blocks = (p.d + kRows - 1) / kRows * p.share;
-    for (int block = blockIdx.x; block < blocks; block += gridDim.x) {
-        const int warp = threadIdx.x / kRows, row = block / p.share * kRows + threadIdx.x % kRows;
-        if (warp >= kWarps || row >= p.d) continue;
-        const Share mine = share_of(l.actives, steps, p.share, block % p.share, warp);
-        const int a = static_cast<int>(mine.at / steps), first = static_cast<int>(mine.at - static_cast<int64_t>(a) * steps);
-        if (mine.at >= mine.end) continue;
-        const int n = static_cast<int>(min(mine.end - mine.at, static_cast<int64_t>(kAhead)));
-        const int bytes = min(n * kStep, p.inner - first * kStep) / 8 * 16;
-        if (bytes > 0)
-            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p.w[2] + l.active[a] * p.expert[2] + row * p.ldw[2] +
-                                                                            first * kStep),
-                         "r"(bytes)
-                         : "memory");
-    }
 }
 
 // ---------------------------------------------------------------- the second products and the weighted sum
@@ -412,8 +383,7 @@ __device__ __forceinline__ void down_part(const Params& p, const Lists& l, const
         }
 }
 
-// A cluster to 16 columns of D: its warps share all the steps of all the chosen experts evenly, one after the
-// other, and their sums are joined in the same order on every run.
+// A cluster to 16 columns of D; the sums of its CTAs' warps are joined in the same order on every run.
 // Dynamic shared memory: the warps' sums [warp][token][16].
 __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant__ Params p) {
     allow_next_kernel();
@@ -426,7 +396,13 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     make_lists(l, p, pair_weight);
     const int cluster = p.share, rank = blockIdx.x % cluster, row0 = blockIdx.x / cluster * kRows;
     const int warp = threadIdx.x >> 5, steps = (p.inner + kStep - 1) / kStep;
-    auto [at, end] = share_of(l.actives, steps, cluster, rank, warp);
+    // The steps of all chosen experts, one after the other, shared out evenly to the cluster's warps.  (Warps that take
+    // an expert's steps in turn, so that a block reads 512 contiguous bytes of a row at a time, took 3 to 10 % longer:
+    // more experts a warp, and a wait for the first loads of each.)
+    const int64_t all = static_cast<int64_t>(l.actives) * steps;
+    const int shares = cluster * kWarps, share = rank * kWarps + warp;
+    int64_t at = all * share / shares;
+    const int64_t end = all * (share + 1) / shares;
     float* y = sums + warp * outputs;
     while (at < end) {
         const int a = static_cast<int>(at / steps), first = static_cast<int>(at - static_cast<int64_t>(a) * steps);
