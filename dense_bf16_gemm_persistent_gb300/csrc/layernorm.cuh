@@ -8,17 +8,25 @@
 namespace gb {
 namespace rowwise {
 
-// The two sums over the row's threads, as row_sum().  `buf`: 32 pairs that no other sum in flight uses.
-__device__ __forceinline__ float2 row_sum2(float a, float b, float2* buf) {
+// The sums of two values over the row's threads, in the same order on every run; `half`: half of the power of two
+// that the row's warps fit in.  `buf`: 32 pairs that no other sum in flight uses.
+__device__ __forceinline__ float2 row_sum2(float a, float b, int half, float2* buf) {
     a = warp_sum(a);
     b = warp_sum(b);
     if (blockDim.y > 1) return make_float2(a, b);  // a row is one warp
-    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, at = lane & (2 * half - 1);
     if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
     __syncthreads();
-    const float2 t = lane < warps ? buf[lane] : make_float2(0.f, 0.f);
-    return make_float2(warp_sum(t.x), warp_sum(t.y));
+    float2 t = at < warps ? buf[at] : make_float2(0.f, 0.f);
+    for (int i = half; i > 0; i >>= 1) {
+        t.x += __shfl_xor_sync(0xffffffffu, t.x, i);
+        t.y += __shfl_xor_sync(0xffffffffu, t.y, i);
+    }
+    return t;
 }
+
+// Half of the least power of two (2 or more) that `warps` fit in.
+__device__ __forceinline__ int half_of(int warps) { return warps <= 2 ? 1 : 1 << (31 - __clz(warps - 1)); }
 
 // Elements of the chunk at `col0` that lie in the row.
 __device__ __forceinline__ int inside(int col0, int cols) { return max(0, min(col0 + 8, cols) - max(col0, 0)); }
@@ -50,33 +58,55 @@ struct LayerNormParams {
 // sums of squares are moved to the row's mean when they are joined,
 //     sum (h - mean)^2 = sum over warps [ S_w + n_w (mean_w - mean)^2 ],
 // so that a row has one barrier, as the root-mean-square norm's has.
+//
+// FULL: rows of whole, aligned 16-byte words (no chunk begins or ends inside one).  What a chunk costs decides: with
+// every chunk's ends looked at, as a shifted row wants it, 8192 x 4096 took 610 instructions a warp's part of a row and
+// 55 us, 62 % of issue slots used.
 // Dynamic shared memory: the rows [stage][x or r][chunk][thread], the weight, the bias.  (Three stages of
 // 16384 columns and both vectors would be 256 KB.)
 __host__ __device__ constexpr int layer_norm_stages(int v) { return v == 4 ? 2 : kRowStages; }
 
-template <int V, int DROP>
-__global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) layer_norm_kernel(const __grid_constant__ LayerNormParams p) {
+// 16 bytes to the thread's own place, which it alone reads.
+__device__ __forceinline__ void fetch_16(uint4* to, const uint16_t* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(to))),
+                 "l"(from)
+                 : "memory");
+}
+
+template <int V, int DROP, bool FULL>
+__global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_kernel(const __grid_constant__ LayerNormParams p) {
     allow_next_kernel();
     wait_for_earlier_kernels();
     constexpr int kStages = layer_norm_stages(V);
+    constexpr bool kHeld = FULL && V == 2;  // the weight and the bias in registers
     __shared__ float2 parts[2][32];
-    __shared__ float counts[32];
+    __shared__ float2 counts[32];  // and one over them
     extern __shared__ __align__(16) uint8_t smem[];
     const int row0 = blockIdx.x * blockDim.y + threadIdx.y, stride = gridDim.x * blockDim.y;
-    const int shift = p.wide ? row_shift(p.x + row0 * p.ldx) : 0;
+    const int shift = !FULL && p.wide ? row_shift(p.x + row0 * p.ldx) : 0;
     const int tid = threadIdx.x, threads = blockDim.x, all = blockDim.x * blockDim.y, lane = tid & 31;
+    const int warps = threads >> 5, half = half_of(warps);
     uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.y * threads + tid;
     const Draw<DROP> draw(p.drop);
+    const uint16_t *x_next = p.x + row0 * p.ldx, *r_next = p.r + row0 * p.ldr;  // (of the row that is fetched next)
     auto fetch = [&](int64_t row, int stage) {
         if (row < p.m) {
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int col0 = 8 * (tid + k * threads) - shift;
-                fetch_chunk(slots + (stage * 2 * V + k) * all, p.x + row * p.ldx, col0, p.d, p.wide, row > 0 && p.ldx >= 8);
-                if (p.r)
-                    fetch_chunk(slots + ((stage * 2 + 1) * V + k) * all, p.r + row * p.ldr, col0, p.d, p.wide,
-                                row > 0 && p.ldr >= 8);
+                uint4* to = slots + stage * 2 * V * all + k * all;
+                if (FULL) {
+                    if (col0 < p.d) {
+                        fetch_16(to, x_next + col0);
+                        if (p.r) fetch_16(to + V * all, r_next + col0);
+                    }
+                } else {
+                    fetch_chunk(to, x_next, col0, p.d, p.wide, row > 0 && p.ldx >= 8);
+                    if (p.r) fetch_chunk(to + V * all, r_next, col0, p.d, p.wide, row > 0 && p.ldr >= 8);
+                }
             }
+            x_next += stride * p.ldx;
+            r_next += stride * p.ldr;
         }
         fetch_commit();
     };
@@ -84,38 +114,56 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) layer_norm_kernel(con
     for (int s = 0; s < kStages - 1; ++s) fetch(row0 + static_cast<int64_t>(s) * stride, s);
     uint4* weight = slots + kStages * 2 * V * all;  // (the thread's own part of it, and of the bias)
     uint4* bias = weight + V * all;
+    float held[2][kHeld ? V : 1][8];
     float count = 0.f;  // of the warp's elements in a row: the same in every row
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int col0 = 8 * (tid + k * threads) - shift;
-        weight[k * all] = load_chunk(p.weight, col0, p.d, shift == 0 && p.wide_weight);
-        if (p.bias) bias[k * all] = load_chunk(p.bias, col0, p.d, shift == 0 && p.wide_bias);
+        const uint4 w = load_chunk(p.weight, col0, p.d, shift == 0 && p.wide_weight);
+        const uint4 b = p.bias ? load_chunk(p.bias, col0, p.d, shift == 0 && p.wide_bias) : make_uint4(0, 0, 0, 0);
+        if constexpr (kHeld) {
+            unpack(w, held[0][k]);
+            unpack(b, held[1][k]);
+        } else {
+            weight[k * all] = w;
+            bias[k * all] = b;
+        }
         count += static_cast<float>(inside(col0, p.d));
     }
     count = warp_sum(count);
-    if (blockDim.y == 1 && lane == 0) counts[tid >> 5] = count;  // (read after a row's barrier)
     const float of_row = 1.f / static_cast<float>(p.d), of_warp = count > 0.f ? 1.f / count : 0.f;
+    if (blockDim.y == 1 && lane == 0) counts[tid >> 5] = make_float2(count, of_warp);  // (read after a row's barrier)
 
     int stage = 0, turn = 0;
-    for (int64_t r = row0; r < p.m; r += stride, turn ^= 1) {
+    uint16_t *h_row = p.h + row0 * p.ldh, *y_row = p.y + row0 * p.ldy;
+    for (int64_t r = row0; r < p.m; r += stride, turn ^= 1, h_row += stride * p.ldh, y_row += stride * p.ldy) {
         const int row = static_cast<int>(r);
         fetch(r + static_cast<int64_t>(kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
         fetch_wait<kStages - 1>();
         float v[V][8], sum = 0.f;
+        const uint4* at = slots + stage * 2 * V * all;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
-            unpack(read_chunk(slots + (stage * 2 * V + k) * all, col0), v[k]);
+            if (FULL && col0 >= p.d) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
+                continue;
+            }
+            unpack(FULL ? at[k * all] : read_chunk(at + k * all, col0), v[k]);
             if (DROP) draw.chunk(v[k], row, col0);
             if (p.r) {
                 float r[8];
-                unpack(read_chunk(slots + ((stage * 2 + 1) * V + k) * all, col0), r);
+                unpack(FULL ? at[(V + k) * all] : read_chunk(at + (V + k) * all, col0), r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] += r[i];
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += v[k][i];  // (outside the row: zeros)
-            if (p.h && col0 < p.d) store_chunk(p.h + row * p.ldh, col0, p.d, p.wide, pack(v[k]));
+            if (p.h) {
+                if (FULL) *reinterpret_cast<uint4*>(h_row + col0) = pack(v[k]);
+                else if (col0 < p.d) store_chunk(h_row, col0, p.d, p.wide, pack(v[k]));
+            }
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
         sum = warp_sum(sum);
@@ -123,10 +171,10 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) layer_norm_kernel(con
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
-            if (col0 >= 0 && col0 + 8 <= p.d) {
+            if (FULL ? col0 < p.d : col0 >= 0 && col0 + 8 <= p.d) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) squares = fmaf(v[k][i] - mean, v[k][i] - mean, squares);
-            } else {
+            } else if (!FULL) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     if (col0 + i >= 0 && col0 + i < p.d) squares = fmaf(v[k][i] - mean, v[k][i] - mean, squares);
@@ -137,12 +185,16 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) layer_norm_kernel(con
             float2* part = parts[turn];
             if (lane == 0) part[tid >> 5] = make_float2(sum, squares);
             __syncthreads();
-            const bool on = lane < threads >> 5;
-            const float2 t = on ? part[lane] : make_float2(0.f, 0.f);
-            const float n = on ? counts[lane] : 0.f;
-            mean = warp_sum(t.x) * of_row;
-            const float off = n > 0.f ? t.x / n - mean : 0.f;
-            squares = warp_sum(fmaf(n * off, off, t.y));
+            const int place = lane & (2 * half - 1);
+            const bool on = place < warps;
+            const float2 t = on ? part[place] : make_float2(0.f, 0.f);
+            const float2 n = on ? counts[place] : make_float2(0.f, 0.f);
+            mean = t.x;
+            for (int i = half; i > 0; i >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, i);
+            mean *= of_row;
+            const float off = n.x > 0.f ? fmaf(t.x, n.y, -mean) : 0.f;
+            squares = fmaf(n.x * off, off, t.y);
+            for (int i = half; i > 0; i >>= 1) squares += __shfl_xor_sync(0xffffffffu, squares, i);
         }
         const float rstd = 1.f / sqrtf(squares * of_row + p.eps);
         if (tid == 0) {
@@ -153,16 +205,18 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP ? 80 : 64) layer_norm_kernel(con
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
             if (col0 >= p.d) continue;
-            float w[8];
-            unpack(weight[k * all], w);
+            if constexpr (kHeld) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = (v[k][i] - mean) * rstd * w[i];
-            if (p.bias) {
-                unpack(bias[k * all], w);
+                for (int i = 0; i < 8; ++i) v[k][i] = fmaf((v[k][i] - mean) * rstd, held[0][k][i], held[1][k][i]);
+            } else {
+                float w[8], b[8];
+                unpack(weight[k * all], w);
+                unpack(bias[k * all], b);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[k][i] += w[i];
+                for (int i = 0; i < 8; ++i) v[k][i] = fmaf((v[k][i] - mean) * rstd, w[i], b[i]);
             }
-            store_chunk(p.y + row * p.ldy, col0, p.d, p.wide, pack(v[k]));
+            if (FULL) *reinterpret_cast<uint4*>(y_row + col0) = pack(v[k]);
+            else store_chunk(y_row, col0, p.d, p.wide, pack(v[k]));
         }
     }
 }
@@ -187,104 +241,160 @@ struct LayerNormBwdParams {
 
 // With xhat = (h - mean) rstd and g = dy weight:  dr = rstd (g - mean(g) - xhat mean(g xhat)) + dh,
 // dx = dropout's gradient of dr,  dweight = sum over rows of dy xhat,  dbias = sum over rows of dy.
-// Rows, stages and the gradients' sums in registers as in norm_bwd_kernel.
+// Rows and the gradients' sums in registers as in norm_bwd_kernel.  FULL as in layer_norm_kernel: g and xhat stay in
+// registers from the first pass over a row to the second.  (With both made again from shared memory, and every chunk's
+// ends looked at, 8192 x 4096 took 700 instructions a warp's part of a row and 68 us.)
 // Dynamic shared memory: the rows [stage][dY, H or dH][chunk][thread], then the weight.
-template <int V, int DROP>
-__global__ void __maxnreg__(V == 4 ? 128 : 80) layer_norm_bwd_kernel(const __grid_constant__ LayerNormBwdParams p) {
+__host__ __device__ constexpr int layer_bwd_stages(int v, bool full) { return full && v == 2 ? 3 : kBwdStages; }
+
+template <int V, int DROP, bool FULL>
+__global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(const __grid_constant__ LayerNormBwdParams p) {
     allow_next_kernel();
     wait_for_earlier_kernels();
+    constexpr int kStages = layer_bwd_stages(V, FULL);
+    constexpr bool kHeld = FULL && V == 2;  // g and xhat, and the weight, in registers
     __shared__ float2 sums[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
     const int row0 = blockIdx.x * blockDim.y + threadIdx.y, stride = gridDim.x * blockDim.y;
-    const int shift = p.wide ? row_shift(p.dy + row0 * p.lddy) : 0;
-    const int tid = threadIdx.x, threads = blockDim.x, all = blockDim.x * blockDim.y;
+    const int shift = !FULL && p.wide ? row_shift(p.dy + row0 * p.lddy) : 0;
+    const int tid = threadIdx.x, threads = blockDim.x, all = blockDim.x * blockDim.y, half = half_of(threads >> 5);
     uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.y * threads + tid;
-    uint4* weight = slots + kBwdStages * 3 * V * all;  // (the thread's own part of it)
+    uint4* weight = slots + kStages * 3 * V * all;  // (the thread's own part of it)
     const Draw<DROP> draw(p.drop);
     auto slot = [&](int stage, int matrix, int k) { return slots + ((stage * 3 + matrix) * V + k) * all; };
+    auto chunk = [&](int stage, int matrix, int k, int col0) {
+        return FULL ? *slot(stage, matrix, k) : read_chunk(slot(stage, matrix, k), col0);
+    };
+    const uint16_t *dy_next = p.dy + row0 * p.lddy, *h_next = p.h + row0 * p.ldh, *dh_next = p.dh + row0 * p.lddh;
     auto fetch = [&](int64_t row, int stage) {
         if (row < p.m) {
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int col0 = 8 * (tid + k * threads) - shift;
-                fetch_chunk(slot(stage, 0, k), p.dy + row * p.lddy, col0, p.d, p.wide, row > 0 && p.lddy >= 8);
-                fetch_chunk(slot(stage, 1, k), p.h + row * p.ldh, col0, p.d, p.wide, row > 0 && p.ldh >= 8);
-                if (p.dh) fetch_chunk(slot(stage, 2, k), p.dh + row * p.lddh, col0, p.d, p.wide, row > 0 && p.lddh >= 8);
+                if (FULL) {
+                    if (col0 < p.d) {
+                        fetch_16(slot(stage, 0, k), dy_next + col0);
+                        fetch_16(slot(stage, 1, k), h_next + col0);
+                        if (p.dh) fetch_16(slot(stage, 2, k), dh_next + col0);
+                    }
+                } else {
+                    fetch_chunk(slot(stage, 0, k), dy_next, col0, p.d, p.wide, row > 0 && p.lddy >= 8);
+                    fetch_chunk(slot(stage, 1, k), h_next, col0, p.d, p.wide, row > 0 && p.ldh >= 8);
+                    if (p.dh) fetch_chunk(slot(stage, 2, k), dh_next, col0, p.d, p.wide, row > 0 && p.lddh >= 8);
+                }
             }
+            dy_next += stride * p.lddy;
+            h_next += stride * p.ldh;
+            dh_next += stride * p.lddh;
         }
         fetch_commit();
     };
-    fetch(row0, 0);
-    float dw[V][8], db[V][8];
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) fetch(row0 + static_cast<int64_t>(s) * stride, s);
+    float dw[V][8], db[V][8], held[kHeld ? V : 1][8];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        weight[k * all] = load_chunk(p.weight, 8 * (tid + k * threads) - shift, p.d, shift == 0 && p.wide_weight);
+        const uint4 w = load_chunk(p.weight, 8 * (tid + k * threads) - shift, p.d, shift == 0 && p.wide_weight);
+        if constexpr (kHeld) unpack(w, held[k]);
+        else weight[k * all] = w;
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[k][i] = db[k][i] = 0.f;
     }
     const float of_row = 1.f / static_cast<float>(p.d);
 
-    int turn = 0;  // of the stages and of row_sum2's places
-    for (int64_t r = row0; r < p.m; r += stride, turn ^= 1) {
+    int stage = 0, turn = 0;  // (of row_sum2's places)
+    uint16_t *dr_row = p.dr + row0 * p.lddr, *dx_row = p.dx + row0 * p.lddx;
+    for (int64_t r = row0; r < p.m; r += stride, turn ^= 1, dr_row += stride * p.lddr, dx_row += stride * p.lddx) {
         const int row = static_cast<int>(r);
         const float rstd = p.rstd[row], mean = p.mean[row];
-        fetch(r + stride, turn ^ 1);
-        fetch_wait<1>();
+        fetch(r + static_cast<int64_t>(kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+        fetch_wait<kStages - 1>();
         float sum = 0.f, dot = 0.f;  // of g and of g xhat
+        float g[kHeld ? V : 1][8], xhat[kHeld ? V : 1][8];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
+            if (FULL && col0 >= p.d) continue;
             float t[8], h[8], w[8];
-            unpack(read_chunk(slot(turn, 0, k), col0), t);  // (outside the row dY is zero, and adds nothing)
-            unpack(read_chunk(slot(turn, 1, k), col0), h);
-            unpack(weight[k * all], w);
+            unpack(chunk(stage, 0, k, col0), t);  // (outside the row dY is zero, and adds nothing)
+            unpack(chunk(stage, 1, k, col0), h);
+            if constexpr (kHeld) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = held[k][i];
+            } else {
+                unpack(weight[k * all], w);
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
+                const float gi = t[i] * w[i], xi = (h[i] - mean) * rstd;
                 db[k][i] += t[i];
-                sum = fmaf(t[i], w[i], sum);
-                t[i] *= (h[i] - mean) * rstd;
-                dot = fmaf(t[i], w[i], dot);
-                dw[k][i] += t[i];
+                sum += gi;
+                dot = fmaf(gi, xi, dot);
+                dw[k][i] = fmaf(t[i], xi, dw[k][i]);
+                if constexpr (kHeld) g[k][i] = gi, xhat[k][i] = xi;
             }
         }
-        const float2 total = row_sum2(sum, dot, sums[turn]);
+        const float2 total = row_sum2(sum, dot, half, sums[turn]);
         const float mean_g = total.x * of_row, mean_gx = total.y * of_row;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
             if (col0 >= p.d) continue;
             float v[8], h[8], w[8];
-            unpack(read_chunk(slot(turn, 0, k), col0), v);
-            unpack(read_chunk(slot(turn, 1, k), col0), h);
-            unpack(weight[k * all], w);
+            if constexpr (kHeld) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = rstd * (v[i] * w[i] - mean_g - (h[i] - mean) * rstd * mean_gx);
-            if (p.dh) {
-                unpack(read_chunk(slot(turn, 2, k), col0), h);
+                for (int i = 0; i < 8; ++i) v[i] = g[k][i] - fmaf(xhat[k][i], mean_gx, mean_g);
+            } else {
+                unpack(chunk(stage, 0, k, col0), v);
+                unpack(chunk(stage, 1, k, col0), h);
+                unpack(weight[k * all], w);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] += h[i];
+                for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] - fmaf((h[i] - mean) * rstd, mean_gx, mean_g);
             }
-            store_chunk(p.dr + row * p.lddr, col0, p.d, p.wide, pack(v));
+            if (p.dh) {
+                unpack(chunk(stage, 2, k, col0), h);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = fmaf(rstd, v[i], h[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] *= rstd;
+            }
+            if (FULL) *reinterpret_cast<uint4*>(dr_row + col0) = pack(v);
+            else store_chunk(dr_row, col0, p.d, p.wide, pack(v));
             if (DROP) {
                 draw.chunk(v, row, col0);
-                store_chunk(p.dx + row * p.lddx, col0, p.d, p.wide, pack(v));
+                if (FULL) *reinterpret_cast<uint4*>(dx_row + col0) = pack(v);
+                else store_chunk(dx_row, col0, p.d, p.wide, pack(v));
             }
         }
+        stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     fetch_wait<0>();
 
     float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.d;
     if (blockDim.y == 1) {
 #pragma unroll
-        for (int k = 0; k < V; ++k)
+        for (int k = 0; k < V; ++k) {
+            const int col0 = 8 * (tid + k * threads) - shift;
+            if (FULL && (reinterpret_cast<uintptr_t>(p.partial) & 15) == 0) {
+                if (col0 >= p.d) continue;
+#pragma unroll
+                for (int i = 0; i < 8; i += 4) {
+                    *reinterpret_cast<float4*>(part + col0 + i) = make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
+                    *reinterpret_cast<float4*>(part + p.d + col0 + i) =
+                        make_float4(db[k][i], db[k][i + 1], db[k][i + 2], db[k][i + 3]);
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int col = 8 * (tid + k * threads) - shift + i;
+                const int col = col0 + i;
                 if (col >= 0 && col < p.d) {
                     part[col] = dw[k][i];
                     part[p.d + col] = db[k][i];
                 }
             }
+        }
         return;
     }
     // several rows a block: the warps add theirs one after the other, where the rows were

@@ -191,45 +191,61 @@ int64_t bwd_workspace(int64_t m, int64_t d, int sms) {
 
 // ---------------------------------------------------------------- layer norm
 
-template <int V, int DROP>
+// Whether every row of the matrices is whole, aligned 16-byte words.
+template <size_t N>
+bool full_rows(const Mat (&mats)[N], int64_t rows, int64_t cols) {
+    if (cols % 8) return false;
+    for (const Mat& m : mats)
+        if (m.p && (!aligned_to(m.p, 16) || (rows > 1 && m.ld % 8))) return false;
+    return true;
+}
+
+template <int V, int DROP, bool FULL>
 gb_status_t launch_layer_norm(const LayerNormParams& p, const RowPlan& pl, int dev, const DeviceInfo& info,
                               cudaStream_t stream) {
     static std::atomic<bool> ready[64];
-    gb_status_t st = allow_smem(layer_norm_kernel<V, DROP>, ready, dev, info.smem_optin - 1024);
+    gb_status_t st = allow_smem(layer_norm_kernel<V, DROP, FULL>, ready, dev, info.smem_optin - 1024);
     if (st != GB_OK) return st;
-    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : DROP ? 768 : 1024, info.sms);
-    const size_t smem = static_cast<size_t>(layer_norm_stages(V) * 2 + 2) * V * 16 * pl.threads * pl.rows;
-    note_plan("kernel=add_layer_norm dropout=%lld threads=%lld rows=%lld chunks=%lld blocks=%lld wide=%lld", DROP,
-              pl.threads, pl.rows, V, blocks, pl.wide);
+    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : DROP || FULL ? 768 : 1024, info.sms);
+    const size_t smem = static_cast<size_t>(layer_norm_stages(V) * 2 + (FULL && V == 2 ? 0 : 2)) * V * 16 * pl.threads * pl.rows;
+    note_plan("kernel=add_layer_norm dropout=%lld threads=%lld rows=%lld blocks=%lld wide=%lld full=%lld", DROP,
+              pl.threads, pl.rows, blocks, pl.wide, FULL);
     return Launch(static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream)(
-        "add_layer_norm launch", layer_norm_kernel<V, DROP>, p);
+        "add_layer_norm launch", layer_norm_kernel<V, DROP, FULL>, p);
 }
 
 template <int DROP>
-gb_status_t run_layer_norm(const LayerNormParams& p, const RowPlan& pl, int dev, const DeviceInfo& info,
+gb_status_t run_layer_norm(const LayerNormParams& p, const RowPlan& pl, bool full, int dev, const DeviceInfo& info,
                            cudaStream_t stream) {
-    return pl.chunks_per_thread <= 2 ? launch_layer_norm<2, DROP>(p, pl, dev, info, stream)
-                                     : launch_layer_norm<4, DROP>(p, pl, dev, info, stream);
+    if (full)
+        return pl.chunks_per_thread <= 2 ? launch_layer_norm<2, DROP, true>(p, pl, dev, info, stream)
+                                         : launch_layer_norm<4, DROP, true>(p, pl, dev, info, stream);
+    return pl.chunks_per_thread <= 2 ? launch_layer_norm<2, DROP, false>(p, pl, dev, info, stream)
+                                     : launch_layer_norm<4, DROP, false>(p, pl, dev, info, stream);
 }
 
-template <int V, int DROP>
-gb_status_t launch_layer_bwd(const LayerNormBwdParams& p, const RowPlan& pl, int blocks, int dev, const DeviceInfo& info,
+template <int V, int DROP, bool FULL>
+gb_status_t launch_layer_bwd(const LayerNormBwdParams& p, const RowPlan& pl, int* blocks, int dev, const DeviceInfo& info,
                              cudaStream_t stream) {
     static std::atomic<bool> ready[64];
-    gb_status_t st = allow_smem(layer_norm_bwd_kernel<V, DROP>, ready, dev, info.smem_optin - 1024);
+    gb_status_t st = allow_smem(layer_norm_bwd_kernel<V, DROP, FULL>, ready, dev, info.smem_optin - 1024);
     if (st != GB_OK) return st;
-    // two stages of three matrices, and the weight; and the join of a block's rows
-    size_t smem = static_cast<size_t>(kBwdStages * 3 + 1) * V * 16 * pl.threads * pl.rows;
+    // the stages of three matrices, and the weight; and the join of a block's rows
+    size_t smem = static_cast<size_t>(layer_bwd_stages(V, FULL) * 3 + (FULL && V == 2 ? 0 : 1)) * V * 16 * pl.threads * pl.rows;
     if (pl.rows > 1) smem = std::max(smem, static_cast<size_t>(p.d) * 8);
-    return Launch(blocks, dim3(pl.threads, pl.rows), smem, stream)("add_layer_norm_backward launch",
-                                                                   layer_norm_bwd_kernel<V, DROP>, p);
+    if (FULL && V == 2) *blocks = static_cast<int>(blocks_for(p.m, pl, 512, info.sms));  // (never more than without)
+    return Launch(*blocks, dim3(pl.threads, pl.rows), smem, stream)("add_layer_norm_backward launch",
+                                                                    layer_norm_bwd_kernel<V, DROP, FULL>, p);
 }
 
 template <int DROP>
-gb_status_t run_layer_bwd(const LayerNormBwdParams& p, const RowPlan& pl, int blocks, int dev, const DeviceInfo& info,
-                          cudaStream_t stream) {
-    return pl.chunks_per_thread <= 2 ? launch_layer_bwd<2, DROP>(p, pl, blocks, dev, info, stream)
-                                     : launch_layer_bwd<4, DROP>(p, pl, blocks, dev, info, stream);
+gb_status_t run_layer_bwd(const LayerNormBwdParams& p, const RowPlan& pl, bool full, int* blocks, int dev,
+                          const DeviceInfo& info, cudaStream_t stream) {
+    if (full)
+        return pl.chunks_per_thread <= 2 ? launch_layer_bwd<2, DROP, true>(p, pl, blocks, dev, info, stream)
+                                         : launch_layer_bwd<4, DROP, true>(p, pl, blocks, dev, info, stream);
+    return pl.chunks_per_thread <= 2 ? launch_layer_bwd<2, DROP, false>(p, pl, blocks, dev, info, stream)
+                                     : launch_layer_bwd<4, DROP, false>(p, pl, blocks, dev, info, stream);
 }
 
 }  // namespace
@@ -499,11 +515,12 @@ gb_status_t gb_add_layer_norm(const void* X, int64_t ldx, const void* R, int64_t
     prm.wide = pl.wide;
     prm.wide_weight = aligned_to(weight, 16);
     prm.wide_bias = aligned_to(bias, 16);
+    const bool full = full_rows(mats, M, D);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     switch (drop_kind(p, rng_state)) {
-        case kNoDrop: return run_layer_norm<kNoDrop>(prm, pl, dev, info, s);
-        case kKeys: return run_layer_norm<kKeys>(prm, pl, dev, info, s);
-        default: return run_layer_norm<kState>(prm, pl, dev, info, s);
+        case kNoDrop: return run_layer_norm<kNoDrop>(prm, pl, full, dev, info, s);
+        case kKeys: return run_layer_norm<kKeys>(prm, pl, full, dev, info, s);
+        default: return run_layer_norm<kState>(prm, pl, full, dev, info, s);
     }
 }
 
@@ -573,10 +590,11 @@ gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void*
         prm.wide = pl.wide;
         prm.wide_weight = aligned_to(weight, 16);
         blocks = bwd_blocks(M, pl, info.sms);
+        const bool full = full_rows(mats, M, D);
         switch (drop_kind(p, rng_state)) {
-            case kNoDrop: st = run_layer_bwd<kNoDrop>(prm, pl, blocks, dev, info, s); break;
-            case kKeys: st = run_layer_bwd<kKeys>(prm, pl, blocks, dev, info, s); break;
-            default: st = run_layer_bwd<kState>(prm, pl, blocks, dev, info, s); break;
+            case kNoDrop: st = run_layer_bwd<kNoDrop>(prm, pl, full, &blocks, dev, info, s); break;
+            case kKeys: st = run_layer_bwd<kKeys>(prm, pl, full, &blocks, dev, info, s); break;
+            default: st = run_layer_bwd<kState>(prm, pl, full, &blocks, dev, info, s); break;
         }
         if (st != GB_OK) return st;
     }

@@ -189,6 +189,15 @@ def test_the_workspace_is_checked_and_any_contents_do():
         gb.add_layer_norm_backward(dy, h, w, mean, rstd, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
 
 
+@pytest.mark.parametrize("m,d", [(9, 64), (20, 4096), (3, 16384)])
+def test_a_workspace_that_begins_anywhere(m, d):
+    h, w, dy = normal(m, d, seed=1), normal(d, seed=2), normal(m, d, seed=3)
+    _, _, mean, rstd = gb.add_layer_norm(h, w)
+    need = gb.add_layer_norm_backward_workspace_bytes(m, d)
+    for offset in (0, 4, 8):
+        check_backward(dy, h, w, mean, rstd, None, workspace=torch.empty(need + 16, dtype=torch.uint8, device=DEV)[offset:])
+
+
 def test_wrong_tensors_are_refused():
     x, w = normal(4, 64, seed=1), normal(64, seed=2)
     f = torch.ones(4, device=DEV)
