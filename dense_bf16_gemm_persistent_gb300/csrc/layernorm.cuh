@@ -31,6 +31,48 @@ __device__ __forceinline__ int half_of(int warps) { return warps <= 2 ? 1 : 1 <<
 // Elements of the chunk at `col0` that lie in the row.
 __device__ __forceinline__ int inside(int col0, int cols) { return max(0, min(col0 + 8, cols) - max(col0, 0)); }
 
+// Eight elements of a vector at `col0` (zeros outside it), which lies aligned: the two 16-byte words that hold them.
+__device__ __forceinline__ uint4 load_vector(const uint16_t* vec, int col0, int cols, bool aligned) {
+    const int first = col0 & ~7, by = col0 & 7;
+    if (!aligned || col0 < 0 || first + 16 > cols || by == 0) return load_chunk(vec, col0, cols, aligned && by == 0);
+    const uint4 a = *reinterpret_cast<const uint4*>(vec + first), b = *reinterpret_cast<const uint4*>(vec + first + 8);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    if (by & 4) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (by & 2) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (by & 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A chunk that a row ends in (`wide`: it begins on 16 bytes), in pieces of 8, 4 and 2 bytes: the warps that hold a
+// row's ends are waited for by all others, and element after element took twice as long.
+__device__ __forceinline__ void store_end(uint16_t* row, int col0, int cols, bool wide, const uint4& u) {
+    if (!wide || (col0 < 0 && col0 + 8 > cols)) {
+        store_chunk(row, col0, cols, false, u);
+        return;
+    }
+    uint16_t* to = row + col0;
+    if (col0 < 0) {  // elements s .. 7
+        const int s = -col0, even = s + (s & 1);
+        if (s & 1) to[s] = static_cast<uint16_t>((s == 1 ? u.x : s == 3 ? u.y : s == 5 ? u.z : u.w) >> 16);
+        if (even & 2) *reinterpret_cast<uint32_t*>(to + even) = even == 2 ? u.y : u.w;
+        if (even <= 4) *reinterpret_cast<uint2*>(to + 4) = make_uint2(u.z, u.w);
+    } else {  // elements 0 .. n - 1
+        const int n = cols - col0;
+        if (n & 4) *reinterpret_cast<uint2*>(to) = make_uint2(u.x, u.y);
+        if (n & 2) *reinterpret_cast<uint32_t*>(to + (n & 4)) = n & 4 ? u.z : u.x;
+        if (n & 1) to[n & 6] = static_cast<uint16_t>((n & 6) == 0 ? u.x : (n & 6) == 2 ? u.y : (n & 6) == 4 ? u.z : u.w);
+    }
+}
+
 // ---------------------------------------------------------------- forward
 
 struct LayerNormParams {
@@ -74,11 +116,11 @@ __device__ __forceinline__ void fetch_16(uint4* to, const uint16_t* from) {
 }
 
 template <int V, int DROP, bool FULL>
-__global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_kernel(const __grid_constant__ LayerNormParams p) {
+__global__ void __maxnreg__(V == 4 ? 128 : 80) layer_norm_kernel(const __grid_constant__ LayerNormParams p) {
     allow_next_kernel();
     wait_for_earlier_kernels();
     constexpr int kStages = layer_norm_stages(V);
-    constexpr bool kHeld = FULL && V == 2;  // the weight and the bias in registers
+    constexpr bool kHeld = V == 2;  // the weight and the bias in registers
     __shared__ float2 parts[2][32];
     __shared__ float2 counts[32];  // and one over them
     extern __shared__ __align__(16) uint8_t smem[];
@@ -88,6 +130,8 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_ke
     const int warps = threads >> 5, half = half_of(warps);
     uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.y * threads + tid;
     const Draw<DROP> draw(p.drop);
+    // a chunk that lies in the row whole (a thread's chunks do so in all its rows, or in none)
+    auto whole = [&](int col0) { return FULL ? col0 < p.d : p.wide && col0 >= 0 && col0 + 8 <= p.d; };
     const uint16_t *x_next = p.x + row0 * p.ldx, *r_next = p.r + row0 * p.ldr;  // (of the row that is fetched next)
     auto fetch = [&](int64_t row, int stage) {
         if (row < p.m) {
@@ -95,12 +139,10 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_ke
             for (int k = 0; k < V; ++k) {
                 const int col0 = 8 * (tid + k * threads) - shift;
                 uint4* to = slots + stage * 2 * V * all + k * all;
-                if (FULL) {
-                    if (col0 < p.d) {
-                        fetch_16(to, x_next + col0);
-                        if (p.r) fetch_16(to + V * all, r_next + col0);
-                    }
-                } else {
+                if (whole(col0)) {
+                    fetch_16(to, x_next + col0);
+                    if (p.r) fetch_16(to + V * all, r_next + col0);
+                } else if (!FULL && col0 < p.d) {
                     fetch_chunk(to, x_next, col0, p.d, p.wide, row > 0 && p.ldx >= 8);
                     if (p.r) fetch_chunk(to + V * all, r_next, col0, p.d, p.wide, row > 0 && p.ldr >= 8);
                 }
@@ -119,8 +161,8 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_ke
 #pragma unroll
     for (int k = 0; k < V; ++k) {
         const int col0 = 8 * (tid + k * threads) - shift;
-        const uint4 w = load_chunk(p.weight, col0, p.d, shift == 0 && p.wide_weight);
-        const uint4 b = p.bias ? load_chunk(p.bias, col0, p.d, shift == 0 && p.wide_bias) : make_uint4(0, 0, 0, 0);
+        const uint4 w = load_vector(p.weight, col0, p.d, p.wide_weight);
+        const uint4 b = p.bias ? load_vector(p.bias, col0, p.d, p.wide_bias) : make_uint4(0, 0, 0, 0);
         if constexpr (kHeld) {
             unpack(w, held[0][k]);
             unpack(b, held[1][k]);
@@ -145,24 +187,24 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_ke
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
-            if (FULL && col0 >= p.d) {
+            if (col0 >= p.d) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] = 0.f;
                 continue;
             }
-            unpack(FULL ? at[k * all] : read_chunk(at + k * all, col0), v[k]);
+            unpack(FULL || col0 >= 0 ? at[k * all] : read_chunk(at + k * all, col0), v[k]);
             if (DROP) draw.chunk(v[k], row, col0);
             if (p.r) {
                 float r[8];
-                unpack(FULL ? at[(V + k) * all] : read_chunk(at + (V + k) * all, col0), r);
+                unpack(FULL || col0 >= 0 ? at[(V + k) * all] : read_chunk(at + (V + k) * all, col0), r);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] += r[i];
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += v[k][i];  // (outside the row: zeros)
             if (p.h) {
-                if (FULL) *reinterpret_cast<uint4*>(h_row + col0) = pack(v[k]);
-                else if (col0 < p.d) store_chunk(h_row, col0, p.d, p.wide, pack(v[k]));
+                if (whole(col0)) *reinterpret_cast<uint4*>(h_row + col0) = pack(v[k]);
+                else store_end(h_row, col0, p.d, p.wide, pack(v[k]));
             }
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
@@ -171,7 +213,7 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_ke
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
-            if (FULL ? col0 < p.d : col0 >= 0 && col0 + 8 <= p.d) {
+            if (FULL ? col0 < p.d : col0 >= 0 && col0 + 8 <= p.d) {  // (also where rows are not wide)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) squares = fmaf(v[k][i] - mean, v[k][i] - mean, squares);
             } else if (!FULL) {
@@ -215,8 +257,8 @@ __global__ void __maxnreg__(V == 4 ? 128 : DROP || FULL ? 80 : 64) layer_norm_ke
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[k][i] = fmaf((v[k][i] - mean) * rstd, w[i], b[i]);
             }
-            if (FULL) *reinterpret_cast<uint4*>(y_row + col0) = pack(v[k]);
-            else store_chunk(y_row, col0, p.d, p.wide, pack(v[k]));
+            if (whole(col0)) *reinterpret_cast<uint4*>(y_row + col0) = pack(v[k]);
+            else store_end(y_row, col0, p.d, p.wide, pack(v[k]));
         }
     }
 }
@@ -232,10 +274,11 @@ struct LayerNormBwdParams {
     const uint16_t* dh;   // the gradient that reaches h past the norm, or null
     uint16_t* dr;
     uint16_t* dx;         // dropout's: dr where kept, over 1 - p (or null)
-    float* partial;       // [gridDim.x][2][d]: each block's part of the weight's and the bias's gradient
+    float* partial;       // [gridDim.x][2][pitch]: each block's part of the weight's and the bias's gradient
     int64_t lddy, ldh, lddh, lddr, lddx;
     int m, d;
     int wide, wide_weight;
+    int pitch;            // columns of a row's chunks, its shift counted in
     Drop drop;
 };
 
@@ -245,14 +288,14 @@ struct LayerNormBwdParams {
 // registers from the first pass over a row to the second.  (With both made again from shared memory, and every chunk's
 // ends looked at, 8192 x 4096 took 700 instructions a warp's part of a row and 68 us.)
 // Dynamic shared memory: the rows [stage][dY, H or dH][chunk][thread], then the weight.
-__host__ __device__ constexpr int layer_bwd_stages(int v, bool full) { return full && v == 2 ? 3 : kBwdStages; }
+__host__ __device__ constexpr int layer_bwd_stages(int v) { return v == 2 ? 3 : kBwdStages; }
 
 template <int V, int DROP, bool FULL>
-__global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(const __grid_constant__ LayerNormBwdParams p) {
+__global__ void __maxnreg__(V == 4 || FULL ? 128 : 96) layer_norm_bwd_kernel(const __grid_constant__ LayerNormBwdParams p) {
     allow_next_kernel();
     wait_for_earlier_kernels();
-    constexpr int kStages = layer_bwd_stages(V, FULL);
-    constexpr bool kHeld = FULL && V == 2;  // g and xhat, and the weight, in registers
+    constexpr int kStages = layer_bwd_stages(V);
+    constexpr bool kXhat = V == 2, kHeld = FULL && V == 2;  // xhat; g and the weight in registers
     __shared__ float2 sums[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
     const int row0 = blockIdx.x * blockDim.y + threadIdx.y, stride = gridDim.x * blockDim.y;
@@ -261,9 +304,11 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
     uint4* slots = reinterpret_cast<uint4*>(smem) + threadIdx.y * threads + tid;
     uint4* weight = slots + kStages * 3 * V * all;  // (the thread's own part of it)
     const Draw<DROP> draw(p.drop);
+    // a chunk that lies in the row whole (a thread's chunks do so in all its rows, or in none)
+    auto whole = [&](int col0) { return FULL ? col0 < p.d : p.wide && col0 >= 0 && col0 + 8 <= p.d; };
     auto slot = [&](int stage, int matrix, int k) { return slots + ((stage * 3 + matrix) * V + k) * all; };
     auto chunk = [&](int stage, int matrix, int k, int col0) {
-        return FULL ? *slot(stage, matrix, k) : read_chunk(slot(stage, matrix, k), col0);
+        return FULL || col0 >= 0 ? *slot(stage, matrix, k) : read_chunk(slot(stage, matrix, k), col0);
     };
     const uint16_t *dy_next = p.dy + row0 * p.lddy, *h_next = p.h + row0 * p.ldh, *dh_next = p.dh + row0 * p.lddh;
     auto fetch = [&](int64_t row, int stage) {
@@ -271,13 +316,11 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int col0 = 8 * (tid + k * threads) - shift;
-                if (FULL) {
-                    if (col0 < p.d) {
-                        fetch_16(slot(stage, 0, k), dy_next + col0);
-                        fetch_16(slot(stage, 1, k), h_next + col0);
-                        if (p.dh) fetch_16(slot(stage, 2, k), dh_next + col0);
-                    }
-                } else {
+                if (whole(col0)) {
+                    fetch_16(slot(stage, 0, k), dy_next + col0);
+                    fetch_16(slot(stage, 1, k), h_next + col0);
+                    if (p.dh) fetch_16(slot(stage, 2, k), dh_next + col0);
+                } else if (!FULL && col0 < p.d) {
                     fetch_chunk(slot(stage, 0, k), dy_next, col0, p.d, p.wide, row > 0 && p.lddy >= 8);
                     fetch_chunk(slot(stage, 1, k), h_next, col0, p.d, p.wide, row > 0 && p.ldh >= 8);
                     if (p.dh) fetch_chunk(slot(stage, 2, k), dh_next, col0, p.d, p.wide, row > 0 && p.lddh >= 8);
@@ -294,7 +337,7 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
     float dw[V][8], db[V][8], held[kHeld ? V : 1][8];
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-        const uint4 w = load_chunk(p.weight, 8 * (tid + k * threads) - shift, p.d, shift == 0 && p.wide_weight);
+        const uint4 w = load_vector(p.weight, 8 * (tid + k * threads) - shift, p.d, p.wide_weight);
         if constexpr (kHeld) unpack(w, held[k]);
         else weight[k * all] = w;
 #pragma unroll
@@ -310,11 +353,11 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
         fetch(r + static_cast<int64_t>(kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
         fetch_wait<kStages - 1>();
         float sum = 0.f, dot = 0.f;  // of g and of g xhat
-        float g[kHeld ? V : 1][8], xhat[kHeld ? V : 1][8];
+        float g[kHeld ? V : 1][8], xhat[kXhat ? V : 1][8];
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
-            if (FULL && col0 >= p.d) continue;
+            if (col0 >= p.d) continue;
             float t[8], h[8], w[8];
             unpack(chunk(stage, 0, k, col0), t);  // (outside the row dY is zero, and adds nothing)
             unpack(chunk(stage, 1, k, col0), h);
@@ -331,7 +374,8 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
                 sum += gi;
                 dot = fmaf(gi, xi, dot);
                 dw[k][i] = fmaf(t[i], xi, dw[k][i]);
-                if constexpr (kHeld) g[k][i] = gi, xhat[k][i] = xi;
+                if constexpr (kHeld) g[k][i] = gi;
+                if constexpr (kXhat) xhat[k][i] = xi;
             }
         }
         const float2 total = row_sum2(sum, dot, half, sums[turn]);
@@ -346,10 +390,17 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
                 for (int i = 0; i < 8; ++i) v[i] = g[k][i] - fmaf(xhat[k][i], mean_gx, mean_g);
             } else {
                 unpack(chunk(stage, 0, k, col0), v);
-                unpack(chunk(stage, 1, k, col0), h);
                 unpack(weight[k * all], w);
+                if constexpr (kXhat) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] - fmaf((h[i] - mean) * rstd, mean_gx, mean_g);
+                    for (int i = 0; i < 8; ++i) h[i] = xhat[k][i];
+                } else {
+                    unpack(chunk(stage, 1, k, col0), h);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = (h[i] - mean) * rstd;
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] - fmaf(h[i], mean_gx, mean_g);
             }
             if (p.dh) {
                 unpack(chunk(stage, 2, k, col0), h);
@@ -359,40 +410,30 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[i] *= rstd;
             }
-            if (FULL) *reinterpret_cast<uint4*>(dr_row + col0) = pack(v);
-            else store_chunk(dr_row, col0, p.d, p.wide, pack(v));
+            if (whole(col0)) *reinterpret_cast<uint4*>(dr_row + col0) = pack(v);
+            else store_end(dr_row, col0, p.d, p.wide, pack(v));
             if (DROP) {
                 draw.chunk(v, row, col0);
-                if (FULL) *reinterpret_cast<uint4*>(dx_row + col0) = pack(v);
-                else store_chunk(dx_row, col0, p.d, p.wide, pack(v));
+                if (whole(col0)) *reinterpret_cast<uint4*>(dx_row + col0) = pack(v);
+                else store_end(dx_row, col0, p.d, p.wide, pack(v));
             }
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
     }
     fetch_wait<0>();
 
-    float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.d;
+    float* part = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.pitch;
     if (blockDim.y == 1) {
+        // as the chunks lie: the join moves them by the block's shift.  (What is outside the row is not read.)
 #pragma unroll
         for (int k = 0; k < V; ++k) {
-            const int col0 = 8 * (tid + k * threads) - shift;
-            if (FULL && (reinterpret_cast<uintptr_t>(p.partial) & 15) == 0) {
-                if (col0 >= p.d) continue;
+            const int at = 8 * (tid + k * threads);
+            if (at >= p.pitch) continue;
 #pragma unroll
-                for (int i = 0; i < 8; i += 4) {
-                    *reinterpret_cast<float4*>(part + col0 + i) = make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
-                    *reinterpret_cast<float4*>(part + p.d + col0 + i) =
-                        make_float4(db[k][i], db[k][i + 1], db[k][i + 2], db[k][i + 3]);
-                }
-                continue;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int col = col0 + i;
-                if (col >= 0 && col < p.d) {
-                    part[col] = dw[k][i];
-                    part[p.d + col] = db[k][i];
-                }
+            for (int i = 0; i < 8; i += 4) {
+                *reinterpret_cast<float4*>(part + at + i) = make_float4(dw[k][i], dw[k][i + 1], dw[k][i + 2], dw[k][i + 3]);
+                *reinterpret_cast<float4*>(part + p.pitch + at + i) =
+                    make_float4(db[k][i], db[k][i + 1], db[k][i + 2], db[k][i + 3]);
             }
         }
         return;
@@ -416,20 +457,25 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 80) layer_norm_bwd_kernel(con
             }
     }
     __syncthreads();
-    for (int c = threadIdx.y * 32 + tid; c < 2 * p.d; c += 32 * blockDim.y) part[c] = total[c];
+    for (int c = threadIdx.y * 32 + tid; c < p.d; c += 32 * blockDim.y) {
+        part[c] = total[c];
+        part[p.pitch + c] = total[p.d + c];
+    }
 }
 
-// The sums of the blocks' parts of both gradients, as join_kernel's.
-__global__ void __launch_bounds__(kJoinColumns * kJoinParts) join2_kernel(const float* partial, int parts, int d,
-                                                                          float* dweight, float* dbias) {
+// The sums of the blocks' parts of both gradients, as join_kernel's.  Column c of block b's part is at c + shift, where
+// shift is row b's in the matrices: (first + b step) mod 8.
+__global__ void __launch_bounds__(kJoinColumns * kJoinParts) join2_kernel(const float* partial, int parts, int d, int pitch,
+                                                                          int first, int step, float* dweight, float* dbias) {
     allow_next_kernel();
     wait_for_earlier_kernels();
     __shared__ float sum[kJoinParts][kJoinColumns + 1];
     const int c = blockIdx.x * kJoinColumns + threadIdx.x;
     float v = 0.f;
     if (c < 2 * d) {
+        const float* from = partial + (c < d ? c : c - d + pitch);
 #pragma unroll 8
-        for (int i = threadIdx.y; i < parts; i += kJoinParts) v += partial[static_cast<int64_t>(i) * 2 * d + c];
+        for (int i = threadIdx.y; i < parts; i += kJoinParts) v += from[static_cast<int64_t>(i) * 2 * pitch + ((first + i * step) & 7)];
     }
     sum[threadIdx.y][threadIdx.x] = v;
     __syncthreads();

@@ -191,6 +191,11 @@ int64_t bwd_workspace(int64_t m, int64_t d, int sms) {
 
 // ---------------------------------------------------------------- layer norm
 
+// A row's columns in the parts of its two gradients: whole chunks, a shift counted in.
+int64_t layer_bwd_pitch(int64_t d) { return ceil_div(d + 7, 8) * 8; }
+
+int64_t layer_bwd_workspace(int64_t m, int64_t d, int sms) { return bwd_workspace(m, d, sms) / d * layer_bwd_pitch(d) * 2; }
+
 // Whether every row of the matrices is whole, aligned 16-byte words.
 template <size_t N>
 bool full_rows(const Mat (&mats)[N], int64_t rows, int64_t cols) {
@@ -206,8 +211,8 @@ gb_status_t launch_layer_norm(const LayerNormParams& p, const RowPlan& pl, int d
     static std::atomic<bool> ready[64];
     gb_status_t st = allow_smem(layer_norm_kernel<V, DROP, FULL>, ready, dev, info.smem_optin - 1024);
     if (st != GB_OK) return st;
-    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : DROP || FULL ? 768 : 1024, info.sms);
-    const size_t smem = static_cast<size_t>(layer_norm_stages(V) * 2 + (FULL && V == 2 ? 0 : 2)) * V * 16 * pl.threads * pl.rows;
+    const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : 768, info.sms);
+    const size_t smem = static_cast<size_t>(layer_norm_stages(V) * 2 + (V == 2 ? 0 : 2)) * V * 16 * pl.threads * pl.rows;
     note_plan("kernel=add_layer_norm dropout=%lld threads=%lld rows=%lld blocks=%lld wide=%lld full=%lld", DROP,
               pl.threads, pl.rows, blocks, pl.wide, FULL);
     return Launch(static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream)(
@@ -231,9 +236,9 @@ gb_status_t launch_layer_bwd(const LayerNormBwdParams& p, const RowPlan& pl, int
     gb_status_t st = allow_smem(layer_norm_bwd_kernel<V, DROP, FULL>, ready, dev, info.smem_optin - 1024);
     if (st != GB_OK) return st;
     // the stages of three matrices, and the weight; and the join of a block's rows
-    size_t smem = static_cast<size_t>(layer_bwd_stages(V, FULL) * 3 + (FULL && V == 2 ? 0 : 1)) * V * 16 * pl.threads * pl.rows;
+    size_t smem = static_cast<size_t>(layer_bwd_stages(V) * 3 + (FULL && V == 2 ? 0 : 1)) * V * 16 * pl.threads * pl.rows;
     if (pl.rows > 1) smem = std::max(smem, static_cast<size_t>(p.d) * 8);
-    if (FULL && V == 2) *blocks = static_cast<int>(blocks_for(p.m, pl, 512, info.sms));  // (never more than without)
+    if (V == 2) *blocks = static_cast<int>(blocks_for(p.m, pl, FULL ? 512 : 576, info.sms));  // (the workspace has room for 768)
     return Launch(*blocks, dim3(pl.threads, pl.rows), smem, stream)("add_layer_norm_backward launch",
                                                                     layer_norm_bwd_kernel<V, DROP, FULL>, p);
 }
@@ -525,9 +530,17 @@ gb_status_t gb_add_layer_norm(const void* X, int64_t ldx, const void* R, int64_t
 }
 
 gb_status_t gb_add_layer_norm_backward_workspace_bytes(int64_t M, int64_t D, size_t* bytes) {
-    const gb_status_t st = gb_add_rms_norm_backward_workspace_bytes(M, D, bytes);
-    if (st == GB_OK) *bytes *= 2;  // (the parts of two gradients)
-    return st;
+    clear_error();
+    gb_status_t st;
+    if (!bytes) return fail(GB_ERR_INVALID_ARG, "bytes is null");
+    *bytes = 0;
+    if ((st = check_sizes(M, D)) != GB_OK) return st;
+    if (M == 0 || D == 0) return GB_OK;
+    int dev = 0;
+    DeviceInfo info;
+    if ((st = device_info(&dev, &info)) != GB_OK) return st;
+    *bytes = static_cast<size_t>(layer_bwd_workspace(M, D, info.sms));
+    return GB_OK;
 }
 
 gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh, const void* weight,
@@ -565,11 +578,11 @@ gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void*
     int blocks = 0;
     RowPlan pl;
     if (M > 0) {
-        const size_t need = 2 * static_cast<size_t>(bwd_workspace(M, D, info.sms));
+        const size_t need = static_cast<size_t>(layer_bwd_workspace(M, D, info.sms));
         if (!workspace || workspace_bytes < need)
             return fail(GB_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", workspace ? workspace_bytes : size_t(0),
                         need);
-        if (!aligned_to(workspace, 4)) return fail(GB_ERR_INVALID_ARG, "workspace must be 4-byte aligned");
+        if (!aligned_to(workspace, 16)) return fail(GB_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
         prm.dy = static_cast<const uint16_t*>(dY);
         prm.h = static_cast<const uint16_t*>(H);
         prm.weight = static_cast<const uint16_t*>(weight);
@@ -579,6 +592,7 @@ gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void*
         prm.dr = static_cast<uint16_t*>(dR);
         prm.dx = static_cast<uint16_t*>(dX);
         prm.partial = static_cast<float*>(workspace);
+        prm.pitch = static_cast<int>(layer_bwd_pitch(D));
         prm.lddy = lddy;
         prm.ldh = ldh;
         prm.lddh = lddh;
@@ -598,11 +612,15 @@ gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void*
         }
         if (st != GB_OK) return st;
     }
+    // (a block of several rows has joined them by column)
+    const bool shifted = prm.wide && pl.rows == 1;
+    const int first = shifted ? static_cast<int>(reinterpret_cast<uintptr_t>(dY) >> 1 & 7) : 0;
+    const int step = shifted ? static_cast<int>(lddy & 7) : 0;
     note_plan("kernel=add_layer_norm_backward blocks=%lld dropout=%lld threads=%lld rows=%lld chunks=%lld wide=%lld", blocks,
               drop, pl.threads, pl.rows, pl.chunks_per_thread, pl.wide);
     return Launch(static_cast<unsigned>(ceil_div(2 * D, kJoinColumns)), dim3(kJoinColumns, kJoinParts), 0, s)(
         "add_layer_norm_backward join launch", join2_kernel, static_cast<const float*>(workspace), blocks,
-        static_cast<int>(D), dweight, dbias);
+        static_cast<int>(D), prm.pitch, first, step, dweight, dbias);
 }
 
 }  // extern "C"

@@ -377,7 +377,7 @@ GB_API gb_status_t gb_add_layer_norm(const void* X, int64_t ldx, const void* R, 
  *
  * H, mean and rstd as gb_add_layer_norm gave them; dweight and dbias are both written whole (zeros if M == 0).
  * The other arguments, the order of sums and the allowed overlaps are as gb_add_rms_norm_backward's; the
- * workspace is of at least gb_add_layer_norm_backward_workspace_bytes().
+ * workspace is 16-byte aligned and of at least gb_add_layer_norm_backward_workspace_bytes().
  */
 GB_API gb_status_t gb_add_layer_norm_backward(const void* dY, int64_t lddy, const void* H, int64_t ldh,
                                               const void* weight, const float* mean, const float* rstd, const void* dH,

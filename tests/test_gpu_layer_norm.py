@@ -183,19 +183,28 @@ def test_the_workspace_is_checked_and_any_contents_do():
     h, w, dy = normal(m, d, seed=1), normal(d, seed=2), normal(m, d, seed=3)
     _, _, mean, rstd = gb.add_layer_norm(h, w)
     need = gb.add_layer_norm_backward_workspace_bytes(m, d)
-    assert need == 2 * gb.add_rms_norm_backward_workspace_bytes(m, d)
     check_backward(dy, h, w, mean, rstd, None, workspace=torch.full((need,), 255, dtype=torch.uint8, device=DEV))
     with pytest.raises(ValueError, match="workspace"):
         gb.add_layer_norm_backward(dy, h, w, mean, rstd, workspace=torch.empty(need - 1, dtype=torch.uint8, device=DEV))
 
 
-@pytest.mark.parametrize("m,d", [(9, 64), (20, 4096), (3, 16384)])
-def test_a_workspace_that_begins_anywhere(m, d):
+@pytest.mark.parametrize("m,d", [(9, 64), (20, 4096), (3, 16384), (40, 4099)])
+def test_a_workspace_that_begins_anywhere_is_refused_or_does(m, d):
     h, w, dy = normal(m, d, seed=1), normal(d, seed=2), normal(m, d, seed=3)
     _, _, mean, rstd = gb.add_layer_norm(h, w)
     need = gb.add_layer_norm_backward_workspace_bytes(m, d)
-    for offset in (0, 4, 8):
-        check_backward(dy, h, w, mean, rstd, None, workspace=torch.empty(need + 16, dtype=torch.uint8, device=DEV)[offset:])
+    room = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
+    check_backward(dy, h, w, mean, rstd, None, workspace=room[16:])
+    with pytest.raises(gb.GBError, match="16-byte"):
+        check_backward(dy, h, w, mean, rstd, None, workspace=room[4:])
+
+
+@pytest.mark.parametrize("m,d", [(700, 600), (700, 4099), (1300, 1031), (40, 16383)])
+def test_many_blocks_with_shifts_of_their_own(m, d):
+    """The gradients' parts lie as each block's rows do."""
+    h, w, dy = padded(normal(m, d, seed=1), 5, 3), normal(d, seed=2), padded(normal(m, d, seed=3), 5, 3)
+    _, _, mean, rstd = gb.add_layer_norm(h, w)
+    check_backward(dy, h, w, mean, rstd, padded(normal(m, d, seed=4), 5, 3))
 
 
 def test_wrong_tensors_are_refused():
