@@ -120,7 +120,7 @@ __global__ void __maxnreg__(V == 4 ? 128 : 80) layer_norm_kernel(const __grid_co
     allow_next_kernel();
     wait_for_earlier_kernels();
     constexpr int kStages = layer_norm_stages(V);
-    constexpr bool kHeld = V == 2;  // the weight and the bias in registers
+    constexpr bool kHeld = FULL && V == 2;  // the weight and the bias in registers
     __shared__ float2 parts[2][32];
     __shared__ float2 counts[32];  // and one over them
     extern __shared__ __align__(16) uint8_t smem[];
@@ -295,7 +295,7 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 96) layer_norm_bwd_kernel(con
     allow_next_kernel();
     wait_for_earlier_kernels();
     constexpr int kStages = layer_bwd_stages(V);
-    constexpr bool kXhat = V == 2, kHeld = FULL && V == 2;  // xhat; g and the weight in registers
+    constexpr bool kXhat = V == 2 && (FULL || DROP == kNoDrop), kHeld = FULL && V == 2;  // xhat; g and the weight in registers
     __shared__ float2 sums[2][32];
     extern __shared__ __align__(16) uint8_t smem[];
     const int row0 = blockIdx.x * blockDim.y + threadIdx.y, stride = gridDim.x * blockDim.y;
@@ -313,6 +313,11 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 96) layer_norm_bwd_kernel(con
     const uint16_t *dy_next = p.dy + row0 * p.lddy, *h_next = p.h + row0 * p.ldh, *dh_next = p.dh + row0 * p.lddh;
     auto fetch = [&](int64_t row, int stage) {
         if (row < p.m) {
+            if (V == 4) {  // (fewer registers than addresses that move along)
+                dy_next = p.dy + row * p.lddy;
+                h_next = p.h + row * p.ldh;
+                dh_next = p.dh + row * p.lddh;
+            }
 #pragma unroll
             for (int k = 0; k < V; ++k) {
                 const int col0 = 8 * (tid + k * threads) - shift;
@@ -326,9 +331,11 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 96) layer_norm_bwd_kernel(con
                     if (p.dh) fetch_chunk(slot(stage, 2, k), dh_next, col0, p.d, p.wide, row > 0 && p.lddh >= 8);
                 }
             }
-            dy_next += stride * p.lddy;
-            h_next += stride * p.ldh;
-            dh_next += stride * p.lddh;
+            if (V == 2) {
+                dy_next += stride * p.lddy;
+                h_next += stride * p.ldh;
+                dh_next += stride * p.lddh;
+            }
         }
         fetch_commit();
     };
@@ -346,8 +353,7 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 96) layer_norm_bwd_kernel(con
     const float of_row = 1.f / static_cast<float>(p.d);
 
     int stage = 0, turn = 0;  // (of row_sum2's places)
-    uint16_t *dr_row = p.dr + row0 * p.lddr, *dx_row = p.dx + row0 * p.lddx;
-    for (int64_t r = row0; r < p.m; r += stride, turn ^= 1, dr_row += stride * p.lddr, dx_row += stride * p.lddx) {
+    for (int64_t r = row0; r < p.m; r += stride, turn ^= 1) {
         const int row = static_cast<int>(r);
         const float rstd = p.rstd[row], mean = p.mean[row];
         fetch(r + static_cast<int64_t>(kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
@@ -380,7 +386,8 @@ __global__ void __maxnreg__(V == 4 || FULL ? 128 : 96) layer_norm_bwd_kernel(con
         }
         const float2 total = row_sum2(sum, dot, half, sums[turn]);
         const float mean_g = total.x * of_row, mean_gx = total.y * of_row;
-#pragma unroll
+        uint16_t *dr_row = p.dr + r * p.lddr, *dx_row = p.dx + r * p.lddx;
+#pragma unroll(V == 4 ? 1 : V)  // (of four chunks, one at a time, for the registers)
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
             if (col0 >= p.d) continue;

@@ -41,19 +41,20 @@ int64_t workspace_of(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
 // with two blocks of columns a warp 34 us, with as many as all run at once 36, since those are not done together.)  Less
 // than 64 rows are requests of a token or a few, with adapters of their own as a rule: a tile each, and the blocks that
 // run at once (48 rows of 14336 columns, rank 64: 20 us; in tiles of 8 rows 24).
-Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t ld, int sms, bool shift) {
+Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t ldx, int64_t ld, int sms, bool shift) {
     Plan pl;
     const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), rows = turn_rows(r <= 16 ? 1 : 2);
     pl.cluster = 1;
     while (pl.cluster < 8 && pl.cluster * kWarps < steps) pl.cluster *= 2;
     while (pl.cluster > 1 && ceil_div(M, slots / pl.cluster) > rows) pl.cluster /= 2;
     pl.down_tile = static_cast<int>(std::min(rows, ceil_div(M, slots / pl.cluster)));
+    while (pl.down_tile > 1 && pl.down_tile * ldx > kMaxDim) pl.down_tile /= 2;  // (the kernels' distances within a tile)
     pl.down_blocks = ceil_div(M, pl.down_tile) * pl.cluster;
     const int64_t turns = ceil_div(N, kWarps * kColumns), pairs = ceil_div(turns, 2);
-    const int64_t places = (shift || low_columns(r) > 32 ? 2 : 3) * sms;
+    const int64_t places = (shift || r > 16 ? 2 : 3) * sms;
     pl.up_tile = kMaxTile;
     while (pl.up_tile > 1 && ceil_div(M, pl.up_tile) * turns * 5 < places * 4) pl.up_tile /= 2;
-    while (pl.up_tile > 1 && pl.up_tile * ld > kMaxDim) pl.up_tile /= 2;  // (the kernel's distances within a tile)
+    while (pl.up_tile > 1 && pl.up_tile * ld > kMaxDim) pl.up_tile /= 2;
     if (M < kMaxTile) pl.up_tile = 1;
     const int64_t up_tiles = ceil_div(M, pl.up_tile);
     pl.parts = static_cast<int>(up_tiles * pairs >= 2 * places ? pairs : turns);
@@ -123,12 +124,14 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
                             "%s: adapters %" PRId64 " elements apart (a multiple of 8, and at least a matrix)", m.name, m.apart);
         }
     }
+    if (any && (r - 1) * lda + K > kMaxDim)  // (distances within a matrix are counted in 32 bits)
+        return fail(GB_ERR_UNSUPPORTED, "A: %" PRId64 " rows %" PRId64 " elements apart are more than 2^31 elements", r, lda);
     int dev = 0;
     DeviceInfo info;
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
     const bool wide_r = aligned_to(R, 16) && (M == 1 || ldr % 8 == 0), wide_d = aligned_to(D, 16) && (M == 1 || ldd % 8 == 0);
     const bool shift = !(wide_d && (wide_r || !R));  // rows start anywhere
-    const Plan pl = make_plan(M, N, K, r, std::max(ldd, R ? ldr : 0), info.sms, shift);
+    const Plan pl = make_plan(M, N, K, r, any ? ldx : 0, std::max(ldd, R ? ldr : 0), info.sms, shift);
     if (pl.down_blocks > kMaxDim || pl.up_blocks > kMaxDim)
         return fail(GB_ERR_UNSUPPORTED, "%" PRId64 " rows of %" PRId64 " columns are more than a launch's blocks", M, N);
     const size_t need = any ? static_cast<size_t>(workspace_of(M, r)) : 0;

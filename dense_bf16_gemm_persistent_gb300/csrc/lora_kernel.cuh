@@ -124,25 +124,26 @@ __device__ __forceinline__ void make_order(Order& o, const Params& p, int64_t ro
 template <int MT, int NT, int ADAPTERS>
 __device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p, const Order& o, int64_t row0, int rank0,
                                           int unit0, int units, int first, int by) {
-    constexpr int kOf = 2 * MT * ADAPTERS + NT, kUnroll = kOf <= 4 ? 4 : kOf <= 8 ? 2 : 1;
+    constexpr int kOf = 2 * MT * ADAPTERS + NT, kUnroll = kOf <= 4 ? 4 : kOf < 8 ? 2 : 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     // (ranks beyond the last are the last's, rows the unit's first's, units the last's: their sums are not used)
-    const uint16_t* a[ADAPTERS][2 * MT];
-    const uint16_t* x[NT];
+    // (distances within a tile's rows and within an adapter's matrix are within 32 bits: the host sees to it)
+    const uint16_t *a[ADAPTERS], *tile = p.x + row0 * p.ldx + 8 * q;
+    uint32_t a_at[2 * MT], x[NT];
     int cut = NT;  // of two adapters: the second's first unit
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int unit = unit0 + min(t, units - 1), place = o.start[unit] + g;
-        x[t] = p.x + (row0 + o.row[place < o.start[unit + 1] ? place : place - g]) * p.ldx + 8 * q;
+        x[t] = o.row[place < o.start[unit + 1] ? place : place - g] * static_cast<uint32_t>(p.ldx);
         if (ADAPTERS == 2 && o.adapter(unit) != o.adapter(unit0)) cut = min(cut, t);
     }
 #pragma unroll
     for (int t = 0; t < ADAPTERS; ++t) {
         const int unit = unit0 + min(ADAPTERS == 2 && t ? cut : t, units - 1);
-#pragma unroll
-        for (int i = 0; i < 2 * MT; ++i)
-            a[t][i] = p.a + o.adapter(unit) * p.apart_a + min(rank0 + g + 8 * i, p.rank - 1) * p.lda + 8 * q;
+        a[t] = p.a + o.adapter(unit) * p.apart_a + 8 * q;
     }
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) a_at[i] = min(rank0 + g + 8 * i, p.rank - 1) * static_cast<uint32_t>(p.lda);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -175,10 +176,10 @@ __device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p
 #pragma unroll
             for (int t = 0; t < ADAPTERS; ++t)
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) u[j][t][i] = *reinterpret_cast<const uint4*>(a[t][i] + col);
+                for (int i = 0; i < 2 * MT; ++i) u[j][t][i] = *reinterpret_cast<const uint4*>(a[t] + a_at[i] + col);
 #pragma unroll
             for (int t = 0; t < NT; ++t)   // (up to 16 ranks X is read by one warp only)
-                v[j][t] = MT == 1 ? load_once(x[t] + col) : *reinterpret_cast<const uint4*>(x[t] + col);
+                v[j][t] = MT == 1 ? load_once(tile + x[t] + col) : *reinterpret_cast<const uint4*>(tile + x[t] + col);
         }
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j)
@@ -190,9 +191,9 @@ __device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p
 #pragma unroll
         for (int t = 0; t < ADAPTERS; ++t)
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) u[t][i] = load_edge(a[t][i], col, left);
+            for (int i = 0; i < 2 * MT; ++i) u[t][i] = load_edge(a[t] + a_at[i], col, left);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) v[t] = load_edge(x[t], col, left);
+        for (int t = 0; t < NT; ++t) v[t] = load_edge(tile + x[t], col, left);
         add(u, v);
     }
 }
@@ -428,7 +429,7 @@ struct __align__(16) RowAt {
 // measurement, the mma, S's loads and B's took 8 % together, R's 40 %, D's 25 %.  Four units at a time in twice the
 // registers took as long, and so did R and B fetched four turns ahead to a ring in shared memory.
 template <int RS, int STEPS, bool SHIFT>
-__global__ void __launch_bounds__(kThreads, STEPS == 1 && !SHIFT ? 3 : 2) up_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kernel(const __grid_constant__ Params p) {
     constexpr int kBatch = 2;
     allow_next_kernel();
     wait_for_earlier_kernels();

@@ -212,7 +212,7 @@ gb_status_t launch_layer_norm(const LayerNormParams& p, const RowPlan& pl, int d
     gb_status_t st = allow_smem(layer_norm_kernel<V, DROP, FULL>, ready, dev, info.smem_optin - 1024);
     if (st != GB_OK) return st;
     const int64_t blocks = blocks_for(p.m, pl, V == 4 ? 512 : 768, info.sms);
-    const size_t smem = static_cast<size_t>(layer_norm_stages(V) * 2 + (V == 2 ? 0 : 2)) * V * 16 * pl.threads * pl.rows;
+    const size_t smem = static_cast<size_t>(layer_norm_stages(V) * 2 + (FULL && V == 2 ? 0 : 2)) * V * 16 * pl.threads * pl.rows;
     note_plan("kernel=add_layer_norm dropout=%lld threads=%lld rows=%lld blocks=%lld wide=%lld full=%lld", DROP,
               pl.threads, pl.rows, blocks, pl.wide, FULL);
     return Launch(static_cast<unsigned>(blocks), dim3(pl.threads, pl.rows), smem, stream)(

@@ -189,6 +189,7 @@ def lora(L, X=P16, ldx=64, A=P16, lda=64, aa=512, B=P16, ldb=8, ab=256, ids=P16,
     (dict(lda=60), GB_ERR_INVALID_ARG, "of A"),
     (dict(B=P4), GB_ERR_UNSUPPORTED, "B"),
     (dict(ldb=12), GB_ERR_UNSUPPORTED, "B"),
+    (dict(lda=1 << 30, aa=1 << 34), GB_ERR_UNSUPPORTED, "2^31 elements"),
     (dict(aa=504), GB_ERR_INVALID_ARG, "A"),
     (dict(ab=260), GB_ERR_UNSUPPORTED, "B"),
     (dict(ldd=31), GB_ERR_INVALID_ARG, "of D"),
