@@ -25,13 +25,16 @@ gb_status_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adap
 }
 
 struct Plan {
+    bool sorted;
     int down_tile, cluster, up_tile, parts;
     int64_t down_blocks, up_blocks;
 };
 
 int64_t low_columns(int64_t r) { return r <= 16 ? 16 : ceil_div(r, 32) * 32; }
 
-int64_t workspace_of(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
+// S's terms; of sorted rows their tiles (a row each at most, and one before them) and their order.
+int64_t low_bytes(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
+int64_t workspace_of(int64_t M, int64_t r) { return low_bytes(M, r) + (M >= kMaxTile ? 16 * (M + 1) + 4 * M : 0); }
 
 // The product down to the rank: X's columns are shared out to a cluster, down to a step for each of its warps, and the
 // rows so that all blocks run at once (two an SM), with as many rows as a turn takes at most.  The product up to D:
@@ -41,8 +44,22 @@ int64_t workspace_of(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
 // with two blocks of columns a warp 34 us, with as many as all run at once 36, since those are not done together.)  Less
 // than 64 rows are requests of a token or a few, with adapters of their own as a rule: a tile each, and the blocks that
 // run at once (48 rows of 14336 columns, rank 64: 20 us; in tiles of 8 rows 24).
-Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t ldx, int64_t ld, int sms, bool shift) {
+Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int64_t ldx, int64_t ld, int sms, bool shift) {
     Plan pl;
+    // (sorted rows are counted from the matrix's first: its distances are within 32 bits)
+    pl.sorted = adapters > 0 && M >= kMaxTile && adapters <= kMaxSorted && M * std::max(ldx, ld) <= kMaxDim;
+    if (pl.sorted) {
+        const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), turns = ceil_div(N, kWarps * kColumns);
+        const int64_t places = (shift || r > 16 ? 2 : 3) * sms;
+        pl.down_tile = pl.up_tile = 8 * turn_units(r <= 16 ? 1 : 2);
+        // (how many tiles there are is known on the GPU only; half of the adapters' last ones are counted here)
+        const int64_t most = ceil_div(M, pl.up_tile) + std::min(adapters, M), likely = ceil_div(M, pl.up_tile) + std::min(adapters, M) / 2;
+        pl.cluster = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, ceil_div(steps, kWarps), slots / likely})));
+        pl.down_blocks = std::min(most, std::max<int64_t>(1, slots / pl.cluster)) * pl.cluster;
+        pl.parts = static_cast<int>(likely * ceil_div(turns, 2) >= 2 * places ? ceil_div(turns, 2) : turns);
+        pl.up_blocks = std::min((most + 1) * pl.parts, places);
+        return pl;
+    }
     const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), rows = turn_rows(r <= 16 ? 1 : 2);
     pl.cluster = 1;
     while (pl.cluster < 8 && pl.cluster * kWarps < steps) pl.cluster *= 2;
@@ -126,12 +143,13 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     }
     if (any && (r - 1) * lda + K > kMaxDim)  // (distances within a matrix are counted in 32 bits)
         return fail(GB_ERR_UNSUPPORTED, "A: %" PRId64 " rows %" PRId64 " elements apart are more than 2^31 elements", r, lda);
+    if (any && kColumns * ldb > kMaxDim) return fail(GB_ERR_UNSUPPORTED, "leading dimension %" PRId64 " of B: below 2^26", ldb);
     int dev = 0;
     DeviceInfo info;
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
     const bool wide_r = aligned_to(R, 16) && (M == 1 || ldr % 8 == 0), wide_d = aligned_to(D, 16) && (M == 1 || ldd % 8 == 0);
     const bool shift = !(wide_d && (wide_r || !R));  // rows start anywhere
-    const Plan pl = make_plan(M, N, K, r, any ? ldx : 0, std::max(ldd, R ? ldr : 0), info.sms, shift);
+    const Plan pl = make_plan(M, N, K, r, any ? adapters : 0, any ? ldx : 0, std::max(ldd, R ? ldr : 0), info.sms, shift);
     if (pl.down_blocks > kMaxDim || pl.up_blocks > kMaxDim)
         return fail(GB_ERR_UNSUPPORTED, "%" PRId64 " rows of %" PRId64 " columns are more than a launch's blocks", M, N);
     const size_t need = any ? static_cast<size_t>(workspace_of(M, r)) : 0;
@@ -165,6 +183,15 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     prm.cluster = pl.cluster;
     prm.parts = pl.parts;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (pl.sorted) {
+        int4* tiles = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + low_bytes(M, r));
+        int32_t* order = reinterpret_cast<int32_t*>(tiles + M + 1);
+        prm.tile = pl.down_tile;
+        st = Launch(1, kSortThreads, (adapters + 1) * sizeof(int), s)("lora sort launch", sort_kernel, prm, tiles, order);
+        if (st != GB_OK) return st;
+        prm.tiles = tiles;
+        prm.order = order;
+    }
     if (any) {
         const int tiles = r <= 16 ? 1 : 2;
         prm.teams = 1;
@@ -178,8 +205,8 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
         if (st != GB_OK) return st;
     }
     prm.tile = pl.up_tile;
-    note_plan("kernel=lora down_tile=%lld cluster=%lld down_blocks=%lld up_tile=%lld up_blocks=%lld shifted=%lld", pl.down_tile,
-              pl.cluster, any ? pl.down_blocks : 0, pl.up_tile, pl.up_blocks, shift);
+    note_plan("kernel=lora sorted=%lld tile=%lld cluster=%lld down_blocks=%lld up_blocks=%lld shifted=%lld", pl.sorted,
+              pl.down_tile, pl.cluster, any ? pl.down_blocks : 0, pl.up_blocks, shift);
     const UpKernel kernel = shift ? up_kernel_for<true>(prm.ldlow) : up_kernel_for<false>(prm.ldlow);
     if (prm.ldlow > 64) {  // (less is within what any kernel may have)
         static std::atomic<bool> ready[2][64];

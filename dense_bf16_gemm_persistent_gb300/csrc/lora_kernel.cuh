@@ -2,10 +2,11 @@
 //
 //   D[m] = act( R[m] + s[a] B[a] (A[a] X[m]) )      a = ids[m], none where it is outside 0 .. adapters - 1
 //
-// Two launches: down to the rank (S = X A^T, the columns split over CTAs), and up to D.  Rows come in any order:
-// each CTA takes a tile of consecutive rows and sorts it by adapter for itself, so that rows of one adapter
-// share its matrices' fragments and no launch is spent on an order of the whole batch.  Both are bound by memory:
-// X, R and D once, and the adapters' matrices.
+// Two launches: down to the rank (S = X A^T, the columns split over CTAs), and up to D.  Rows come in any order, and
+// rows of one adapter share its matrices' fragments.  Few rows: each CTA takes a tile of consecutive ones and sorts it by
+// adapter for itself.  64 and more: a launch before the two sorts them all, and a tile has rows of one adapter.  (A tile
+// in which two requests meet takes a turn for each, and the launch waits for it: 1000 rows of 30 requests, with tiles
+// of consecutive rows, 49 us.)  Both products are bound by memory: X, R and D once, and the adapters' matrices.
 #pragma once
 
 #include <type_traits>
@@ -40,7 +41,98 @@ struct Params {
     int tile;                // rows of a tile (of the launch at hand)
     int parts;               // CTAs of a tile that share the columns of D
     int teams;               // of a CTA's warps: 16 or 32 ranks each
+    // of sorted rows (else null): {tiles whose rows have an adapter, all tiles}, then the tiles; the rows in order
+    const int4* tiles;
+    const int32_t* order;
 };
+
+// A tile of sorted rows.
+__device__ __forceinline__ int4 tile_of(int adapter, int start, int count) { return make_int4(adapter, start, count, 0); }
+
+// ---------------------------------------------------------------- all rows by adapter
+
+constexpr int kSortThreads = 1024, kSortBatch = 8, kMaxSorted = 8191;  // adapters: a counter each in shared memory
+
+// A count of the rows of each adapter (and of those without one), the starts, and each row to its adapter's next
+// place.  Which place is its own decides nothing: a row's result does not depend on where in a tile it stands.
+__global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constant__ Params p, int4* tiles, int32_t* order) {
+    allow_next_kernel();
+    wait_for_earlier_kernels();
+    extern __shared__ int next[];  // of an adapter: its rows, then their next place
+    __shared__ int sums[32][2];
+    const int tid = threadIdx.x, lane = tid & 31, bins = p.adapters + 1;
+    for (int i = tid; i < bins; i += kSortThreads) next[i] = 0;
+    __syncthreads();
+    // A batch of rows from `base` on: their adapters' counters, and each row's place among its adapter's.  (The lanes of
+    // one adapter as one: rows of a request lie together.)
+    int key[kSortBatch], place[kSortBatch];
+    auto count_rows = [&](int64_t base) {
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) {
+            const int64_t row = base + u * kSortThreads + tid;
+            const int id = row < p.m ? p.ids[row] : 0;
+            key[u] = row >= p.m ? -1 : id >= 0 && id < p.adapters ? id : p.adapters;
+        }
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) {
+            if (base + u * kSortThreads >= p.m) break;
+            const uint32_t same = __match_any_sync(0xffffffffu, key[u]);
+            const int leader = __ffs(same) - 1;
+            int at = 0;
+            if (key[u] >= 0 && lane == leader) at = atomicAdd(&next[key[u]], __popc(same));
+            place[u] = __shfl_sync(0xffffffffu, at, leader) + __popc(same & ((1u << lane) - 1));
+        }
+    };
+    constexpr int kBatchRows = kSortThreads * kSortBatch;
+    for (int64_t base = 0; base < p.m; base += kBatchRows) count_rows(base);
+    __syncthreads();
+    // the starts, and the tiles: a thread to a part of the counters
+    const int per = (bins + kSortThreads - 1) / kSortThreads, first = min(tid * per, bins), last = min(first + per, bins);
+    int rows = 0, count = 0;
+    for (int i = first; i < last; ++i) {
+        rows += next[i];
+        count += (next[i] + p.tile - 1) / p.tile;
+    }
+    int rows_to = rows, count_to = count;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+        const int a = __shfl_up_sync(0xffffffffu, rows_to, i), b = __shfl_up_sync(0xffffffffu, count_to, i);
+        if (lane >= i) rows_to += a, count_to += b;
+    }
+    if (lane == 31) sums[tid >> 5][0] = rows_to, sums[tid >> 5][1] = count_to;
+    __syncthreads();
+    if (tid < 32) {
+        int a = sums[tid][0], b = sums[tid][1];
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+            const int c = __shfl_up_sync(0xffffffffu, a, i), d = __shfl_up_sync(0xffffffffu, b, i);
+            if (lane >= i) a += c, b += d;
+        }
+        sums[tid][0] = a, sums[tid][1] = b;
+    }
+    __syncthreads();
+    int start = rows_to - rows, tile = count_to - count;
+    if (tid >= 32) start += sums[(tid >> 5) - 1][0], tile += sums[(tid >> 5) - 1][1];
+    for (int i = first; i < last; ++i) {
+        const int n = next[i];
+        if (i == p.adapters) tiles[0] = make_int4(tile, tile + (n + p.tile - 1) / p.tile, 0, 0);
+        next[i] = start;
+        for (int at = 0; at < n; at += p.tile)
+            tiles[1 + tile++] = tile_of(i < p.adapters ? i : -1, start + at, min(p.tile, n - at));
+        start += n;
+    }
+    __syncthreads();
+    // (a batch that is the only one is known already; else the places are counted again, from the starts)
+    for (int64_t base = 0; base < p.m; base += kBatchRows) {
+        const bool again = p.m > kBatchRows;
+        if (again) count_rows(base);
+#pragma unroll
+        for (int u = 0; u < kSortBatch; ++u) {
+            const int64_t row = base + u * kSortThreads + tid;
+            if (row < p.m) order[again ? place[u] : next[key[u]] + place[u]] = static_cast<int>(row);
+        }
+    }
+}
 
 // Where the terms of rank j of a row of S are, of RS ranks a step of the product up to D (16, or 32 beyond 16 ranks):
 // a lane's quarter of a step lies together, first terms and second terms.
@@ -57,15 +149,39 @@ struct Order {
     int row[kMaxTile];         // in order: rows of one adapter together, those without one last
     int start[kMaxTile + 1];   // the units' first places
     int units;
+    int ends;                  // bit 0: the matrix's first row is in the tile, bit 1: its last
     __device__ __forceinline__ int adapter(int unit) const { return id[start[unit]]; }  // -1: none
 };
 
-// By all threads of a block.
+// Tile `tile`, by all threads of a block: its first row (what o.row counts from) and how many it has.
 template <int UNIT>
-__device__ __forceinline__ void make_order(Order& o, const Params& p, int64_t row0, int rows) {
+__device__ __forceinline__ int64_t make_order(Order& o, const Params& p, int tile, int& rows) {
     __shared__ int given[kMaxTile];
     __shared__ bool begins[kMaxTile];  // (in order) a unit
     const int t = threadIdx.x;
+    if (p.tiles) {
+        const int4 sorted = p.tiles[1 + tile];
+        rows = sorted.z;
+        int ends = 0;
+        if (t < rows) {
+            const int row = p.order[sorted.y + t];
+            o.row[t] = row;
+            o.id[t] = sorted.x;
+            ends = (row == 0 ? 1 : 0) | (row == p.m - 1 ? 2 : 0);
+        }
+        const int units = (rows + UNIT - 1) / UNIT;
+        if (t <= units) o.start[t] = min(t * UNIT, rows);
+        const int any0 = __syncthreads_or(ends & 1), any1 = __syncthreads_or(ends & 2);
+        if (t == 0) {
+            o.units = units;
+            o.ends = (any0 ? 1 : 0) | (any1 ? 2 : 0);
+        }
+        __syncthreads();
+        return 0;
+    }
+    const int64_t row0 = static_cast<int64_t>(tile) * p.tile;
+    rows = static_cast<int>(min(static_cast<int64_t>(p.tile), p.m - row0));
+    if (t == 0) o.ends = (row0 == 0 ? 1 : 0) | (row0 + rows == p.m ? 2 : 0);
     int key = p.adapters, first = p.adapters;  // (without one: after all others)
     if (t < rows) {
         const int id = p.ids[row0 + t], id0 = p.ids[row0];
@@ -82,7 +198,7 @@ __device__ __forceinline__ void make_order(Order& o, const Params& p, int64_t ro
         if (t <= units) o.start[t] = min(t * UNIT, rows);
         if (t == 0) o.units = units;
         __syncthreads();
-        return;
+        return row0;
     }
     if (t < rows) {
         int less = 0, same = 0;
@@ -111,6 +227,7 @@ __device__ __forceinline__ void make_order(Order& o, const Params& p, int64_t ro
         }
     }
     __syncthreads();
+    return row0;
 }
 
 // ---------------------------------------------------------------- down to the rank
@@ -259,12 +376,20 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     __shared__ Order o;
     extern __shared__ __align__(16) float sums[];
     const int rank = blockIdx.x % p.cluster;
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.cluster) * p.tile;
-    make_order<8>(o, p, row0, static_cast<int>(min(static_cast<int64_t>(p.tile), p.m - row0)));
     constexpr int kMost = turn_units(MT);
+    __shared__ int next_tile;  // (here for the registers: it is wanted once a tile)
+    if (threadIdx.x == 0) next_tile = blockIdx.x / p.cluster;
+    int turn = 0;
+    for (;;) {
+    int rows;
+    __syncthreads();  // (the tile before has been read)
+    const int tile = next_tile, clusters = gridDim.x / p.cluster;
+    if (tile >= (p.tiles ? p.tiles[0].x : clusters)) break;
+    const int64_t row0 = make_order<8>(o, p, tile, rows);  // (by when all have read next_tile)
+    if (threadIdx.x == 0) next_tile = tile + clusters;
     int units = 0;  // with an adapter
     while (units < o.units && o.adapter(units) >= 0) ++units;
-    for (int unit = 0, turn = 0; unit < units; turn ^= 1) {
+    for (int unit = 0; unit < units; turn ^= 1) {
         int n = 0, two = 0;  // units of one adapter, and of two
         for (int i = unit, changes = 0; i < min(units, unit + kMost); ++i) {
             changes += i > unit && o.adapter(i) != o.adapter(i - 1);
@@ -291,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
             down_turn<MT, 8, 1>(p, o, sums, mine, row0, rank, unit, n);
         }
         unit += n;
+    }
     }
     cluster_sync();  // (the others may still read this CTA's sums)
 }
@@ -430,15 +556,21 @@ struct __align__(16) RowAt {
 // registers took as long, and so did R and B fetched four turns ahead to a ring in shared memory.
 template <int RS, int STEPS, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kernel(const __grid_constant__ Params p) {
-    constexpr int kBatch = 2;
+    constexpr int kBatch = SHIFT && STEPS != 1 ? 1 : 2;  // (units at once: for the registers)
     allow_next_kernel();
     wait_for_earlier_kernels();
     __shared__ Order o;
     __shared__ RowAt rows_at[kMaxTile * 16];
     extern __shared__ __align__(16) uint32_t low[];
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / p.parts) * p.tile;
-    const int rows = static_cast<int>(min(static_cast<int64_t>(p.tile), p.m - row0));
-    make_order<16>(o, p, row0, rows);
+    __shared__ int next_item;  // (here for the registers: it is wanted once an item)
+    if (threadIdx.x == 0) next_item = blockIdx.x;
+    for (;;) {
+    int rows;
+    __syncthreads();  // (the item before has been read)
+    const int item = next_item;
+    if (item >= (p.tiles ? p.tiles[0].y * p.parts : static_cast<int>(gridDim.x))) break;
+    const int64_t row0 = make_order<16>(o, p, item / p.parts, rows);  // (by when all have read next_item)
+    if (threadIdx.x == 0) next_item = item + gridDim.x;
     const int words = low_words(p.ldlow), chunks = p.ldlow / 4, units = o.units;
     for (int i = threadIdx.x; i < units * 16; i += kThreads) {
         const int end = o.start[i / 16 + 1], place = o.start[i / 16] + i % 16, at = min(place, end - 1);
@@ -454,41 +586,42 @@ __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kerne
     __syncthreads();
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const bool whole = p.rank == p.ldlow;
-    const int64_t step = static_cast<int64_t>(p.parts) * kWarps * kColumns;
+    // (of sorted rows, whose distances are the matrix's, 0)
     const uint16_t* r_tile = p.r + row0 * p.ldr;
     uint16_t* d_tile = p.d + row0 * p.ldd;
-    for (int64_t at64 = (static_cast<int64_t>(blockIdx.x % p.parts) * kWarps + warp) * kColumns; at64 < p.n; at64 += step) {
-        const int col0 = static_cast<int>(at64), col = col0 + 8 * q;
+    for (uint32_t at = (item % p.parts * kWarps + warp) * kColumns; at < static_cast<uint32_t>(p.n);
+         at += static_cast<uint32_t>(p.parts) * kWarps * kColumns) {  // (twice N is within 32 bits)
+        const int col0 = static_cast<int>(at), col = col0 + 8 * q;
         // Element by element: a block that is cut off, and, since rows that start anywhere are read in whole 16-byte
         // words, where those may begin before the matrix or end after it.
         const bool edge = col0 + kColumns > p.n ||
-                          (SHIFT && ((col0 == 0 && row0 == 0) || (col0 + kColumns + 8 > p.n && row0 + rows == p.m)));
-        int64_t b_at[4];  // (columns beyond the last are the last's)
+                          (SHIFT && ((col0 == 0 && (o.ends & 1)) || (col0 + kColumns + 8 > p.n && (o.ends & 2))));
+        uint32_t b_at[4];  // (columns beyond the last are the last's; the host keeps 32 rows of B within 32 bits)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) b_at[j] = min(col0 + 8 * (g >> 1) + 2 * j + (g & 1), p.n - 1) * p.ldb + RS / 4 * q;
+        for (int j = 0; j < 4; ++j)
+            b_at[j] = min(8 * (g >> 1) + 2 * j + (g & 1), p.n - 1 - col0) * static_cast<uint32_t>(p.ldb) + RS / 4 * q;
         for (int unit = 0, n; unit < units; unit += n) {
             const int adapter = o.adapter(unit);
-            n = unit + 1 < units && o.adapter(unit + 1) == adapter ? 2 : 1;
-            const RowAt* at = rows_at + 16 * unit + g;
+            n = kBatch == 2 && unit + 1 < units && o.adapter(unit + 1) == adapter ? 2 : 1;
+            const int here = 16 * unit + g;
             Row8<SHIFT> r[kBatch][2];
             auto load_r = [&](auto units_here) {
 #pragma unroll
                 for (int i = 0; i < decltype(units_here)::value; ++i)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) r[i][h].load(r_tile + at[16 * i + 8 * h].r + col);
+                    for (int h = 0; h < 2; ++h) r[i][h].load(r_tile + rows_at[here + 16 * i + 8 * h].r + col);
             };
             if (p.r && !edge) {
-                if (n == 2) load_r(std::integral_constant<int, 2>());
+                if (n == 2) load_r(std::integral_constant<int, kBatch>());
                 else load_r(std::integral_constant<int, 1>());
             } else if (p.r) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < 2 * n) r[i / 2][i % 2].a = load_cut(r_tile + at[8 * i].r + col, p.n - col);
+                for (int i = 0; i < 2 * kBatch; ++i)
+                    if (i < 2 * n) r[i / 2][i % 2].a = load_cut(r_tile + rows_at[here + 8 * i].r + col, p.n - col);
             }
-            const uint16_t* b = p.b + max(adapter, 0) * p.apart_b;
+            const uint16_t* b = p.b + (max(adapter, 0) * p.apart_b + col0 * p.ldb);
             auto load_b = [&](Words<RS>(&to)[4], int k0) {
-                if (whole) {
+                if (p.rank == p.ldlow) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) to[j] = load_words<RS, true>(b + b_at[j], k0, p.rank);
                 } else {
@@ -504,11 +637,11 @@ __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kerne
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 if (i >= n) continue;
-                const RowAt row[2] = {at[16 * i], at[16 * i + 8]};
+                const RowAt* row = rows_at + here + 16 * i;  // (and 8 on; read where they are wanted, for the registers)
                 float c[4][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint4 u = p.r ? r[i][h].get(r_tile + row[h].r + col, edge) : make_uint4(0, 0, 0, 0);
+                    const uint4 u = p.r ? r[i][h].get(r_tile + row[8 * h].r + col, edge) : make_uint4(0, 0, 0, 0);
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -521,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kerne
                         Words<RS> s[2][2];  // [row][term]
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            const Words<RS>* from = reinterpret_cast<const Words<RS>*>(low + row[h].low + k0 + RS / 4 * q);
+                            const Words<RS>* from = reinterpret_cast<const Words<RS>*>(low + row[8 * h].low + k0 + RS / 4 * q);
                             s[h][0] = from[0], s[h][1] = from[1];
                         }
 #pragma unroll
@@ -556,15 +689,16 @@ __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kerne
                     uint32_t w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) w[j] = pack2(c[j][2 * h], c[j][2 * h + 1]);
-                    uint16_t* to = d_tile + row[h].d + col;
+                    uint16_t* to = d_tile + row[8 * h].d + col;
                     if (!edge) {
-                        store_row8<SHIFT>(to, make_uint4(w[0], w[1], w[2], w[3]), q, row[h].on);
-                    } else if (row[h].on) {
+                        store_row8<SHIFT>(to, make_uint4(w[0], w[1], w[2], w[3]), q, row[8 * h].on);
+                    } else if (row[8 * h].on) {
                         store_cut(to, make_uint4(w[0], w[1], w[2], w[3]), p.n - col);
                     }
                 }
             }
         }
+    }
     }
 }
 

@@ -439,7 +439,8 @@ GB_API gb_status_t gb_moe_ffn_gated_workspace_bytes(int64_t T, int64_t I, int64_
  *   workspace  device memory, 16-byte aligned, of at least gb_lora_workspace_bytes(); need not be cleared;
  *          calls that overlap on the GPU need one each
  * X, A, B: bf16, base address 16-byte aligned, leading dimensions and distances of adapters multiples of 8
- * elements; M, N, K any number, r at most 256, and a matrix of A less than 2^31 elements.  Products are bf16 with fp32 sums; A . X, scaled, is multiplied
+ * elements; M, N, K any number, r at most 256, a matrix of A less than 2^31 elements, and
+ * ldb below 2^26.  Products are bf16 with fp32 sums; A . X, scaled, is multiplied
  * by B as two bf16 terms (16 bits), and the result is rounded once.  An infinity in B gives NaN.  M == 0 or N == 0 is a
  * no-op.  Results are the same on every run, and a row's do not depend on the other rows' ids.
  */

@@ -69,6 +69,28 @@ def test_many_rows(m):
     check(q)
 
 
+@pytest.mark.parametrize("m", [63, 64, 500, 8193, 20000])
+@pytest.mark.parametrize("adapters", [1, 2, 300, 8191, 8192])
+@pytest.mark.parametrize("r", [8, 24])
+def test_pools_of_many_adapters(m, adapters, r):
+    """Rows are sorted by up to 8191 adapters, and tile by tile beyond that; most tiles have one row of many, or all."""
+    q = problem(m, 72, 64, r, adapters, seed=m + adapters)
+    check(q)
+    q["ids"] = pick(m, adapters - 1, adapters + 1, 3)  # the last one, or none
+    d = check(q)
+    assert torch.equal(d, gb.lora(**q))
+
+
+@pytest.mark.parametrize("m,n", [(200, 4099), (300, 33), (65, 1001)])
+@pytest.mark.parametrize("r", [16, 32, 64, 130])
+def test_rows_that_start_anywhere_in_any_order(m, n, r):
+    q = problem(m, n, 96, r, 7, seed=r)
+    want = check(q)
+    out = torch.full((m * n + 3,), 9.0, dtype=BF16, device=DEV)
+    gb.lora(**q, out=out[1:1 + m * n].view(m, n))
+    assert torch.equal(out[1:1 + m * n].view(m, n), want) and (out[[0, -2, -1]] == 9).all()
+
+
 @pytest.mark.parametrize("act", ["none", "gelu_tanh", "silu", "relu"])
 @pytest.mark.parametrize("residual", [True, False])
 def test_epilogue(act, residual):

@@ -189,6 +189,7 @@ def lora(L, X=P16, ldx=64, A=P16, lda=64, aa=512, B=P16, ldb=8, ab=256, ids=P16,
     (dict(lda=60), GB_ERR_INVALID_ARG, "of A"),
     (dict(B=P4), GB_ERR_UNSUPPORTED, "B"),
     (dict(ldb=12), GB_ERR_UNSUPPORTED, "B"),
+    (dict(ldb=1 << 26, ab=1 << 34), GB_ERR_UNSUPPORTED, "2^26"),
     (dict(lda=1 << 30, aa=1 << 34), GB_ERR_UNSUPPORTED, "2^31 elements"),
     (dict(aa=504), GB_ERR_INVALID_ARG, "A"),
     (dict(ab=260), GB_ERR_UNSUPPORTED, "B"),
@@ -208,6 +209,9 @@ def test_empty_lora_is_a_noop(L):
     assert lora(L, X=None, A=None, B=None, D=None, ids=None, N=0) == GB_OK
     n = ctypes.c_size_t(7)
     assert L.gb_lora_workspace_bytes(0, 8, 8, 8, ctypes.byref(n)) == GB_OK and n.value == 0
+    # two terms of two bytes for each row and rank, in whole steps of 16 or 32; of 64 rows and more their order too
+    for m, r, want in ((3, 5, 3 * 16 * 4), (63, 40, 63 * 64 * 4), (64, 16, 64 * 16 * 4 + 65 * 16 + 64 * 4)):
+        assert L.gb_lora_workspace_bytes(m, 8, 8, r, ctypes.byref(n)) == GB_OK and n.value == want
     assert L.gb_lora_workspace_bytes(8, 8, 8, 300, ctypes.byref(n)) == GB_ERR_UNSUPPORTED
     assert L.gb_lora_workspace_bytes(8, 8, 8, 8, None) == GB_ERR_INVALID_ARG
 
