@@ -4,7 +4,7 @@
 //
 // Two launches: down to the rank (S = X A^T, the columns split over CTAs), and up to D.  Rows come in any order, and
 // rows of one adapter share its matrices' fragments.  Few rows: each CTA takes a tile of consecutive ones and sorts it by
-// adapter for itself.  64 and more: a launch before the two sorts them all, and a tile has rows of one adapter.  (A tile
+// adapter for itself.  More: a launch before the two sorts them all, and a tile has rows of one adapter.  (A tile
 // in which two requests meet takes a turn for each, and the launch waits for it: 1000 rows of 30 requests, with tiles
 // of consecutive rows, 49 us.)  Both products are bound by memory: X, R and D once, and the adapters' matrices.
 #pragma once

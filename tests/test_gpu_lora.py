@@ -69,7 +69,7 @@ def test_many_rows(m):
     check(q)
 
 
-@pytest.mark.parametrize("m", [63, 64, 500, 8193, 20000])
+@pytest.mark.parametrize("m", [31, 32, 64, 500, 8193, 20000])
 @pytest.mark.parametrize("adapters", [1, 2, 300, 8191, 8192])
 @pytest.mark.parametrize("r", [8, 24])
 def test_pools_of_many_adapters(m, adapters, r):
