@@ -64,7 +64,7 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int
         pl.up_blocks = std::min((most + 1) * pl.parts, places);
         return pl;
     }
-    const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), rows = turn_rows(r <= 16 ? 1 : 2);
+    const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), rows = 8 * turn_units(r <= 16 ? 1 : 2);
     pl.cluster = 1;
     while (pl.cluster < 8 && pl.cluster * kWarps < steps) pl.cluster *= 2;
     while (pl.cluster > 1 && ceil_div(M, slots / pl.cluster) > rows) pl.cluster /= 2;
@@ -145,6 +145,10 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
                             "%s: adapters %" PRId64 " elements apart (a multiple of 8, and at least a matrix)", m.name, m.apart);
         }
     }
+    // (the distance of rows says nothing of one row)
+    if (M == 1) ldx = K, ldr = N, ldd = N;
+    if (r == 1) lda = K;
+    if (N == 1) ldb = r;
     if (any && (r - 1) * lda + K > kMaxDim)  // (distances within a matrix are counted in 32 bits)
         return fail(GB_ERR_UNSUPPORTED, "A: %" PRId64 " rows %" PRId64 " elements apart are more than 2^31 elements", r, lda);
     if (any && kColumns * ldb > kMaxDim) return fail(GB_ERR_UNSUPPORTED, "leading dimension %" PRId64 " of B: below 2^26", ldb);

@@ -134,6 +134,23 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     }
 }
 
+// Where a row ends inside eight elements: the first `columns` of them, zeros for the rest.  (Not inlined: it is wanted once
+// in a while, and code that is not there need not be fetched.  With the ends in line a launch of a few blocks waited
+// for instructions more than for memory.)
+static __device__ __noinline__ uint4 load_cut(const uint16_t* at, int columns) {
+    uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < columns) w[i >> 1] |= static_cast<uint32_t>(at[i]) << (i & 1) * 16;
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+static __device__ __noinline__ void store_cut(uint16_t* at, uint4 v, int columns) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (i < columns) at[i] = static_cast<uint16_t>(w[i >> 1] >> (i & 1) * 16);
+}
+
 // Where the terms of rank j of a row of S are, of RS ranks a step of the product up to D (16, or 32 beyond 16 ranks):
 // a lane's quarter of a step lies together, first terms and second terms.
 template <int RS>
@@ -232,101 +249,80 @@ __device__ __forceinline__ int64_t make_order(Order& o, const Params& p, int til
 
 // ---------------------------------------------------------------- down to the rank
 
-// 16 MT ranks with NT units of rows, over the steps first, first + by, ...  ADAPTERS: how many the units have at most
-// (they are in order; NT: each has its own), whose fragments the units of one share.
+// 16 MT ranks of one adapter with NT units of its rows, over the steps first, first + by, ...
 //
 // Loads go straight to the fragments.  Each row's 64 bytes come from one warp, 512 contiguous bytes from the block's
 // eight, and two blocks an SM have 70 to 80 KB on their way: 64 rows of 4096 columns a block and a cluster of two
 // stream at 7.4 TB/s (8192 rows of 67 MB).  A ring of steps in shared memory, filled by cp.async, streamed at 4.8.
-template <int MT, int NT, int ADAPTERS>
+template <int MT, int NT>
 __device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p, const Order& o, int64_t row0, int rank0,
                                           int unit0, int units, int first, int by) {
-    constexpr int kOf = 2 * MT * ADAPTERS + NT, kUnroll = kOf <= 4 ? 4 : kOf < 8 ? 2 : 1;
+    constexpr int kOf = 2 * MT + NT, kUnroll = kOf <= 4 ? 4 : kOf < 8 ? 2 : 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    // (ranks beyond the last are the last's, rows the unit's first's, units the last's: their sums are not used)
-    // (distances within a tile's rows and within an adapter's matrix are within 32 bits: the host sees to it)
-    const uint16_t *a[ADAPTERS], *tile = p.x + row0 * p.ldx + 8 * q;
+    // (ranks beyond the last are the last's, rows the unit's first's, units the last's: their sums are not used;
+    // distances within a tile's rows and within an adapter's matrix are within 32 bits: the host sees to it)
+    const uint16_t *a = p.a + o.adapter(unit0) * p.apart_a + 8 * q, *tile = p.x + row0 * p.ldx + 8 * q;
     uint32_t a_at[2 * MT], x[NT];
-    int cut = NT;  // of two adapters: the second's first unit
+#pragma unroll
+    for (int i = 0; i < 2 * MT; ++i) a_at[i] = min(rank0 + g + 8 * i, p.rank - 1) * static_cast<uint32_t>(p.lda);
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
         const int unit = unit0 + min(t, units - 1), place = o.start[unit] + g;
         x[t] = o.row[place < o.start[unit + 1] ? place : place - g] * static_cast<uint32_t>(p.ldx);
-        if (ADAPTERS == 2 && o.adapter(unit) != o.adapter(unit0)) cut = min(cut, t);
     }
-#pragma unroll
-    for (int t = 0; t < ADAPTERS; ++t) {
-        const int unit = unit0 + min(ADAPTERS == 2 && t ? cut : t, units - 1);
-        a[t] = p.a + o.adapter(unit) * p.apart_a + 8 * q;
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) a_at[i] = min(rank0 + g + 8 * i, p.rank - 1) * static_cast<uint32_t>(p.lda);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[m][t][i] = 0.f;
-    auto add = [&](const uint4 (&u)[ADAPTERS][2 * MT], const uint4 (&v)[NT]) {
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            if constexpr (ADAPTERS == 2) {
-                const bool later = t >= cut;
-#pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    if (later) mma_step(c[m][t], u[1][2 * m], u[1][2 * m + 1], v[t]);
-                    else mma_step(c[m][t], u[0][2 * m], u[0][2 * m + 1], v[t]);
-                }
-            } else {
-                constexpr bool kOwn = ADAPTERS == NT;
-#pragma unroll
-                for (int m = 0; m < MT; ++m) mma_step(c[m][t], u[kOwn ? t : 0][2 * m], u[kOwn ? t : 0][2 * m + 1], v[t]);
-            }
-        }
-    };
     const int whole = p.k / kStep;
     for (int s = first; s < whole; s += kUnroll * by) {
-        uint4 u[kUnroll][ADAPTERS][2 * MT], v[kUnroll][NT];
+        uint4 u[kUnroll][2 * MT], v[kUnroll][NT];
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {  // (all loads at once; beyond the last step, it again)
             const int col = min(s + j * by, whole - 1) * kStep;
 #pragma unroll
-            for (int t = 0; t < ADAPTERS; ++t)
+            for (int i = 0; i < 2 * MT; ++i) u[j][i] = *reinterpret_cast<const uint4*>(a + a_at[i] + col);
 #pragma unroll
-                for (int i = 0; i < 2 * MT; ++i) u[j][t][i] = *reinterpret_cast<const uint4*>(a[t] + a_at[i] + col);
-#pragma unroll
-            for (int t = 0; t < NT; ++t)   // (up to 16 ranks X is read by one warp only)
+            for (int t = 0; t < NT; ++t)  // (up to 16 ranks X is read by one warp only)
                 v[j][t] = MT == 1 ? load_once(tile + x[t] + col) : *reinterpret_cast<const uint4*>(tile + x[t] + col);
         }
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j)
-            if (s + j * by < whole) add(u[j], v[j]);
+        for (int j = 0; j < kUnroll; ++j) {
+            if (s + j * by >= whole) continue;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) mma_step(c[m][t], u[j][2 * m], u[j][2 * m + 1], v[j][t]);
+        }
     }
     if (whole * kStep < p.k && first == 0) {
-        const int col = whole * kStep, left = p.k - 8 * q;
-        uint4 u[ADAPTERS][2 * MT], v[NT];
+        const int col = whole * kStep, left = p.k - 8 * q - col;
+        uint4 u[2 * MT];
 #pragma unroll
-        for (int t = 0; t < ADAPTERS; ++t)
+        for (int i = 0; i < 2 * MT; ++i) u[i] = load_cut(a + a_at[i] + col, left);
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) u[t][i] = load_edge(a[t] + a_at[i], col, left);
+        for (int t = 0; t < NT; ++t) {
+            const uint4 v = load_cut(tile + x[t] + col, left);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) v[t] = load_edge(tile + x[t], col, left);
-        add(u, v);
+            for (int m = 0; m < MT; ++m) mma_step(c[m][t], u[2 * m], u[2 * m + 1], v);
+        }
     }
 }
 
-// A turn: `units` units of rows (up to NT).  The cluster's CTAs share the columns, and in each CTA a team of warps
+// A turn: `units` units of rows of one adapter (up to NT).  The cluster's CTAs share the columns, and in each CTA a team of warps
 // 16 MT ranks and, again, the columns; the sums are joined over the warps, then over the CTAs, in the same order on
 // every run.  `joined`: the warps' sums; `mine`: the CTA's, one of two places in turn, so that a turn has one barrier
 // of the cluster.
-template <int MT, int NT, int ADAPTERS>
+template <int MT, int NT>
 __device__ __forceinline__ void down_turn(const Params& p, const Order& o, float* joined, float* mine, int64_t row0, int rank,
                                           int unit0, int units) {
     constexpr int kOf = MT * NT * 128;  // sums of a warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sharing = kWarps / p.teams, team = warp / sharing, part = warp % sharing;
     float c[MT][NT][4];
-    down_sums<MT, NT, ADAPTERS>(c, p, o, row0, team * 16 * MT, unit0, units, rank * sharing + part, p.cluster * sharing);
+    down_sums<MT, NT>(c, p, o, row0, team * 16 * MT, unit0, units, rank * sharing + part, p.cluster * sharing);
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -361,11 +357,8 @@ __device__ __forceinline__ void down_turn(const Params& p, const Order& o, float
     }
 }
 
-// Units a turn takes (rows of one adapter, or of two; of more, half of them at most), and rows a tile has so that the
-// rows of two adapters make no more units than that: where one request ends in a tile, that tile would else take
-// another turn, and the launch waits for it (8192 rows of 12 requests: 27 us instead of 20).
+// Units of one adapter that a turn takes.
 __host__ __device__ constexpr int turn_units(int mt) { return mt == 1 ? 8 : 4; }
-__host__ __device__ constexpr int turn_rows(int mt) { return 8 * (turn_units(mt) - 1); }
 constexpr int kSums = 8 * 128;  // of a warp in a turn, at most
 
 // Dynamic shared memory: the warps' sums, and two places for the CTA's.
@@ -387,35 +380,14 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     if (tile >= (p.tiles ? p.tiles[0].x : clusters)) break;
     const int64_t row0 = make_order<8>(o, p, tile, rows);  // (by when all have read next_tile)
     if (threadIdx.x == 0) next_tile = tile + clusters;
-    int units = 0;  // with an adapter
-    while (units < o.units && o.adapter(units) >= 0) ++units;
-    for (int unit = 0; unit < units; turn ^= 1) {
-        int n = 0, two = 0;  // units of one adapter, and of two
-        for (int i = unit, changes = 0; i < min(units, unit + kMost); ++i) {
-            changes += i > unit && o.adapter(i) != o.adapter(i - 1);
-            n += changes == 0;
-            two += changes <= 1;
-        }
+    for (int unit = 0, n; unit < o.units && o.adapter(unit) >= 0; unit += n, turn ^= 1) {  // (those without are last)
+        n = 1;
+        while (n < kMost && unit + n < o.units && o.adapter(unit + n) == o.adapter(unit)) ++n;
         float* mine = sums + (kWarps + turn * p.teams) * kSums;
-        const int left = min(units - unit, kMost);
-        if (n < left && two == left) {  // (all that a turn can have)
-            n = two;
-            if (n <= 2) down_turn<MT, 2, 2>(p, o, sums, mine, row0, rank, unit, n);
-            else down_turn<MT, kMost, 2>(p, o, sums, mine, row0, rank, unit, n);
-        } else if (n < min(left, kMost / 2)) {
-            n = min(left, kMost / 2);
-            if (n <= 2) down_turn<MT, 2, 2>(p, o, sums, mine, row0, rank, unit, n);
-            else if constexpr (MT == 1) down_turn<MT, kMost / 2, kMost / 2>(p, o, sums, mine, row0, rank, unit, n);
-        } else if (n == 1) {
-            down_turn<MT, 1, 1>(p, o, sums, mine, row0, rank, unit, n);
-        } else if (n == 2) {
-            down_turn<MT, 2, 1>(p, o, sums, mine, row0, rank, unit, n);
-        } else if (MT == 2 || n <= 4) {
-            down_turn<MT, 4, 1>(p, o, sums, mine, row0, rank, unit, n);
-        } else if constexpr (MT == 1) {
-            down_turn<MT, 8, 1>(p, o, sums, mine, row0, rank, unit, n);
-        }
-        unit += n;
+        if (n == 1) down_turn<MT, 1>(p, o, sums, mine, row0, rank, unit, n);
+        else if (n == 2) down_turn<MT, 2>(p, o, sums, mine, row0, rank, unit, n);
+        else if (MT == 2 || n <= 4) down_turn<MT, 4>(p, o, sums, mine, row0, rank, unit, n);
+        else if constexpr (MT == 1) down_turn<MT, 8>(p, o, sums, mine, row0, rank, unit, n);
     }
     }
     cluster_sync();  // (the others may still read this CTA's sums)
@@ -466,21 +438,6 @@ __device__ __forceinline__ uint4 window(const uint4& a, const uint4& b, int by) 
 
 // Elements between the 16-byte boundary below p and p.
 __device__ __forceinline__ int shift_of(const uint16_t* p) { return static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 7; }
-
-// A lane's columns where a block is cut off: the first `columns` of eight.  (Few blocks: their code is kept small.)
-__device__ __noinline__ uint4 load_cut(const uint16_t* at, int columns) {
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < columns) w[i >> 1] |= static_cast<uint32_t>(at[i]) << (i & 1) * 16;
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __noinline__ void store_cut(uint16_t* at, uint4 v, int columns) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < columns) at[i] = static_cast<uint16_t>(w[i >> 1] >> (i & 1) * 16);
-}
 
 // A lane's eight columns of 32 in a row (8q .. 8q + 7, at `at`), on their way.  SHIFT: rows start anywhere; the two
 // 16-byte words are loaded that hold them.

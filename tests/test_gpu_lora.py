@@ -181,6 +181,21 @@ def test_layouts_of_adapters():
     assert torch.equal(gb.lora(**q), want)
 
 
+def test_single_rows_of_any_stride():
+    """The stride of a dimension of one says nothing."""
+    q = problem(1, 40, 64, 1, 1, seed=21)
+    q["ids"][:] = 0
+    want = check(q)
+    far = 1 << 40
+    q["X"], q["R"] = q["X"].as_strided((1, 64), (far, 1)), q["R"].as_strided((1, 40), (far, 1))
+    q["A"] = q["A"].as_strided((1, 1, 64), (far, far, 1))
+    assert torch.equal(gb.lora(**q), want)
+    q = problem(70, 1, 64, 8, 2, seed=22)
+    want = check(q)
+    q["B"] = q["B"].as_strided((2, 1, 8), (q["B"].stride(0), far, 1))
+    assert torch.equal(gb.lora(**q), want)
+
+
 def test_a_long_pool_of_adapters():
     """Offsets of adapters pass 2^31 elements."""
     count, r, k, n = 1100, 128, 16384, 40
