@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cinttypes>
+#include <cmath>
 
 #include "host.h"
 #include "lora_kernel.cuh"
@@ -56,12 +57,23 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int
         const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), turns = ceil_div(N, kWarps * kColumns);
         const int64_t places = (shift || r > 16 ? 2 : 3) * sms;
         pl.down_tile = pl.up_tile = 8 * turn_units(r <= 16 ? 1 : 2);
-        // (how many tiles there are is known on the GPU only; half of the adapters' last ones are counted here)
-        const int64_t most = ceil_div(M, pl.up_tile) + std::min(adapters, M), likely = ceil_div(M, pl.up_tile) + std::min(adapters, M) / 2;
+        // How many tiles there are is known on the GPU only.  Here: as many adapters as would be met if each row chose one
+        // at random, each with a last tile that is half full, or with one.
+        const int64_t full = ceil_div(M, pl.up_tile), most = full + std::min(adapters, M) + 1;
+        const double met = adapters * (1.0 - std::exp(-static_cast<double>(M) / adapters));
+        const int64_t likely = std::min(most, static_cast<int64_t>(std::max(met, full + 0.5 * met)) + 1);
         pl.cluster = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, ceil_div(steps, kWarps), slots / likely})));
         pl.down_blocks = std::min(most, std::max<int64_t>(1, slots / pl.cluster)) * pl.cluster;
-        pl.parts = static_cast<int>(likely * ceil_div(turns, 2) >= 2 * places ? ceil_div(turns, 2) : turns);
-        pl.up_blocks = std::min((most + 1) * pl.parts, places);
+        // D's columns to blocks of a tile: of least time if a tile's order and S take a block what 32 columns take a warp.
+        int64_t best = 0;
+        for (int64_t each = 1; each <= std::min<int64_t>(turns, 16); ++each) {
+            const int64_t parts = ceil_div(turns, each), time = ceil_div(likely * parts, places) * (each + 1);
+            if (best == 0 || time < best) {
+                best = time;
+                pl.parts = static_cast<int>(parts);
+            }
+        }
+        pl.up_blocks = std::min(most * pl.parts, places);
         return pl;
     }
     const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), rows = 8 * turn_units(r <= 16 ? 1 : 2);
