@@ -95,17 +95,21 @@ struct LayerNormParams {
 // h = dropout(x) + r;  mean, rstd = 1 / sqrt(mean((h - mean)^2) + eps);  y = (h - mean) rstd weight + bias,
 // in fp32 from h before its rounding.
 //
-// The variance is a sum of squares of differences, never a difference of sums (which loses what the mean is
-// larger than the deviation by): each warp takes its own part's mean first, from registers, and the parts'
-// sums of squares are moved to the row's mean when they are joined,
+// The variance is a sum of squares of differences, never a difference of sums (which loses what the mean is larger than
+// the deviation by): each warp takes its own part's mean first, from registers, and the parts' sums of squares are moved
+// to the row's mean when they are joined,
 //     sum (h - mean)^2 = sum over warps [ S_w + n_w (mean_w - mean)^2 ],
 // so that a row has one barrier, as the root-mean-square norm's has.
 //
-// FULL: rows of whole, aligned 16-byte words (no chunk begins or ends inside one).  What a chunk costs decides: with
-// every chunk's ends looked at, as a shifted row wants it, 8192 x 4096 took 610 instructions a warp's part of a row and
-// 55 us, 62 % of issue slots used.
-// Dynamic shared memory: the rows [stage][x or r][chunk][thread], the weight, the bias.  (Three stages of
-// 16384 columns and both vectors would be 256 KB.)
+// FULL: rows of whole, aligned 16-byte words (no chunk begins or ends inside one); other rows' chunks are the same but
+// for those that a row begins and ends in.
+//
+// 8192 x 4096 with a residual and a bias on a GB300: 47 us, 5.7 TB/s (0.84 of the copy bandwidth); 41 us by ncu, the
+// bytes' own time. What a chunk costs decides: with every chunk's ends looked at it took 610 instructions a warp's part
+// of a row, 62 % of issue slots and 55 us.
+//
+// Dynamic shared memory: the rows [stage][x or r][chunk][thread], the weight, the bias.  (Three stages of 16384 columns
+// and both vectors would be 256 KB.)
 __host__ __device__ constexpr int layer_norm_stages(int v) { return v == 4 ? 2 : kRowStages; }
 
 // 16 bytes to the thread's own place, which it alone reads.
@@ -284,9 +288,14 @@ struct LayerNormBwdParams {
 
 // With xhat = (h - mean) rstd and g = dy weight:  dr = rstd (g - mean(g) - xhat mean(g xhat)) + dh,
 // dx = dropout's gradient of dr,  dweight = sum over rows of dy xhat,  dbias = sum over rows of dy.
-// Rows and the gradients' sums in registers as in norm_bwd_kernel.  FULL as in layer_norm_kernel: g and xhat stay in
-// registers from the first pass over a row to the second.  (With both made again from shared memory, and every chunk's
-// ends looked at, 8192 x 4096 took 700 instructions a warp's part of a row and 68 us.)
+// Rows and the gradients' sums in registers as in norm_bwd_kernel. FULL as in layer_norm_kernel: g and xhat stay in
+// registers from the first pass over a row to the second; with chunks that end inside a row xhat does, for two blocks of
+// nine warps an SM.
+//
+// 8192 x 4096 with dH on a GB300, the join with it: 50 us, 5.3 TB/s (0.79 of the copy bandwidth); 3001 x 4099 32 us,
+// 0.45. With g and xhat made again from shared memory, and every chunk's ends looked at, 8192 x 4096 took 700
+// instructions a warp's part of a row and 69 us, 3001 x 4099 40.
+//
 // Dynamic shared memory: the rows [stage][dY, H or dH][chunk][thread], then the weight.
 __host__ __device__ constexpr int layer_bwd_stages(int v) { return v == 2 ? 3 : kBwdStages; }
 

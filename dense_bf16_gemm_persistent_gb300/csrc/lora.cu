@@ -25,8 +25,8 @@ gb_status_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adap
     return GB_OK;
 }
 
-// Rows that are sorted by adapter, from so many on.  (48 rows of 40 adapters, rank 64, take 30 us either way; 1000 rows of 30
-// requests 39 us instead of 49.)
+// Rows that are sorted by adapter, from so many on. (48 rows of 40 adapters, rank 64: 26 us, tile by tile 30; 1000 rows
+// of 30 requests 39 and 49. Fewer rows have a tile each in any case, and a launch less.)
 constexpr int64_t kSortFrom = 32;
 
 struct Plan {
@@ -41,14 +41,9 @@ int64_t low_columns(int64_t r) { return r <= 16 ? 16 : ceil_div(r, 32) * 32; }
 int64_t low_bytes(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
 int64_t workspace_of(int64_t M, int64_t r) { return low_bytes(M, r) + (M >= kSortFrom ? 16 * (M + 1) + 4 * M : 0); }
 
-// The product down to the rank: X's columns are shared out to a cluster, down to a step for each of its warps, and the
-// rows so that all blocks run at once (two an SM), with as many rows as a turn takes at most.  The product up to D:
-// tiles of 64 rows, fewer where these and all columns' warps are not enough for the SMs; a block of columns a warp, or
-// two where that is twice as many blocks as run at once.  (Small tiles cost more than few blocks of them: 1000 rows of
-// 4099 columns in 16 tiles of 64 took 15 us, in 63 of 16 rows, which two adapters meet in more often, 24.  8192 x 4096
-// with two blocks of columns a warp 34 us, with as many as all run at once 36, since those are not done together.)  Less
-// than 64 rows are requests of a token or a few, with adapters of their own as a rule: a tile each, and the blocks that
-// run at once (48 rows of 14336 columns, rank 64: 20 us; in tiles of 8 rows 24).
+// The product down to the rank: X's columns are shared out to a cluster, down to a step for each of its warps, so that
+// about as many blocks as run at once (two an SM) have a tile each.  The product up to D: a tile's columns to `parts`
+// blocks.
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int64_t ldx, int64_t ld, int sms, bool shift) {
     Plan pl;
     // (sorted rows are counted from the matrix's first: its distances are within 32 bits)
@@ -57,14 +52,15 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int
         const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), turns = ceil_div(N, kWarps * kColumns);
         const int64_t places = (shift || r > 16 ? 2 : 3) * sms;
         pl.down_tile = pl.up_tile = 8 * turn_units(r <= 16 ? 1 : 2);
-        // How many tiles there are is known on the GPU only.  Here: as many adapters as would be met if each row chose one
-        // at random, each with a last tile that is half full, or with one.
+        // How many tiles there are is known on the GPU only.  Here: as many adapters as would be met if each row chose
+        // one at random, each with a last tile that is half full, or with one.
         const int64_t full = ceil_div(M, pl.up_tile), most = full + std::min(adapters, M) + 1;
         const double met = adapters * (1.0 - std::exp(-static_cast<double>(M) / adapters));
         const int64_t likely = std::min(most, static_cast<int64_t>(std::max(met, full + 0.5 * met)) + 1);
         pl.cluster = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, ceil_div(steps, kWarps), slots / likely})));
         pl.down_blocks = std::min(most, std::max<int64_t>(1, slots / pl.cluster)) * pl.cluster;
-        // D's columns to blocks of a tile: of least time if a tile's order and S take a block what 32 columns take a warp.
+        // D's columns to blocks of a tile: of least time if a tile's order and S take a block what 32 columns take a
+        // warp.
         int64_t best = 0;
         for (int64_t each = 1; each <= std::min<int64_t>(turns, 16); ++each) {
             const int64_t parts = ceil_div(turns, each), time = ceil_div(likely * parts, places) * (each + 1);
@@ -83,15 +79,13 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int
     pl.down_tile = static_cast<int>(std::min(rows, ceil_div(M, slots / pl.cluster)));
     while (pl.down_tile > 1 && pl.down_tile * ldx > kMaxDim) pl.down_tile /= 2;  // (the kernels' distances within a tile)
     pl.down_blocks = ceil_div(M, pl.down_tile) * pl.cluster;
-    const int64_t turns = ceil_div(N, kWarps * kColumns), pairs = ceil_div(turns, 2);
-    const int64_t places = (shift || r > 16 ? 2 : 3) * sms;
-    pl.up_tile = kMaxTile;
-    while (pl.up_tile > 1 && ceil_div(M, pl.up_tile) * turns * 5 < places * 4) pl.up_tile /= 2;
+    // Few rows are requests of a token each, with adapters of their own as a rule: a tile each.  (48 rows of 14336
+    // columns, rank 64: 20 us; in tiles of 8 rows 24.)  Many whose adapters are too many to be sorted by: tiles of 64.
+    const int64_t turns = ceil_div(N, kWarps * kColumns), places = (shift || r > 16 ? 2 : 3) * sms;
+    pl.up_tile = M < kSortFrom ? 1 : kMaxTile;
     while (pl.up_tile > 1 && pl.up_tile * ld > kMaxDim) pl.up_tile /= 2;
-    if (M < kMaxTile) pl.up_tile = 1;
     const int64_t up_tiles = ceil_div(M, pl.up_tile);
-    pl.parts = static_cast<int>(up_tiles * pairs >= 2 * places ? pairs : turns);
-    if (M < kMaxTile) pl.parts = static_cast<int>(ceil_div(turns, ceil_div(turns, std::max<int64_t>(1, places / M))));
+    pl.parts = static_cast<int>(ceil_div(turns, ceil_div(turns, std::max<int64_t>(1, places / up_tiles))));
     pl.up_blocks = up_tiles * pl.parts;
     return pl;
 }

@@ -51,6 +51,7 @@ __device__ __forceinline__ int4 tile_of(int adapter, int start, int count) { ret
 
 // ---------------------------------------------------------------- all rows by adapter
 
+// One block: 5 us for 1000 rows, 7.5 for 8192, of which the launch and the first loads are the half.
 constexpr int kSortThreads = 1024, kSortBatch = 8, kMaxSorted = 8191;  // adapters: a counter each in shared memory
 
 // A count of the rows of each adapter (and of those without one), the starts, and each row to its adapter's next
@@ -134,9 +135,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     }
 }
 
-// Where a row ends inside eight elements: the first `columns` of them, zeros for the rest.  (Not inlined: it is wanted once
-// in a while, and code that is not there need not be fetched.  With the ends in line a launch of a few blocks waited
-// for instructions more than for memory.)
+// Where a row ends inside eight elements: the first `columns` of them, zeros for the rest.  (Not inlined: it is wanted
+// once in a while, and code that is not there need not be fetched.  With the ends in line a launch of a few blocks
+// waited for instructions more than for memory.)
 static __device__ __noinline__ uint4 load_cut(const uint16_t* at, int columns) {
     uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -311,10 +312,10 @@ __device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p
     }
 }
 
-// A turn: `units` units of rows of one adapter (up to NT).  The cluster's CTAs share the columns, and in each CTA a team of warps
-// 16 MT ranks and, again, the columns; the sums are joined over the warps, then over the CTAs, in the same order on
-// every run.  `joined`: the warps' sums; `mine`: the CTA's, one of two places in turn, so that a turn has one barrier
-// of the cluster.
+// A turn: `units` units of rows of one adapter (up to NT).  The cluster's CTAs share the columns, and in each CTA a team
+// of warps 16 MT ranks and, again, the columns; the sums are joined over the warps, then over the CTAs, in the same
+// order on every run.  `joined`: the warps' sums; `mine`: the CTA's, one of two places in turn, so that a turn has one
+// barrier of the cluster.
 template <int MT, int NT>
 __device__ __forceinline__ void down_turn(const Params& p, const Order& o, float* joined, float* mine, int64_t row0, int rank,
                                           int unit0, int units) {
@@ -454,9 +455,9 @@ struct Row8 {
     }
 };
 
-// A lane's eight columns of 32 in a row (8q .. 8q + 7, at `at`) written.  With rows that start anywhere a lane writes the 16-byte word that ends in its
-// columns, with its neighbour's; the four lanes' first and last words are parts, in pieces of 8, 4 and 2 bytes.
-// By all lanes of a warp; `on`: the lane's row is written.
+// A lane's eight columns of 32 in a row (8q .. 8q + 7, at `at`) written.  With rows that start anywhere a lane writes
+// the 16-byte word that ends in its columns, with its neighbour's; the four lanes' first and last words are parts, in
+// pieces of 8, 4 and 2 bytes. By all lanes of a warp; `on`: the lane's row is written.
 template <bool SHIFT>
 __device__ __forceinline__ void store_row8(uint16_t* at, const uint4& v, int q, bool on) {
     if (!SHIFT) {
@@ -498,19 +499,20 @@ struct __align__(16) RowAt {
     int on;  // else beyond the unit's last row, which stands in its place
 };
 
-// A CTA: a tile of rows, and a part of D's columns in blocks of 32, a warp each.  The mma's columns are taken in an
-// order in which a lane's sums are 8 neighbouring columns of a row: of a block's four mma tiles, column i of tile j
-// is number 8 (i / 2) + 2 j + i % 2.  Of a block a warp takes two units (16 rows) of one adapter at a time: their R,
-// and B, are asked for at once, and B's fragments serve both.  All that a row needs comes from shared memory in one
-// load, since the blocks are short.
+// A CTA: a tile of rows, and a part of D's columns in blocks of 32, a warp each. The mma's columns are taken in an order
+// in which a lane's sums are 8 neighbouring columns of a row: of a block's four mma tiles, column i of tile j is number
+// 8 (i / 2) + 2 j + i % 2. Of a block a warp takes two units (16 rows) of one adapter at a time: their R, and B, are
+// asked for at once, and B's fragments serve both. All that a row needs comes from shared memory in one load, since the
+// blocks are short.
 // RS: ranks of a step (of a lane's loads of 8 or 16 bytes); STEPS: steps of B in registers (0: the rank has more than
 // two, and B is read step by step, after the first unit from L1).
 // Dynamic shared memory: S [row in order][low_words].
 //
-// 8192 x 4096 of rank 16 (134 MB) takes 36 us, 3.7 TB/s.  While all SMs are full it moves 5 TB/s; the rest is the start
-// (1.5 us until a block knows its rows' order and has S), and blocks that are not done together.  Left out for a
-// measurement, the mma, S's loads and B's took 8 % together, R's 40 %, D's 25 %.  Four units at a time in twice the
-// registers took as long, and so did R and B fetched four turns ahead to a ring in shared memory.
+// 8192 x 4096 of rank 16 (134 MB), rows of 12 requests, on a GB300: 31 us, 4.3 TB/s (0.64 of the copy bandwidth).  While
+// all SMs are full it moves 5 TB/s; the rest is the start of a tile (1.5 us until its rows and S are there) and blocks
+// that are not done together.  Left out for a measurement, the mma, S's loads and B's took 8 % together, R's loads 40 %,
+// D's stores 25 %.  Four units at a time in twice the registers took as long, and so did R and B fetched four turns
+// ahead to a ring in shared memory.  30 tiles of one or two rows with 14336 columns and rank 64: 15.6 us for 55 MB of B.
 template <int RS, int STEPS, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kernel(const __grid_constant__ Params p) {
     constexpr int kBatch = SHIFT && STEPS != 1 ? 1 : 2;  // (units at once: for the registers)
