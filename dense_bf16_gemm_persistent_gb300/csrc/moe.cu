@@ -35,8 +35,9 @@ gb_status_t check_sizes(int64_t T, int64_t D, int64_t I, int64_t E, int top) {
         return fail(GB_ERR_INVALID_ARG, "negative size T=%" PRId64 " D=%" PRId64 " I=%" PRId64 " E=%" PRId64, T, D, I, E);
     if (T > kMaxDim || D > kMaxDim || I > kMaxDim)
         return fail(GB_ERR_UNSUPPORTED, "sizes must be below 2^31 (T=%" PRId64 " D=%" PRId64 " I=%" PRId64 ")", T, D, I);
-    if (D > kMaxDim - 256 || I > kMaxDim - 256)  // (the kernels count columns in 32 bits, a step ahead)
-        return fail(GB_ERR_UNSUPPORTED, "rows of 2^31 - 256 columns at most (D=%" PRId64 " I=%" PRId64 ")", D, I);
+    // (the kernels count columns in 32 bits: some steps ahead, and the router rounded up to 256 for each of 64 parts)
+    if (D > kMaxDim - 65536 || I > kMaxDim - 65536)
+        return fail(GB_ERR_UNSUPPORTED, "rows of 2^31 - 65536 columns at most (D=%" PRId64 " I=%" PRId64 ")", D, I);
     if (E > kMaxExperts) return fail(GB_ERR_UNSUPPORTED, "%" PRId64 " experts: at most %d", E, kMaxExperts);
     if (top < 1 || top > E) return fail(GB_ERR_INVALID_ARG, "top_k=%d of %" PRId64 " experts", top, E);
     if (top > kMaxTop) return fail(GB_ERR_UNSUPPORTED, "top_k=%d: at most %d", top, kMaxTop);

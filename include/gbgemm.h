@@ -409,7 +409,7 @@ GB_API gb_status_t gb_add_layer_norm_backward_workspace_bytes(int64_t M, int64_t
  *   workspace  device memory, 16-byte aligned, of at least gb_moe_ffn_gated_workspace_bytes(); need not be
  *           cleared; calls that overlap on the GPU need one each
  * X, G, W1, W3, W2: bf16, base address 16-byte aligned, and leading dimensions and distances of experts
- * multiples of 8 elements; D and I any number.  At most 1024 experts and top_k = 16.  Up to 64 tokens read each
+ * multiples of 8 elements; D and I below 2^31 - 65536.  At most 1024 experts and top_k = 16.  Up to 64 tokens read each
  * chosen expert's matrices once (up to 32 that chose it: once in registers, beyond it again from L2); the call's
  * time then grows as if there were a call for each 64.  T == 0 is a no-op.
  * An infinity in W2 gives NaN.
@@ -439,7 +439,7 @@ GB_API gb_status_t gb_moe_ffn_gated_workspace_bytes(int64_t T, int64_t I, int64_
  *   workspace  device memory, 16-byte aligned, of at least gb_lora_workspace_bytes(); need not be cleared;
  *          calls that overlap on the GPU need one each
  * X, A, B: bf16, base address 16-byte aligned, leading dimensions and distances of adapters multiples of 8
- * elements; M, N, K any number, r at most 256, a matrix of A less than 2^31 elements, and
+ * elements; M below 2^31, N and K 2^31 - 4096; r at most 256, a matrix of A less than 2^31 elements, and
  * ldb below 2^26.  Products are bf16 with fp32 sums; A . X, scaled, is multiplied
  * by B as two bf16 terms (16 bits), and the result is rounded once.  An infinity in B gives NaN.  M == 0 or N == 0 is a
  * no-op.  Results are the same on every run, and a row's do not depend on the other rows' ids.

@@ -150,6 +150,13 @@ def test_moe_ffn_gated_rejects(L, kwargs, status, needle):
     assert needle in L.gb_last_error().decode()
 
 
+# A row of so many columns is within 32 bits, but not what the router counts ahead in it (2048 columns a turn).
+@pytest.mark.parametrize("kwargs", [dict(d=2**31 - 1000), dict(inner=2**31 - 1000), dict(d=2**31 - 65535)])
+def test_moe_ffn_gated_rejects_rows_that_are_counted_past_32_bits(L, kwargs):
+    assert moe(L, **kwargs) == GB_ERR_UNSUPPORTED
+    assert "65536" in L.gb_last_error().decode()
+
+
 def test_empty_moe_is_a_noop_and_its_workspace_is_counted(L):
     assert moe(L, X=None, D=None, T=0) == GB_OK
     n = ctypes.c_size_t(7)
