@@ -25,12 +25,16 @@ gb_status_t check_sizes(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adap
     return GB_OK;
 }
 
-// Rows that are sorted by adapter, from so many on. (48 rows of 40 adapters, rank 64: 26 us, tile by tile 30; 1000 rows
-// of 30 requests 39 and 49. Fewer rows have a tile each in any case, and a launch less.)
-constexpr int64_t kSortFrom = 32;
+// Rows that are sorted by adapter: from 32 on by each block for itself, more than kHere by a launch before.  4096 x 4096
+// of rank 16 with 64 adapters, and 14336 x 4096 of rank 64 with 4, in us (graphs of ten calls):
+//     rows                16           31           64           128          200
+//     not sorted          8.3  13.4    9.9  19.0
+//     by each block      10.7  12.0   11.2  12.8   13.4  16.5   14.0  17.7   18.7  22.6
+//     by a launch                                  18.1  17.3   17.7  20.7   16.3  21.0
+constexpr int64_t kHereFrom = 32;
 
 struct Plan {
-    bool sorted;
+    bool sorted, here;
     int down_tile, cluster, up_tile, parts;
     int64_t down_blocks, up_blocks;
 };
@@ -39,50 +43,41 @@ int64_t low_columns(int64_t r) { return r <= 16 ? 16 : ceil_div(r, 32) * 32; }
 
 // S's terms; of sorted rows their tiles (a row each at most, and one before them) and their order.
 int64_t low_bytes(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
-int64_t workspace_of(int64_t M, int64_t r) { return low_bytes(M, r) + (M >= kSortFrom ? 16 * (M + 1) + 4 * M : 0); }
+int64_t workspace_of(int64_t M, int64_t r) { return low_bytes(M, r) + (M > kHere ? 16 * (M + 1) + 4 * M : 0); }
 
 // The product down to the rank: X's columns are shared out to a cluster, down to a step for each of its warps, so that
 // about as many blocks as run at once (two an SM) have a tile each.  The product up to D: a tile's columns to `parts`
-// blocks.
+// blocks, as many as run at once.
 Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int64_t ldx, int64_t ld, int sms, bool shift) {
     Plan pl;
+    const int64_t slots = 2 * sms, places = (shift || r > 16 ? 2 : 3) * sms;
+    const int64_t steps = ceil_div(K, kStep), turns = ceil_div(N, kWarps * kColumns), rows = 8 * turn_units(r <= 16 ? 1 : 2);
+    pl.here = M <= kHere;
     // (sorted rows are counted from the matrix's first: its distances are within 32 bits)
-    pl.sorted = adapters > 0 && M >= kSortFrom && adapters <= kMaxSorted && M * std::max(ldx, ld) <= kMaxDim;
+    pl.sorted = adapters > 0 && M >= kHereFrom && adapters <= (pl.here ? kMaxHere : kMaxSorted) && M * std::max(ldx, ld) <= kMaxDim;
     if (pl.sorted) {
-        const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), turns = ceil_div(N, kWarps * kColumns);
-        const int64_t places = (shift || r > 16 ? 2 : 3) * sms;
-        pl.down_tile = pl.up_tile = 8 * turn_units(r <= 16 ? 1 : 2);
+        pl.down_tile = pl.up_tile = rows;
         // How many tiles there are is known on the GPU only.  Here: as many adapters as would be met if each row chose
-        // one at random, each with a last tile that is half full, or with one.
-        const int64_t full = ceil_div(M, pl.up_tile), most = full + std::min(adapters, M) + 1;
-        const double met = adapters * (1.0 - std::exp(-static_cast<double>(M) / adapters));
+        // one at random, and two standard deviations, each with a last tile that is half full, or with one.  (A tile
+        // more than clusters would be a second round.)
+        const int64_t full = ceil_div(M, rows), most = full + std::min(adapters, M) + 1;
+        const double none = std::exp(-static_cast<double>(M) / adapters);
+        const double met = adapters * (1.0 - none) + 2.0 * std::sqrt(adapters * none * (1.0 - none));
         const int64_t likely = std::min(most, static_cast<int64_t>(std::max(met, full + 0.5 * met)) + 1);
         pl.cluster = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, ceil_div(steps, kWarps), slots / likely})));
         pl.down_blocks = std::min(most, std::max<int64_t>(1, slots / pl.cluster)) * pl.cluster;
-        // D's columns to blocks of a tile: of least time if a tile's order and S take a block what 32 columns take a
-        // warp.
-        int64_t best = 0;
-        for (int64_t each = 1; each <= std::min<int64_t>(turns, 16); ++each) {
-            const int64_t parts = ceil_div(turns, each), time = ceil_div(likely * parts, places) * (each + 1);
-            if (best == 0 || time < best) {
-                best = time;
-                pl.parts = static_cast<int>(parts);
-            }
-        }
-        pl.up_blocks = std::min(most * pl.parts, places);
+        pl.parts = 0;  // (as many as the tiles leave room for, known then)
+        pl.up_blocks = std::min(most * turns, places);
         return pl;
     }
-    const int64_t slots = 2 * sms, steps = ceil_div(K, kStep), rows = 8 * turn_units(r <= 16 ? 1 : 2);
     pl.cluster = 1;
     while (pl.cluster < 8 && pl.cluster * kWarps < steps) pl.cluster *= 2;
     while (pl.cluster > 1 && ceil_div(M, slots / pl.cluster) > rows) pl.cluster /= 2;
     pl.down_tile = static_cast<int>(std::min(rows, ceil_div(M, slots / pl.cluster)));
     while (pl.down_tile > 1 && pl.down_tile * ldx > kMaxDim) pl.down_tile /= 2;  // (the kernels' distances within a tile)
     pl.down_blocks = ceil_div(M, pl.down_tile) * pl.cluster;
-    // Few rows are requests of a token each, with adapters of their own as a rule: a tile each.  (48 rows of 14336
-    // columns, rank 64: 20 us; in tiles of 8 rows 24.)  Many whose adapters are too many to be sorted by: tiles of 64.
-    const int64_t turns = ceil_div(N, kWarps * kColumns), places = (shift || r > 16 ? 2 : 3) * sms;
-    pl.up_tile = M < kSortFrom ? 1 : kMaxTile;
+    // Few rows are requests of a token each, with adapters of their own as a rule: a tile each.
+    pl.up_tile = M < kHereFrom ? 1 : kMaxTile;
     while (pl.up_tile > 1 && pl.up_tile * ld > kMaxDim) pl.up_tile /= 2;
     const int64_t up_tiles = ceil_div(M, pl.up_tile);
     pl.parts = static_cast<int>(ceil_div(turns, ceil_div(turns, std::max<int64_t>(1, places / up_tiles))));
@@ -196,8 +191,10 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     prm.act = act;
     prm.cluster = pl.cluster;
     prm.parts = pl.parts;
+    prm.up_blocks = static_cast<int>(pl.up_blocks);
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (pl.sorted) {
+    prm.here = pl.sorted && pl.here;
+    if (pl.sorted && !pl.here) {
         int4* tiles = reinterpret_cast<int4*>(static_cast<uint8_t*>(workspace) + low_bytes(M, r));
         int32_t* order = reinterpret_cast<int32_t*>(tiles + M + 1);
         prm.tile = pl.down_tile;
@@ -219,7 +216,7 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
         if (st != GB_OK) return st;
     }
     prm.tile = pl.up_tile;
-    note_plan("kernel=lora sorted=%lld tile=%lld cluster=%lld down_blocks=%lld up_blocks=%lld shifted=%lld", pl.sorted,
+    note_plan("kernel=lora sorted=%lld tile=%lld cluster=%lld down_blocks=%lld up_blocks=%lld shifted=%lld", pl.sorted + prm.here,
               pl.down_tile, pl.cluster, any ? pl.down_blocks : 0, pl.up_blocks, shift);
     const UpKernel kernel = shift ? up_kernel_for<true>(prm.ldlow) : up_kernel_for<false>(prm.ldlow);
     if (prm.ldlow > 64) {  // (less is within what any kernel may have)

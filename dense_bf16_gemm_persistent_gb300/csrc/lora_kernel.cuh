@@ -3,8 +3,8 @@
 //   D[m] = act( R[m] + s[a] B[a] (A[a] X[m]) )      a = ids[m], none where it is outside 0 .. adapters - 1
 //
 // Two launches: down to the rank (S = X A^T, the columns split over CTAs), and up to D.  Rows come in any order, and
-// rows of one adapter share its matrices' fragments.  Few rows: each CTA takes a tile of consecutive ones and sorts it by
-// adapter for itself.  More: a launch before the two sorts them all, and a tile has rows of one adapter.  (A tile
+// rows of one adapter share its matrices' fragments: from 32 rows on they are sorted, and a tile has rows of one
+// adapter.  (A tile
 // in which two requests meet takes a turn for each, and the launch waits for it: 1000 rows of 30 requests, with tiles
 // of consecutive rows, 49 us.)  Both products are bound by memory: X, R and D once, and the adapters' matrices.
 #pragma once
@@ -39,15 +39,27 @@ struct Params {
     int act;
     int cluster;             // CTAs that share the columns of X
     int tile;                // rows of a tile (of the launch at hand)
-    int parts;               // CTAs of a tile that share the columns of D
+    int parts;               // CTAs of a tile that share the columns of D (of sorted rows: tiles[0] has them)
+    int up_blocks;           // of the product up to D
     int teams;               // of a CTA's warps: 16 or 32 ranks each
-    // of sorted rows (else null): {tiles whose rows have an adapter, all tiles}, then the tiles; the rows in order
+    // of sorted rows (else null): {tiles whose rows have an adapter, all tiles, blocks of a tile in the product up to D},
+    // then the tiles; the rows in order
     const int4* tiles;
     const int32_t* order;
+    int here;                // few rows, which each CTA sorts for itself
 };
 
 // A tile of sorted rows.
 __device__ __forceinline__ int4 tile_of(int adapter, int start, int count) { return make_int4(adapter, start, count, 0); }
+
+// Blocks that share a tile's columns in the product up to D, by a warp: of least time if a tile's order and S take a
+// block what 32 columns take a warp.
+__device__ __forceinline__ int parts_of(int tiles, int blocks, int n) {
+    const int turns = (n + kWarps * kColumns - 1) / (kWarps * kColumns), each = min(static_cast<int>(threadIdx.x & 15) + 1, turns);
+    const uint32_t parts = (turns + each - 1) / each, rounds = (tiles * parts + blocks - 1) / blocks;
+    const uint32_t best = __reduce_min_sync(0xffffffffu, rounds * (each + 1) * 32 + each);
+    return (turns + (best & 31) - 1) / (best & 31);
+}
 
 // ---------------------------------------------------------------- all rows by adapter
 
@@ -114,15 +126,20 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
     __syncthreads();
     int start = rows_to - rows, tile = count_to - count;
     if (tid >= 32) start += sums[(tid >> 5) - 1][0], tile += sums[(tid >> 5) - 1][1];
+    __syncthreads();
     for (int i = first; i < last; ++i) {
         const int n = next[i];
-        if (i == p.adapters) tiles[0] = make_int4(tile, tile + (n + p.tile - 1) / p.tile, 0, 0);
+        if (i == p.adapters) sums[0][0] = tile, sums[0][1] = tile + (n + p.tile - 1) / p.tile;
         next[i] = start;
         for (int at = 0; at < n; at += p.tile)
             tiles[1 + tile++] = tile_of(i < p.adapters ? i : -1, start + at, min(p.tile, n - at));
         start += n;
     }
     __syncthreads();
+    if (tid < 32) {
+        const int parts = parts_of(sums[0][1], p.up_blocks, p.n);
+        if (tid == 0) tiles[0] = make_int4(sums[0][0], sums[0][1], parts, 0);
+    }
     // (a batch that is the only one is known already; else the places are counted again, from the starts)
     for (int64_t base = 0; base < p.m; base += kBatchRows) {
         const bool again = p.m > kBatchRows;
@@ -133,6 +150,71 @@ __global__ void __launch_bounds__(kSortThreads) sort_kernel(const __grid_constan
             if (row < p.m) order[again ? place[u] : next[key[u]] + place[u]] = static_cast<int>(row);
         }
     }
+}
+
+// The same of up to kHere rows by each CTA for itself, in the order of the rows (so that a cluster's CTAs agree): a row's
+// place is the count of the rows that go before it.  All comparisons take every CTA's issue slots: 1 us in both launches
+// for 64 rows, 2.5 for 128, 5 for 256.
+constexpr int kHere = 128, kMaxHere = (1 << 22) - 1;  // adapters: an adapter and a row are one number
+
+struct Sorted {
+    int4 tiles[1 + kHere];
+    int order[kHere];
+    uint32_t begin[2][kHere / 32];  // the places that an adapter, and a tile, begins at
+};
+
+__device__ __forceinline__ void sort_here(Sorted& s, const Params& p) {
+    int *keys = reinterpret_cast<int*>(s.tiles), *adapters = keys + kHere;  // (until the tiles are written)
+    const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+    const bool on = t < p.m;  // (m <= kHere)
+    int key = 0x7fffffff;
+    if (on) {
+        const int id = p.ids[t];
+        key = (id >= 0 && id < p.adapters ? id : p.adapters) * kHere + t;
+    }
+    if (t < kHere) keys[t] = key;
+    __syncthreads();
+    if (on) {
+        int place = 0;
+#pragma unroll 4
+        for (int i = 0; i < p.m; i += 4) {  // (those beyond the last row are above all)
+            const int4 four = *reinterpret_cast<const int4*>(keys + i);
+            place += (four.x < key) + (four.y < key) + (four.z < key) + (four.w < key);
+        }
+        s.order[place] = t;
+        adapters[place] = key / kHere;
+    }
+    __syncthreads();
+    const int adapter = on ? adapters[t] : 0;
+    const uint32_t begin = __ballot_sync(0xffffffffu, on && (t == 0 || adapters[t - 1] != adapter));
+    if (lane == 0 && t < kHere) s.begin[0][warp] = begin;
+    __syncthreads();
+    // the adapter's first place, and the next one's
+    const uint32_t upto = 0xffffffffu >> (31 - lane);
+    uint32_t low = begin & upto, high = begin & ~upto;
+    int w = warp;
+    while (on && low == 0 && w > 0) low = s.begin[0][--w];
+    const int first = 32 * w + 31 - __clz(low);
+    w = warp;
+    while (high == 0 && w < kHere / 32 - 1) high = s.begin[0][++w];
+    const int end = high ? 32 * w + __ffs(high) - 1 : p.m;
+    const bool tile = on && ((t - first) & (p.tile - 1)) == 0;  // (32 or 64)
+    const uint32_t tiles = __ballot_sync(0xffffffffu, tile);
+    if (lane == 0 && t < kHere) s.begin[1][warp] = tiles;
+    const int with = __syncthreads_count(tile && adapter < p.adapters);
+    int all = 0, at = __popc(tiles & (upto >> 1));
+#pragma unroll
+    for (int i = 0; i < kHere / 32; ++i) {
+        const int n = __popc(s.begin[1][i]);
+        at += i < warp ? n : 0;
+        all += n;
+    }
+    if (tile) s.tiles[1 + at] = tile_of(adapter < p.adapters ? adapter : -1, t, min(p.tile, end - t));
+    if (warp == 0) {
+        const int parts = parts_of(all, gridDim.x, p.n);
+        if (lane == 0) s.tiles[0] = make_int4(with, all, parts, 0);
+    }
+    __syncthreads();
 }
 
 // Where a row ends inside eight elements: the first `columns` of them, zeros for the rest.  (Not inlined: it is wanted
@@ -173,16 +255,16 @@ struct Order {
 
 // Tile `tile`, by all threads of a block: its first row (what o.row counts from) and how many it has.
 template <int UNIT>
-__device__ __forceinline__ int64_t make_order(Order& o, const Params& p, int tile, int& rows) {
+__device__ __forceinline__ int64_t make_order(Order& o, const Sorted& s, const Params& p, int tile, int& rows) {
     __shared__ int given[kMaxTile];
     __shared__ bool begins[kMaxTile];  // (in order) a unit
     const int t = threadIdx.x;
-    if (p.tiles) {
-        const int4 sorted = p.tiles[1 + tile];
+    if (p.here || p.tiles) {
+        const int4 sorted = p.here ? s.tiles[1 + tile] : p.tiles[1 + tile];
         rows = sorted.z;
         int ends = 0;
         if (t < rows) {
-            const int row = p.order[sorted.y + t];
+            const int row = p.here ? s.order[sorted.y + t] : p.order[sorted.y + t];
             o.row[t] = row;
             o.id[t] = sorted.x;
             ends = (row == 0 ? 1 : 0) | (row == p.m - 1 ? 2 : 0);
@@ -372,14 +454,16 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
     const int rank = blockIdx.x % p.cluster;
     constexpr int kMost = turn_units(MT);
     __shared__ int next_tile;  // (here for the registers: it is wanted once a tile)
+    __shared__ Sorted sorted;
+    if (p.here) sort_here(sorted, p);
     if (threadIdx.x == 0) next_tile = blockIdx.x / p.cluster;
     int turn = 0;
     for (;;) {
     int rows;
     __syncthreads();  // (the tile before has been read)
     const int tile = next_tile, clusters = gridDim.x / p.cluster;
-    if (tile >= (p.tiles ? p.tiles[0].x : clusters)) break;
-    const int64_t row0 = make_order<8>(o, p, tile, rows);  // (by when all have read next_tile)
+    if (tile >= (p.here ? sorted.tiles[0].x : p.tiles ? p.tiles[0].x : clusters)) break;
+    const int64_t row0 = make_order<8>(o, sorted, p, tile, rows);  // (by when all have read next_tile)
     if (threadIdx.x == 0) next_tile = tile + clusters;
     for (int unit = 0, n; unit < o.units && o.adapter(unit) >= 0; unit += n, turn ^= 1) {  // (those without are last)
         n = 1;
@@ -522,13 +606,21 @@ __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kerne
     __shared__ RowAt rows_at[kMaxTile * 16];
     extern __shared__ __align__(16) uint32_t low[];
     __shared__ int next_item;  // (here for the registers: it is wanted once an item)
-    if (threadIdx.x == 0) next_item = blockIdx.x;
+    __shared__ Sorted sorted;
+    if (p.here) sort_here(sorted, p);
+    __shared__ int items, parts;
+    if (threadIdx.x == 0) {
+        const int4 all = p.here ? sorted.tiles[0] : p.tiles ? p.tiles[0] : make_int4(0, 0, p.parts, 0);
+        items = all.y > 0 ? all.y * all.z : gridDim.x;
+        parts = all.z;
+        next_item = blockIdx.x;
+    }
     for (;;) {
     int rows;
     __syncthreads();  // (the item before has been read)
     const int item = next_item;
-    if (item >= (p.tiles ? p.tiles[0].y * p.parts : static_cast<int>(gridDim.x))) break;
-    const int64_t row0 = make_order<16>(o, p, item / p.parts, rows);  // (by when all have read next_item)
+    if (item >= items) break;
+    const int64_t row0 = make_order<16>(o, sorted, p, item / parts, rows);  // (by when all have read next_item)
     if (threadIdx.x == 0) next_item = item + gridDim.x;
     const int words = low_words(p.ldlow), chunks = p.ldlow / 4, units = o.units;
     for (int i = threadIdx.x; i < units * 16; i += kThreads) {
@@ -548,8 +640,8 @@ __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kerne
     // (of sorted rows, whose distances are the matrix's, 0)
     const uint16_t* r_tile = p.r + row0 * p.ldr;
     uint16_t* d_tile = p.d + row0 * p.ldd;
-    for (uint32_t at = (item % p.parts * kWarps + warp) * kColumns; at < static_cast<uint32_t>(p.n);
-         at += static_cast<uint32_t>(p.parts) * kWarps * kColumns) {  // (twice N is within 32 bits)
+    for (uint32_t at = (item % parts * kWarps + warp) * kColumns; at < static_cast<uint32_t>(p.n);
+         at += static_cast<uint32_t>(parts) * kWarps * kColumns) {  // (twice N is within 32 bits)
         const int col0 = static_cast<int>(at), col = col0 + 8 * q;
         // Element by element: a block that is cut off, and, since rows that start anywhere are read in whole 16-byte
         // words, where those may begin before the matrix or end after it.

@@ -81,6 +81,18 @@ def test_pools_of_many_adapters(m, adapters, r):
     assert torch.equal(d, gb.lora(**q))
 
 
+@pytest.mark.parametrize("m", [32, 33, 63, 96, 127, 128, 129])
+@pytest.mark.parametrize("adapters,r", [(1, 16), (2, 40), (3, 16), (90, 20), (9000, 16)])
+def test_rows_that_each_block_sorts(m, adapters, r):
+    """Tiles of 64 or 32 rows of one adapter, whole and cut off, and rows without one."""
+    q = problem(m, 264, 200, r, adapters, seed=m + adapters)
+    for ids in (pick(m, -2, adapters + 1, 1), pick(m, 0, 1, 2), pick(m, -1, 1, 3), pick(m, -5, 0, 4),
+                torch.arange(m, dtype=torch.int32, device=DEV).flip(0) // 3):
+        q["ids"] = ids
+        d = check(q)
+        assert torch.equal(d, gb.lora(**q))
+
+
 @pytest.mark.parametrize("m,n", [(200, 4099), (300, 33), (65, 1001)])
 @pytest.mark.parametrize("r", [16, 32, 64, 130])
 def test_rows_that_start_anywhere_in_any_order(m, n, r):

@@ -216,8 +216,8 @@ def test_empty_lora_is_a_noop(L):
     assert lora(L, X=None, A=None, B=None, D=None, ids=None, N=0) == GB_OK
     n = ctypes.c_size_t(7)
     assert L.gb_lora_workspace_bytes(0, 8, 8, 8, ctypes.byref(n)) == GB_OK and n.value == 0
-    # two terms of two bytes for each row and rank, in whole steps of 16 or 32; of 32 rows and more their order too
-    for m, r, want in ((3, 5, 3 * 16 * 4), (31, 40, 31 * 64 * 4), (32, 16, 32 * 16 * 4 + 33 * 16 + 32 * 4)):
+    # two terms of two bytes for each row and rank, in whole steps of 16 or 32; of more than 128 rows their order too
+    for m, r, want in ((3, 5, 3 * 16 * 4), (128, 40, 128 * 64 * 4), (129, 16, 129 * 16 * 4 + 130 * 16 + 129 * 4)):
         assert L.gb_lora_workspace_bytes(m, 8, 8, r, ctypes.byref(n)) == GB_OK and n.value == want
     assert L.gb_lora_workspace_bytes(8, 8, 8, 300, ctypes.byref(n)) == GB_ERR_UNSUPPORTED
     assert L.gb_lora_workspace_bytes(8, 8, 8, 8, None) == GB_ERR_INVALID_ARG
