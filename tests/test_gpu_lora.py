@@ -218,6 +218,34 @@ def test_a_long_pool_of_adapters():
     check(q)
 
 
+@pytest.mark.parametrize("m", [5, 40, 200])
+def test_millions_of_adapters(m):
+    """More than are sorted by: tiles of consecutive rows."""
+    count = (1 << 22) + 3
+    q = dict(X=normal(m, 8, seed=1), A=normal(count, 1, 8, seed=2), B=normal(count, 8, 8, seed=3)[:, :, :1], scale=None,
+             R=normal(m, 8, seed=4), ids=pick(m, count - 5, count + 2, 5))
+    assert torch.equal(check(q), gb.lora(**q))
+
+
+@pytest.mark.parametrize("m", [5, 40, 130])
+def test_rows_that_lie_far_apart(m):
+    """A matrix of 2^31 elements and more, whose rows' distances are not counted in 32 bits: X, then R and D."""
+    ld = (2 ** 31 // m // 8 + 1) * 8
+    q = problem(m, 72, 64, 16, 3, seed=m)
+    want = check(q)
+    far = torch.empty(m * ld, dtype=BF16, device=DEV)
+    wide = far.as_strided((m, 72), (ld, 1))
+    assert m * ld > 2 ** 31
+    x = q["X"]
+    q["X"] = wide[:, :64].copy_(x)
+    check(q)
+    q["X"], r = x, q["R"]
+    q["R"] = wide.copy_(r)
+    d = gb.lora(**q, out=wide)
+    assert_within(d, *more_ref.lora(x, q["A"], q["B"], q["ids"], q["scale"], r))
+    assert d.shape == want.shape
+
+
 def test_nothing_to_do():
     q = problem(5, 48, 64, 8, 3, seed=13)
     for change in (dict(A=q["A"][:0], B=q["B"][:0], scale=q["scale"][:0]), dict(X=q["X"][:, :0], A=q["A"][:, :, :0]),
