@@ -82,6 +82,26 @@ gb_status_t allow_smem(Kernel kernel, std::atomic<bool>* ready, int dev, size_t 
     return GB_OK;
 }
 
+// Clusters of a size that run at once (a GPC's SMs hold whole clusters only: of blocks that fit two on each of 152 SMs, 36
+// clusters of eight), asked for once for each kernel, device and size.
+struct ClusterCounts {
+    std::atomic<int> known[64][9] = {};
+
+    template <class Kernel>
+    gb_status_t get(Kernel kernel, int threads, size_t smem, int dev, int cluster, int64_t* count) {
+        int n = known[dev][cluster].load(std::memory_order_relaxed);
+        if (n == 0) {
+            Launch launch(cluster, threads, smem, nullptr, cluster);
+            launch.config.numAttrs = 2;  // (a cluster of one too)
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, kernel, &launch.config);
+            if (e != cudaSuccess) return cuda_fail(e, "cudaOccupancyMaxActiveClusters");
+            known[dev][cluster].store(n, std::memory_order_relaxed);
+        }
+        *count = n;
+        return GB_OK;
+    }
+};
+
 inline bool aligned_to(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 

@@ -45,10 +45,11 @@ int64_t low_columns(int64_t r) { return r <= 16 ? 16 : ceil_div(r, 32) * 32; }
 int64_t low_bytes(int64_t M, int64_t r) { return M * low_columns(r) * 4; }
 int64_t workspace_of(int64_t M, int64_t r) { return low_bytes(M, r) + (M > kHere ? 16 * (M + 1) + 4 * M : 0); }
 
-// The product down to the rank: X's columns are shared out to a cluster, down to a step for each of its warps, so that
-// about as many blocks as run at once (two an SM) have a tile each.  The product up to D: a tile's columns to `parts`
-// blocks, as many as run at once.
-Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int64_t ldx, int64_t ld, int sms, bool shift) {
+// The product down to the rank: X's columns are shared out to a cluster, down to a step for each of its warps, as far as
+// clusters for all tiles run at once (at_once[size] of them).  The product up to D: a tile's columns to `parts` blocks,
+// as many as run at once.
+Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int64_t ldx, int64_t ld, int sms, bool shift,
+               const int64_t (&at_once)[9]) {
     Plan pl;
     const int64_t slots = 2 * sms, places = (shift || r > 16 ? 2 : 3) * sms;
     const int64_t steps = ceil_div(K, kStep), turns = ceil_div(N, kWarps * kColumns), rows = 8 * turn_units(r <= 16 ? 1 : 2);
@@ -58,14 +59,16 @@ Plan make_plan(int64_t M, int64_t N, int64_t K, int64_t r, int64_t adapters, int
     if (pl.sorted) {
         pl.down_tile = pl.up_tile = rows;
         // How many tiles there are is known on the GPU only.  Here: as many adapters as would be met if each row chose
-        // one at random, and two standard deviations, each with a last tile that is half full, or with one.  (A tile
-        // more than clusters would be a second round.)
+        // one at random, and two standard deviations, each with a last tile that is half full, or with one.  (With a
+        // tile more than clusters at once the launch takes two turns: 1000 rows in 37 tiles, with clusters of eight, of
+        // which 36 run at once, 18 us, of seven 16.5.)
         const int64_t full = ceil_div(M, rows), most = full + std::min(adapters, M) + 1;
         const double none = std::exp(-static_cast<double>(M) / adapters);
         const double met = adapters * (1.0 - none) + 2.0 * std::sqrt(adapters * none * (1.0 - none));
         const int64_t likely = std::min(most, static_cast<int64_t>(std::max(met, full + 0.5 * met)) + 1);
-        pl.cluster = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({8, ceil_div(steps, kWarps), slots / likely})));
-        pl.down_blocks = std::min(most, std::max<int64_t>(1, slots / pl.cluster)) * pl.cluster;
+        pl.cluster = static_cast<int>(std::min<int64_t>(8, ceil_div(steps, kWarps)));
+        while (pl.cluster > 1 && at_once[pl.cluster] < likely) --pl.cluster;
+        pl.down_blocks = std::min(most, at_once[pl.cluster]) * pl.cluster;
         pl.parts = 0;  // (as many as the tiles leave room for, known then)
         pl.up_blocks = std::min(most * turns, places);
         return pl;
@@ -158,7 +161,22 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
     const bool wide_r = aligned_to(R, 16) && (M == 1 || ldr % 8 == 0), wide_d = aligned_to(D, 16) && (M == 1 || ldd % 8 == 0);
     const bool shift = !(wide_d && (wide_r || !R));  // rows start anywhere
-    const Plan pl = make_plan(M, N, K, r, any ? adapters : 0, any ? ldx : 0, std::max(ldd, R ? ldr : 0), info.sms, shift);
+    // the ranks of a warp in the product down, and the warps that share the rank
+    const int tiles = r <= 16 ? 1 : 2;
+    int teams = 1;
+    while (teams < kWarps && teams * 16 * tiles < r) teams *= 2;
+    const auto down = tiles == 1 ? down_kernel<1> : down_kernel<2>;
+    int64_t at_once[9] = {};
+    if (any) {
+        static std::atomic<bool> ready[2][64];
+        static ClusterCounts counts[2];
+        const size_t most = down_smem(tiles == 1 ? 1 : kWarps);
+        if ((st = allow_smem(down, ready[tiles - 1], dev, most)) != GB_OK) return st;
+        for (int size = 1; size <= 8; ++size)
+            if ((st = counts[tiles - 1].get(down, kThreads, most, dev, size, &at_once[size])) != GB_OK) return st;
+    }
+    const Plan pl =
+        make_plan(M, N, K, r, any ? adapters : 0, any ? ldx : 0, std::max(ldd, R ? ldr : 0), info.sms, shift, at_once);
     if (pl.down_blocks > kMaxDim || pl.up_blocks > kMaxDim)
         return fail(GB_ERR_UNSUPPORTED, "%" PRId64 " rows of %" PRId64 " columns are more than a launch's blocks", M, N);
     const size_t need = any ? static_cast<size_t>(workspace_of(M, r)) : 0;
@@ -204,15 +222,10 @@ gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int6
         prm.order = order;
     }
     if (any) {
-        const int tiles = r <= 16 ? 1 : 2;
-        prm.teams = 1;
-        while (prm.teams < kWarps && prm.teams * 16 * tiles < r) prm.teams *= 2;
+        prm.teams = teams;
         prm.tile = pl.down_tile;
-        static std::atomic<bool> ready[2][64];
-        const auto kernel = tiles == 1 ? down_kernel<1> : down_kernel<2>;
-        if ((st = allow_smem(kernel, ready[tiles - 1], dev, down_smem(tiles == 1 ? 1 : kWarps))) != GB_OK) return st;
-        st = Launch(static_cast<unsigned>(pl.down_blocks), kThreads, down_smem(prm.teams), s, pl.cluster)(
-            "lora down launch", kernel, prm);
+        st = Launch(static_cast<unsigned>(pl.down_blocks), kThreads, down_smem(teams), s, pl.cluster)("lora down launch", down,
+                                                                                                     prm);
         if (st != GB_OK) return st;
     }
     prm.tile = pl.up_tile;

@@ -102,7 +102,9 @@ gb_status_t gb_moe_ffn_gated(const void* X, int64_t ldx, const void* router, int
     DeviceInfo info;
     if ((st = device_info(&dev, &info)) != GB_OK) return st;
     static std::atomic<bool> ready[64];
-    if ((st = allow_smem(down_kernel, ready, dev, kWarps * kPassTokens * kRows * sizeof(float))) != GB_OK) return st;
+    static ClusterCounts counts;
+    const size_t most = kWarps * kPassTokens * kRows * sizeof(float);
+    if ((st = allow_smem(down_kernel, ready, dev, most)) != GB_OK) return st;
 
     Params prm{};
     prm.x = static_cast<const uint16_t*>(X);
@@ -137,7 +139,10 @@ gb_status_t gb_moe_ffn_gated(const void* X, int64_t ldx, const void* router, int
     while (2 * parts * E <= route * kWarps && parts < ceil_div(D, 256)) parts *= 2;
     const int64_t tiles = ceil_div(D, kRows), slots = 2 * info.sms;
     int share = 1;  // CTAs of a tile of D: as many as run at once
-    while (share < 8 && tiles * share * 2 <= slots) share *= 2;
+    for (int64_t at_once; share < 8; share *= 2) {
+        if ((st = counts.get(down_kernel, kThreads, most, dev, 2 * share, &at_once)) != GB_OK) return st;
+        if (tiles > at_once) break;
+    }
     prm.share = share;
     for (int64_t at = 0; at < T; at += kPassTokens) {
         prm.tokens = static_cast<int>(std::min<int64_t>(T - at, kPassTokens));
