@@ -3,10 +3,10 @@
 //   D[m] = act( R[m] + s[a] B[a] (A[a] X[m]) )      a = ids[m], none where it is outside 0 .. adapters - 1
 //
 // Two launches: down to the rank (S = X A^T, the columns split over CTAs), and up to D.  Rows come in any order, and
-// rows of one adapter share its matrices' fragments: from 32 rows on they are sorted, and a tile has rows of one
-// adapter.  (A tile
-// in which two requests meet takes a turn for each, and the launch waits for it: 1000 rows of 30 requests, with tiles
-// of consecutive rows, 49 us.)  Both products are bound by memory: X, R and D once, and the adapters' matrices.
+// rows of one adapter share its matrices' fragments: from 32 rows on they are sorted (up to 128 by each CTA for itself,
+// more by a launch before the two), and a tile has rows of one adapter.  (A tile in which two requests meet takes a turn
+// for each, and the launch waits for it: 1000 rows of 30 requests, with tiles of consecutive rows, 49 us.)  Both products
+// are bound by memory: X, R and D once, and the adapters' matrices.
 #pragma once
 
 #include <type_traits>
@@ -63,7 +63,7 @@ __device__ __forceinline__ int parts_of(int tiles, int blocks, int n) {
 
 // ---------------------------------------------------------------- all rows by adapter
 
-// One block: 5 us for 1000 rows, 7.5 for 8192, of which the launch and the first loads are the half.
+// One block: 5.5 us for 1000 rows, 7.8 for 8192, of which the launch and the first loads are the half.
 constexpr int kSortThreads = 1024, kSortBatch = 8, kMaxSorted = 8191;  // adapters: a counter each in shared memory
 
 // A count of the rows of each adapter (and of those without one), the starts, and each row to its adapter's next
@@ -596,7 +596,7 @@ struct __align__(16) RowAt {
 // all SMs are full it moves 5 TB/s; the rest is the start of a tile (1.5 us until its rows and S are there) and blocks
 // that are not done together.  Left out for a measurement, the mma, S's loads and B's took 8 % together, R's loads 40 %,
 // D's stores 25 %.  Four units at a time in twice the registers took as long, and so did R and B fetched four turns
-// ahead to a ring in shared memory.  30 tiles of one or two rows with 14336 columns and rank 64: 15.6 us for 55 MB of B.
+// ahead to a ring in shared memory.  30 tiles of one or two rows with 14336 columns and rank 64: 16.5 us for 55 MB of B.
 template <int RS, int STEPS, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, RS == 16 && !SHIFT ? 3 : 2) up_kernel(const __grid_constant__ Params p) {
     constexpr int kBatch = SHIFT && STEPS != 1 ? 1 : 2;  // (units at once: for the registers)
