@@ -274,6 +274,22 @@ def test_results_repeat_also_in_a_graph_on_another_stream():
     assert torch.equal(captured, gb.lora(**q))
 
 
+@pytest.mark.parametrize("m", [20, 48, 300])
+def test_a_graph_of_one_request_serves_many(m):
+    """How many tiles there are changes from replay to replay: from one adapter's to one for each row."""
+    q = problem(m, 264, 520, 40, 300, seed=m)
+    q["ids"].zero_()
+    gb.lora(**q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = gb.lora(**q)
+    for ids in (torch.arange(m), torch.arange(m) // 7 * 3 - 1, torch.full((m,), -1), torch.zeros(m)):
+        q["ids"].copy_(ids)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert_within(captured, *more_ref.lora(q["X"], q["A"], q["B"], q["ids"], q["scale"], q["R"]))
+
+
 def test_the_workspace_is_checked_and_any_contents_do():
     q = problem(20, 96, 512, 16, 4, seed=15)
     need = gb.lora_workspace_bytes(20, 96, 512, 16)
