@@ -23,3 +23,28 @@ def test_experts(d, inner, t, experts, top_k):
     # exp to 2 ulp of its value and 2^-24 of its argument (below 64 here), a tree of sums, a quotient
     assert_within(weights, want_w, want_w * 2.0 ** -17 + 1e-38, "weights")
     assert_within(out, *exact.moe(q, want_ids, weights), "D")  # (with the weights that were given, which are looked at above)
+
+
+def test_experts_far_into_a_long_stack():
+    """Offsets of experts pass 2^31 elements: D is, bit for bit, what a copy of the two chosen experts gives."""
+    experts, inner, d = 72, 3840, 8192
+    x = normal(5, d, seed=1)
+    x[:, 0] = 1.0
+    router = torch.zeros((experts, d), dtype=BF16, device=DEV)
+    router[70, 0], router[71, 0] = 3.0, 4.0  # (logits that are exact, in any order of their sum)
+    w = {}
+    for name, shape in (("W1", (experts, inner, d)), ("W3", (experts, inner, d)), ("W2", (experts, d, inner))):
+        w[name] = torch.randn(shape, dtype=BF16, device=DEV, generator=torch.Generator(device=DEV).manual_seed(len(w))) * shape[2] ** -0.5
+        assert w[name][:70].numel() > 2 ** 31
+    out, ids, weights = gb.moe_ffn_gated(x, router, **w, top_k=2)
+    assert torch.equal(ids, torch.tensor([[71, 70]] * 5, dtype=torch.int32, device=DEV))
+    some = lambda *which: gb.moe_ffn_gated(x, router[70:], **{k: v[list(which)] for k, v in w.items()}, top_k=2)  # noqa: E731
+    alone = some(70, 71)
+    assert torch.equal(weights, alone[2]) and torch.equal(out, alone[0])
+    # what other experts, the same two in the other's place, or none would give is another D
+    for other in (some(71, 70)[0], some(68, 69)[0], some(0, 1)[0], torch.zeros_like(out)):
+        assert ((out - other).float().abs() > 0.02 * out.float().abs()).float().mean() > 0.9
+
+
+def normal(*shape, seed):
+    return torch.randn(shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV).to(BF16)
