@@ -25,6 +25,32 @@ def spans(n):
     return [(at, min(at + STEP, n)) for at in range(0, n, STEP)]
 
 
+# ------------------------------------------------------------------------------------------------ adapters
+
+def lora_problem(m, n, k, r, adapters, seed, device):
+    gen = torch.Generator(device=device).manual_seed(seed)
+    b = signs(gen, adapters, n, r)
+    b *= torch.randint(1, 3, b.shape, generator=gen, device=device)
+    q = dict(X=signs(gen, m, k), A=signs(gen, adapters, r, k), B=b,
+             ids=torch.randint(-1, adapters, (m,), generator=gen, device=device).to(torch.int32),
+             scale=2.0 ** torch.randint(-1, 2, (adapters,), generator=gen, device=device),
+             R=torch.randint(-64, 65, (m, n), generator=gen, device=device).to(BF16))
+    # X A^T has 15 bits at most (two bf16 terms have 16), and the sum over the ranks, in halves, 24
+    assert k < 2 ** 15 and 2 * (2 * k * r * 2 + 64) < 2 ** 24
+    return q
+
+
+def lora(q, without=(0, 0)):
+    """D as it has to be, bit for bit, or with a range of X's columns left out."""
+    x, a, b = q["X"].double(), q["A"].double(), q["B"].double()
+    v = q["R"].double().clone()
+    x[:, without[0]:without[1]] = 0
+    for i in range(a.shape[0]):
+        rows = (q["ids"] == i).nonzero()[:, 0]
+        v[rows] += (x[rows] @ a[i].T * q["scale"][i].double()) @ b[i].T
+    return v.float().to(BF16)  # (exact in fp32: rounded once)
+
+
 # ------------------------------------------------------------------------------------------------ experts
 
 def moe_problem(t, d, inner, experts, seed, device):

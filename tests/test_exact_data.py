@@ -5,7 +5,25 @@ import torch
 from tests import exact_data as exact
 from tests import more_ref
 
+LORA = [(k, r) for k in (4104, 14336, 14337) for r in (16, 64)]
 MOE = [(2056, 1416), (4099, 515), (4096, 48), (48, 4096), (264, 1000), (1000, 264), (31, 33), (40, 17)]
+
+
+@pytest.mark.parametrize("k,r", LORA)
+def test_a_step_of_the_adapters_that_is_left_out_shows_in_every_row(k, r):
+    q = exact.lora_problem(9, 64, k, r, 3, k + r, "cpu")
+    want = exact.lora(q)
+    live = q["ids"] >= 0
+    assert live.any() and torch.equal(want[~live], q["R"][~live])
+    for span in exact.spans(k):
+        assert ((exact.lora(q, span) != want).any(dim=1) == live).all(), span
+
+
+@pytest.mark.parametrize("k,r", LORA)
+def test_the_adapters_exact_result_is_the_definitions(k, r):
+    q = exact.lora_problem(20, 40, k, r, 3, k + r, "cpu")
+    want, tol = more_ref.lora(q["X"], q["A"], q["B"], q["ids"], q["scale"], q["R"])
+    assert torch.equal(want.float().to(torch.bfloat16), exact.lora(q))
 
 
 def outside(got, want, tol):

@@ -48,3 +48,14 @@ def test_experts_far_into_a_long_stack():
 
 def normal(*shape, seed):
     return torch.randn(shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV).to(BF16)
+
+
+@pytest.mark.parametrize("k", [4104, 14336, 14337])
+@pytest.mark.parametrize("r", [16, 40, 64])
+@pytest.mark.parametrize("m,adapters", [(1, 2), (20, 3), (48, 3), (48, 60), (130, 5), (1000, 5)])
+def test_adapters(m, adapters, k, r):
+    for n in (264, 333):
+        q = exact.lora_problem(m, n, k, r, adapters, m + r + k, DEV)
+        assert torch.equal(gb.lora(**q), exact.lora(q))
+    q["ids"].fill_(adapters - 1)  # one request's
+    assert torch.equal(gb.lora(**q), exact.lora(q))
