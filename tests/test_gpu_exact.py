@@ -59,3 +59,32 @@ def test_adapters(m, adapters, k, r):
         assert torch.equal(gb.lora(**q), exact.lora(q))
     q["ids"].fill_(adapters - 1)  # one request's
     assert torch.equal(gb.lora(**q), exact.lora(q))
+
+
+@pytest.mark.parametrize("m", [200, 1000])
+@pytest.mark.parametrize("n", [333, 1000])
+@pytest.mark.parametrize("r", [16, 64])
+@pytest.mark.parametrize("extra,offset", [(0, 0), (8, 0), (3, 1), (0, 5)])
+def test_adapters_in_place_with_rows_in_any_order(m, n, r, extra, offset):
+    """A block's rows lie anywhere in the matrix, beside rows that other blocks write at the time."""
+    q = exact.lora_problem(m, n, 264, r, 7, m + n + r, DEV)
+    want = exact.lora(q)
+    assert torch.equal(gb.lora(**q), want)
+    room = torch.full((offset + m * (n + extra) + 16,), 9.0, dtype=BF16, device=DEV)
+    rows = room[offset:offset + m * (n + extra)].view(m, n + extra)
+    for _ in range(3):
+        rows[:, :n] = q["R"]
+        gb.lora(**dict(q, R=rows[:, :n]), out=rows[:, :n])
+        assert torch.equal(rows[:, :n], want)
+        assert (rows[:, n:] == 9).all() and (room[:offset] == 9).all() and (room[offset + m * (n + extra):] == 9).all()
+
+
+@pytest.mark.parametrize("d,extra,offset", [(264, 0, 0), (136, 3, 1)])
+def test_experts_in_place_over_several_passes(d, extra, offset):
+    q = exact.moe_problem(130, d, 72, 12, d, DEV)
+    want, ids, weights = gb.moe_ffn_gated(**q, top_k=4)
+    assert_within(want, *exact.moe(q, ids.long(), weights), "D")
+    rows = torch.full((130 * (d + extra) + offset,), 9.0, dtype=BF16, device=DEV)[offset:].view(130, d + extra)
+    rows[:, :d] = q["R"]
+    gb.moe_ffn_gated(**dict(q, R=rows[:, :d]), top_k=4, out=rows[:, :d])
+    assert torch.equal(rows[:, :d], want) and (rows[:, d:] == 9).all()
