@@ -399,7 +399,7 @@ GB_API gb_status_t gb_add_layer_norm_backward_workspace_bytes(int64_t M, int64_t
  * Equal logits: the lower expert first.  The logits are summed exactly enough (beyond 32 bits) that the choice
  * does not depend on the order of a sum.  A NaN logit counts as the lowest and makes the token's weights NaN.
  * Products are bf16 with fp32 sums; the inner activation, between the two products, is kept as two bf16 terms
- * (16 bits); the weighted sum is fp32, and D is rounded once.  Results are the same on every run.
+ * (17 bits); the weighted sum is fp32, and D is rounded once.  Results are the same on every run.
  *   X       [T,D] (ldx);  G (router) [E,D] (ldrouter)
  *   W1, W3  E matrices [I,D] (ld1, ld3), `expert1`, `expert3` elements apart
  *   W2      E matrices [D,I] (ld2), `expert2` elements apart
@@ -441,7 +441,7 @@ GB_API gb_status_t gb_moe_ffn_gated_workspace_bytes(int64_t T, int64_t I, int64_
  * X, A, B: bf16, base address 16-byte aligned, leading dimensions and distances of adapters multiples of 8
  * elements; M below 2^31, N and K 2^31 - 4096; r at most 256, a matrix of A less than 2^31 elements, and
  * ldb below 2^26.  Products are bf16 with fp32 sums; A . X, scaled, is multiplied
- * by B as two bf16 terms (16 bits), and the result is rounded once.  An infinity in B gives NaN.  M == 0 or N == 0 is a
+ * by B as two bf16 terms (17 bits), and the result is rounded once.  An infinity in B gives NaN.  M == 0 or N == 0 is a
  * no-op.  Results are the same on every run, and a row's do not depend on the other rows' ids.
  */
 GB_API gb_status_t gb_lora(const void* X, int64_t ldx, const void* A, int64_t lda, int64_t apart_a, const void* B, int64_t ldb,
