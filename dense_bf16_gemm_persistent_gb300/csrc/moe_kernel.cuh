@@ -247,25 +247,44 @@ __device__ __forceinline__ void up_unit(const Params& p, const Lists& l, float* 
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[m][t][i] = 0.f;
 
+    constexpr int kSteps = kChain / 2;  // (of a warp: two mma each)
     const int steps = p.d / kStep;
-    for (int s = warp; s < steps; s += kUnroll * kWarps) {
-        uint4 a[kUnroll][4], b[kUnroll][NT];
+    const bool chains = steps > kWarps * kSteps;
+    float* mine = joined + warp * 2 * NT * 128 + lane;  // [matrix][tokens][i][lane]
+    if (chains) __syncthreads();  // (the unit before has been read)
+    for (int from = warp; from < steps; from += kWarps * kSteps) {
+        const int to = min(steps, from + kWarps * kSteps);
+        for (int s = from; s < to; s += kUnroll * kWarps) {
+            uint4 a[kUnroll][4], b[kUnroll][NT];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {  // (all loads at once; beyond the last step, it again)
-            const int col = min(s + u * kWarps, steps - 1) * kStep + 8 * q;
+            for (int u = 0; u < kUnroll; ++u) {  // (all loads at once; beyond the last step, it again)
+                const int col = min(s + u * kWarps, steps - 1) * kStep + 8 * q;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a[u][i] = load_once(w[i] + col);
+                for (int i = 0; i < 4; ++i) a[u][i] = load_once(w[i] + col);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) b[u][t] = *reinterpret_cast<const uint4*>(x[t] + col);
-        }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (s + u * kWarps >= steps) continue;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                mma_step(c[0][t], a[u][0], a[u][1], b[u][t]);
-                mma_step(c[1][t], a[u][2], a[u][3], b[u][t]);
+                for (int t = 0; t < NT; ++t) b[u][t] = *reinterpret_cast<const uint4*>(x[t] + col);
             }
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (s + u * kWarps >= to) continue;
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    mma_step(c[0][t], a[u][0], a[u][1], b[u][t]);
+                    mma_step(c[1][t], a[u][2], a[u][3], b[u][t]);
+                }
+            }
+        }
+        if (chains) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float& sum = mine[((m * NT + t) * 4 + i) * 32];
+                        sum = from == warp ? c[m][t][i] : sum + c[m][t][i];
+                        c[m][t][i] = 0.f;
+                    }
         }
     }
     if (steps * kStep < p.d && warp == 0) {
@@ -280,13 +299,16 @@ __device__ __forceinline__ void up_unit(const Params& p, const Lists& l, float* 
             mma_step(c[1][t], a[2], a[3], b);
         }
     }
-    __syncthreads();  // (the unit before has been read)
+    if (!chains) __syncthreads();  // (the unit before has been read)
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) joined[(((warp * 2 + m) * NT + t) * 4 + i) * 32 + lane] = c[m][t][i];
+            for (int i = 0; i < 4; ++i) {
+                float& sum = mine[((m * NT + t) * 4 + i) * 32];
+                sum = chains ? sum + c[m][t][i] : c[m][t][i];
+            }
     __syncthreads();
     for (int at = threadIdx.x; at < NT * 128; at += kThreads) {
         float gate = 0.f, up = 0.f;
@@ -342,6 +364,8 @@ __device__ __forceinline__ void down_part(const Params& p, const Lists& l, const
     for (int t = 0; t < NT; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) c[t][i] = 0.f;
+    static_assert(4 * kUnroll <= kChain);  // (what is loaded at once is a chain; ends that are looked for took more registers)
+    float total[NT][4] = {};
     const int whole = min(last, p.inner / kStep);
     for (int s = first; s < whole; s += kUnroll) {
         uint4 a[kUnroll][2], b[kUnroll][NT][2];
@@ -363,6 +387,10 @@ __device__ __forceinline__ void down_part(const Params& p, const Lists& l, const
 #pragma unroll
                 for (int i = 0; i < 2; ++i) mma_step(c[t], a[u][0], a[u][1], b[u][t][i]);
         }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) total[t][i] += c[t][i], c[t][i] = 0.f;
     }
     if (whole < last) {
         const int col = whole * kStep + 8 * q;
@@ -382,7 +410,7 @@ __device__ __forceinline__ void down_part(const Params& p, const Lists& l, const
             const int pair = 8 * t + 2 * q + (i & 1);
             if (pair >= pairs) continue;
             float* to = y + l.token[pair0 + pair] * kRows + g + 8 * (i >> 1);
-            *to = fmaf(pair_weight[pair0 + pair], c[t][i], *to);
+            *to = fmaf(pair_weight[pair0 + pair], total[t][i] + c[t][i], *to);
         }
 }
 
