@@ -332,14 +332,15 @@ __device__ __forceinline__ int64_t make_order(Order& o, const Sorted& s, const P
 
 // ---------------------------------------------------------------- down to the rank
 
-// 16 MT ranks of one adapter with NT units of its rows, over the steps first, first + by, ...
+// 16 MT ranks of one adapter with NT units of its rows, over the steps first, first + by, ...: the lane's sums, at `mine` in
+// shared memory.
 //
 // Loads go straight to the fragments.  Each row's 64 bytes come from one warp, 512 contiguous bytes from the block's
 // eight, and two blocks an SM have 70 to 80 KB on their way: 64 rows of 4096 columns a block and a cluster of two
 // stream at 7.4 TB/s (8192 rows of 67 MB).  A ring of steps in shared memory, filled by cp.async, streamed at 4.8.
 template <int MT, int NT>
-__device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p, const Order& o, int64_t row0, int rank0,
-                                          int unit0, int units, int first, int by) {
+__device__ __forceinline__ void down_sums(float* mine, const Params& p, const Order& o, int64_t row0, int rank0, int unit0,
+                                          int units, int first, int by) {
     constexpr int kOf = 2 * MT + NT, kUnroll = kOf <= 4 ? 4 : kOf < 8 ? 2 : 1;
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     // (ranks beyond the last are the last's, rows the unit's first's, units the last's: their sums are not used;
@@ -353,31 +354,49 @@ __device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p
         const int unit = unit0 + min(t, units - 1), place = o.start[unit] + g;
         x[t] = o.row[place < o.start[unit + 1] ? place : place - g] * static_cast<uint32_t>(p.ldx);
     }
+    float c[MT][NT][4];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[m][t][i] = 0.f;
-    const int whole = p.k / kStep;
-    for (int s = first; s < whole; s += kUnroll * by) {
-        uint4 u[kUnroll][2 * MT], v[kUnroll][NT];
+    constexpr int kSteps = kChain / 2;  // (two mma each)
+    const int whole = p.k / kStep, chain = kSteps * by;
+    const bool chains = whole - first > chain;
+    for (int from = first; from < whole; from += chain) {
+        const int to = min(whole, from + chain);
+        for (int s = from; s < to; s += kUnroll * by) {
+            uint4 u[kUnroll][2 * MT], v[kUnroll][NT];
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {  // (all loads at once; beyond the last step, it again)
-            const int col = min(s + j * by, whole - 1) * kStep;
+            for (int j = 0; j < kUnroll; ++j) {  // (all loads at once; beyond the last step, it again)
+                const int col = min(s + j * by, whole - 1) * kStep;
 #pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) u[j][i] = *reinterpret_cast<const uint4*>(a + a_at[i] + col);
+                for (int i = 0; i < 2 * MT; ++i) u[j][i] = *reinterpret_cast<const uint4*>(a + a_at[i] + col);
 #pragma unroll
-            for (int t = 0; t < NT; ++t)  // (up to 16 ranks X is read by one warp only)
-                v[j][t] = MT == 1 ? load_once(tile + x[t] + col) : *reinterpret_cast<const uint4*>(tile + x[t] + col);
+                for (int t = 0; t < NT; ++t)  // (up to 16 ranks X is read by one warp only)
+                    v[j][t] = MT == 1 ? load_once(tile + x[t] + col) : *reinterpret_cast<const uint4*>(tile + x[t] + col);
+            }
+#pragma unroll
+            for (int j = 0; j < kUnroll; ++j) {
+                if (s + j * by >= to) continue;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_step(c[m][t], u[j][2 * m], u[j][2 * m + 1], v[j][t]);
+            }
         }
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-            if (s + j * by >= whole) continue;
+        if (chains) {
 #pragma unroll
             for (int m = 0; m < MT; ++m)
 #pragma unroll
-                for (int t = 0; t < NT; ++t) mma_step(c[m][t], u[j][2 * m], u[j][2 * m + 1], v[j][t]);
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float& sum = mine[(m * NT + t) * 128 + i * 32];
+                        sum = from == first ? c[m][t][i] : sum + c[m][t][i];
+                        c[m][t][i] = 0.f;
+                    }
         }
     }
     if (whole * kStep < p.k && first == 0) {
@@ -392,6 +411,15 @@ __device__ __forceinline__ void down_sums(float (&c)[MT][NT][4], const Params& p
             for (int m = 0; m < MT; ++m) mma_step(c[m][t], u[2 * m], u[2 * m + 1], v);
         }
     }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float& sum = mine[(m * NT + t) * 128 + i * 32];
+                sum = chains ? sum + c[m][t][i] : c[m][t][i];
+            }
 }
 
 // A turn: `units` units of rows of one adapter (up to NT).  The cluster's CTAs share the columns, and in each CTA a team
@@ -404,14 +432,8 @@ __device__ __forceinline__ void down_turn(const Params& p, const Order& o, float
     constexpr int kOf = MT * NT * 128;  // sums of a warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sharing = kWarps / p.teams, team = warp / sharing, part = warp % sharing;
-    float c[MT][NT][4];
-    down_sums<MT, NT>(c, p, o, row0, team * 16 * MT, unit0, units, rank * sharing + part, p.cluster * sharing);
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) joined[warp * kOf + (m * NT + t) * 128 + i * 32 + lane] = c[m][t][i];
+    down_sums<MT, NT>(joined + warp * kOf + lane, p, o, row0, team * 16 * MT, unit0, units, rank * sharing + part,
+                      p.cluster * sharing);
     __syncthreads();
     for (int at = threadIdx.x; at < p.teams * kOf; at += kThreads) {
         const int its = at / kOf, in = at % kOf;

@@ -51,3 +51,16 @@ def test_experts_of_long_rows(t):
     r = torch.full((t, d), -want, device=DEV).to(BF16)
     out, _, _ = gb.moe_ffn_gated(x, torch.zeros((1, d), dtype=BF16, device=DEV), w, w, w2, 1, R=r)
     assert error(out, want, r) <= 2 * SUM + TERMS + 2.0 ** -20
+
+
+@pytest.mark.parametrize("m,r", [(8192, 256), (8192, 16), (16, 64)])
+def test_adapters_of_long_rows(m, r):
+    """With 256 ranks and a tile for each CTA a warp has all of a row's columns."""
+    k, n = 32768, 40
+    x, a = torch.full((m, k), 127 / 128, device=DEV).to(BF16), torch.full((1, r, k), 129 / 128, device=DEV).to(BF16)
+    b = torch.zeros((1, n, r), dtype=BF16, device=DEV)
+    b[:, torch.arange(n), torch.arange(n) % r] = 1.0
+    want = k * (127 / 128) * (129 / 128)
+    residual = torch.full((m, n), -want, device=DEV).to(BF16)
+    out = gb.lora(x, a, b, torch.zeros(m, dtype=torch.int32, device=DEV), R=residual)
+    assert error(out, want, residual) <= SUM + TERMS
