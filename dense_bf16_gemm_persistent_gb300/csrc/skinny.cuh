@@ -43,10 +43,11 @@ __device__ __forceinline__ void mma_step(float (&c)[4], const uint4& lo, const u
     mma(c, lo.z, hi.z, lo.w, hi.w, x.z, x.w);
 }
 
-// Weights are read once: they need no place in L1, which the tokens have.
+// What is read once needs no place in L1, which the tokens have.  (Not the non-coherent load: these kernels start while the
+// one before still writes, perhaps what they read, and lora writes D where it read R.  It is no faster.)
 __device__ __forceinline__ uint4 load_once(const uint16_t* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;

@@ -15,3 +15,12 @@ def test_no_load_with_cluster_multicast():
         with open(path) as f:
             for asm in re.findall(r'"[^"\n]*\.multicast[^"\n]*"', f.read()):
                 assert "tcgen05.commit" in asm, (path, asm)
+
+
+def test_no_non_coherent_load_in_kernels_that_start_early():
+    """Kernels that are launched while the one before still runs (host.h: Launch) read what that one may be writing, and
+    some write in the place of an input: ld.global.nc and __ldg are for memory that nobody writes as long as a kernel lives."""
+    for name in ("layernorm.cuh", "lora_kernel.cuh", "moe_kernel.cuh", "rowwise.cuh", "skinny.cuh", "w4_kernel.cuh"):
+        with open(os.path.join(CSRC, name)) as f:
+            text = f.read()
+        assert "ld.global.nc" not in text and "__ldg" not in text, name
