@@ -28,6 +28,12 @@ __device__ __forceinline__ float2 row_sum2(float a, float b, int half, float2* b
 // Half of the least power of two (2 or more) that `warps` fit in.
 __device__ __forceinline__ int half_of(int warps) { return warps <= 2 ? 1 : 1 << (31 - __clz(warps - 1)); }
 
+// sum / n, by way of `inverse` = 1 / n, and once more for what that leaves: where n values are equal, that value.
+__device__ __forceinline__ float mean_of(float sum, float n, float inverse) {
+    const float mean = sum * inverse, rest = fmaf(-mean, n, sum);
+    return fabsf(sum) <= 3.4028235e38f ? fmaf(rest, inverse, mean) : mean;  // (an infinite sum leaves nothing)
+}
+
 // Elements of the chunk at `col0` that lie in the row.
 __device__ __forceinline__ int inside(int col0, int cols) { return max(0, min(col0 + 8, cols) - max(col0, 0)); }
 
@@ -99,7 +105,9 @@ struct LayerNormParams {
 // the deviation by): each warp takes its own part's mean first, from registers, and the parts' sums of squares are moved
 // to the row's mean when they are joined,
 //     sum (h - mean)^2 = sum over warps [ S_w + n_w (mean_w - mean)^2 ],
-// so that a row has one barrier, as the root-mean-square norm's has.
+// so that a row has one barrier, as the root-mean-square norm's has. Means are quotients to the last bit or nearly (mean_of),
+// so that a row of one value has that as its mean, and no variance: as a product by 1 / d, of 777 columns and -30000, rstd
+// was 306 and not 316.
 //
 // FULL: rows of whole, aligned 16-byte words (no chunk begins or ends inside one); other rows' chunks are the same but
 // for those that a row begins and ends in.
@@ -213,7 +221,7 @@ __global__ void __maxnreg__(V == 4 ? 128 : 80) layer_norm_kernel(const __grid_co
         }
         stage = stage == kStages - 1 ? 0 : stage + 1;
         sum = warp_sum(sum);
-        float mean = sum * of_warp, squares = 0.f;
+        float mean = mean_of(sum, count, of_warp), squares = 0.f;
 #pragma unroll
         for (int k = 0; k < V; ++k) {
             const int col0 = 8 * (tid + k * threads) - shift;
@@ -237,8 +245,8 @@ __global__ void __maxnreg__(V == 4 ? 128 : 80) layer_norm_kernel(const __grid_co
             const float2 n = on ? counts[place] : make_float2(0.f, 0.f);
             mean = t.x;
             for (int i = half; i > 0; i >>= 1) mean += __shfl_xor_sync(0xffffffffu, mean, i);
-            mean *= of_row;
-            const float off = n.x > 0.f ? fmaf(t.x, n.y, -mean) : 0.f;
+            mean = mean_of(mean, static_cast<float>(p.d), of_row);
+            const float off = fmaf(-n.x, mean, t.x) * n.y;  // of the warp's mean from the row's
             squares = fmaf(n.x * off, off, t.y);
             for (int i = half; i > 0; i >>= 1) squares += __shfl_xor_sync(0xffffffffu, squares, i);
         }
