@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 2) down_kernel(const __grid_constant
         sums[i] = v;
     }
     cluster_sync();
-    for (int i = rank * kThreads + threadIdx.x; i < outputs; i += cluster * kThreads) {
+    // (the rank again, as it is wanted: held since the start it was one register too many)
+    for (int i = cluster_ctarank() * kThreads + threadIdx.x; i < outputs; i += cluster * kThreads) {
         const int token = i / kRows, col = row0 + i % kRows;
         float v = 0.f;
         for (int k = 0; k < cluster; ++k) {
