@@ -191,7 +191,9 @@ def lora(X: torch.Tensor, A: torch.Tensor, B: torch.Tensor, ids: torch.Tensor, s
          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """D = bf16(act(R + scale[id] * (X @ A[id].T) @ B[id].T)), id = ids[row]: low-rank adapters of many requests at once
     (X [M,K], A [adapters,r,K], B [adapters,N,r], ids [M] int32, scale [adapters] fp32 or None, R [M,N] or None).  A
-    row whose id is outside 0 .. adapters - 1 has none: act(R).  Beside a projection: linear(X, W, bias,
+    row whose id is outside 0 .. adapters - 1 has none: act(R).  Rows of X, A and B begin on 16 bytes: a B of a rank that
+    is no multiple of 8 is refused unless its rows are padded (torch.zeros(adapters, N, 8, ...)[:, :, :r]).
+    Beside a projection: linear(X, W, bias,
     R=lora(X, A, B, ids, scale)), or before its activation lora(..., R=linear(X, W, bias), act=...)."""
     if stream is not None:
         return _on(stream, lora, X, A, B, ids, scale, R, act, out, workspace)

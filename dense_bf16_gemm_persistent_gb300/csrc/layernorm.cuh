@@ -112,8 +112,8 @@ struct LayerNormParams {
 // FULL: rows of whole, aligned 16-byte words (no chunk begins or ends inside one); other rows' chunks are the same but
 // for those that a row begins and ends in.
 //
-// 8192 x 4096 with a residual and a bias on a GB300: 47 us, 5.7 TB/s (0.84 of the copy bandwidth); 41 us by ncu, the
-// bytes' own time. What a chunk costs decides: with every chunk's ends looked at it took 610 instructions a warp's part
+// 8192 x 4096 with a residual and a bias on a GB300: 45 us, 5.9 TB/s (0.88 of the copy bandwidth), 43 us by ncu; with
+// dropout 63. Rows that begin anywhere, 3001 x 4099: 32 us (0.46), with dropout 54. What a chunk costs decides: with every chunk's ends looked at it took 610 instructions a warp's part
 // of a row, 62 % of issue slots and 55 us.
 //
 // Dynamic shared memory: the rows [stage][x or r][chunk][thread], the weight, the bias.  (Three stages of 16384 columns
@@ -300,8 +300,8 @@ struct LayerNormBwdParams {
 // registers from the first pass over a row to the second; with chunks that end inside a row xhat does, for two blocks of
 // nine warps an SM.
 //
-// 8192 x 4096 with dH on a GB300, the join with it: 50 us, 5.3 TB/s (0.79 of the copy bandwidth); 3001 x 4099 32 us,
-// 0.45. With g and xhat made again from shared memory, and every chunk's ends looked at, 8192 x 4096 took 700
+// 8192 x 4096 with dH on a GB300, the join with it: 51 us, 5.3 TB/s (0.78 of the copy bandwidth), with dropout 72; 3001 x
+// 4099 32 us (0.45), with dropout 50. With g and xhat made again from shared memory, and every chunk's ends looked at, 8192 x 4096 took 700
 // instructions a warp's part of a row and 69 us, 3001 x 4099 40.
 //
 // Dynamic shared memory: the rows [stage][dY, H or dH][chunk][thread], then the weight.

@@ -336,8 +336,9 @@ __device__ __forceinline__ int64_t make_order(Order& o, const Sorted& s, const P
 // shared memory.
 //
 // Loads go straight to the fragments.  Each row's 64 bytes come from one warp, 512 contiguous bytes from the block's
-// eight, and two blocks an SM have 70 to 80 KB on their way: 64 rows of 4096 columns a block and a cluster of two
-// stream at 7.4 TB/s (8192 rows of 67 MB).  A ring of steps in shared memory, filled by cp.async, streamed at 4.8.
+// eight, and two blocks an SM have 70 to 80 KB on their way: 64 rows of 4096 columns a block and a cluster of two, of 8192
+// rows (67 MB), take 21 us by ncu with caches cold (3.2 TB/s), 19 in a stream of calls.  A ring of steps in shared memory,
+// filled by cp.async, took half as long again on rows that lay in L2.
 template <int MT, int NT>
 __device__ __forceinline__ void down_sums(float* mine, const Params& p, const Order& o, int64_t row0, int rank0, int unit0,
                                           int units, int first, int by) {

@@ -89,8 +89,8 @@ __device__ __forceinline__ double value_of(uint64_t key) {
 
 // A cluster to a token: its warps share the experts and, where there are more warps than experts, `parts` of the
 // columns; the cluster's first CTA chooses.  A logit that is NaN is chosen last, and makes the token's weights NaN.
-// Latency is all it costs: 6 us for a token of 8 experts and 4096 columns, 10 for five of 64 and 2048 (ncu, caches cold);
-// with one warp to an expert, and choices by comparisons in 64-bit floating point, 14 and 16.
+// Latency is all it costs: 8 us for a token of 8 experts and 4096 columns, 13 for five of 64 and 2048 (ncu, caches cold);
+// one warp to an expert, and choices by comparisons in 64-bit floating point, took longer.
 __global__ void __launch_bounds__(kThreads) router_kernel(const __grid_constant__ Params p, int cluster, int parts) {
     allow_next_kernel();
     wait_for_earlier_kernels();

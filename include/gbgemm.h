@@ -397,7 +397,8 @@ GB_API gb_status_t gb_add_layer_norm_backward_workspace_bytes(int64_t M, int64_t
  *   D[t]   = bf16( R[t] + sum_j w[t,j] W2[e_j] . ( silu(W1[e_j] . X[t]) * (W3[e_j] . X[t]) ) )
  *
  * Equal logits: the lower expert first.  The logits are summed exactly enough (beyond 32 bits) that the choice
- * does not depend on the order of a sum.  A NaN logit counts as the lowest and makes the token's weights NaN.
+ * does not depend on the order of a sum (products and sums beyond fp32's range are infinite).  A NaN logit counts
+ * as the lowest and makes the token's weights NaN.
  * Products are bf16 with fp32 sums; the inner activation, between the two products, is kept as two bf16 terms
  * (17 bits); the weighted sum is fp32, and D is rounded once.  Results are the same on every run.
  *   X       [T,D] (ldx);  G (router) [E,D] (ldrouter)
@@ -439,7 +440,8 @@ GB_API gb_status_t gb_moe_ffn_gated_workspace_bytes(int64_t T, int64_t I, int64_
  *   workspace  device memory, 16-byte aligned, of at least gb_lora_workspace_bytes(); need not be cleared;
  *          calls that overlap on the GPU need one each
  * X, A, B: bf16, base address 16-byte aligned, leading dimensions and distances of adapters multiples of 8
- * elements; M below 2^31, N and K 2^31 - 4096; r at most 256, a matrix of A less than 2^31 elements, and
+ * elements (so a B without gaps between its rows has a rank that is one); M below 2^31, N and K 2^31 - 4096; r at
+ * most 256, a matrix of A less than 2^31 elements, and
  * ldb below 2^26.  Products are bf16 with fp32 sums; A . X, scaled, is multiplied
  * by B as two bf16 terms (17 bits), and the result is rounded once.  An infinity in B gives NaN.  M == 0 or N == 0 is a
  * no-op.  Results are the same on every run, and a row's do not depend on the other rows' ids.
